@@ -392,6 +392,125 @@ hm_status hm_silu_mul_fp8(const uint16_t* gu, int64_t rows, int64_t d, uint8_t* 
 hm_status hm_moe_combine(const uint16_t* y, const float* w, int64_t t, int32_t topk, int64_t n,
                          uint16_t* out, hipStream_t stream);
 
+/* ------------------------------------------------ MoE rows in expert order */
+
+/* Workspace bytes hm_moe_dispatch needs (that of hm_moe_sort; may be 0). */
+hm_status hm_moe_dispatch_workspace_size(int64_t t, int32_t topk, int32_t num_experts, size_t* bytes);
+
+/* Tokens sorted by expert: the stable order of hm_moe_sort and the token rows
+ * in that order,
+ *   xs[positions[p]][:] = x[p / topk][:]   for every routed pair p = t'*topk + j.
+ *   x             bf16 [t][n];  topk_ids int32 [t][topk].
+ *   xs            bf16 [t*topk][n]: row i is the row of pair sorted_pairs[i];
+ *                 rows from offsets[E] on (as many as pairs were dropped) are
+ *                 left as they were.
+ *   counts, offsets, sorted_pairs   as hm_moe_sort writes them.
+ *   positions     int32 [t][topk]: the row of xs that holds the pair, -1 for
+ *                 a dropped pair (id outside [0, num_experts)).
+ * hm_moe_gemm runs on the rows of xs with a_rows_are_pairs = 1, t*topk
+ * "tokens", topk = 1, these offsets and the identity 0, 1, 2, ... as
+ * sorted_pairs; its output is then in expert order too.
+ * Any n >= 1; x and xs 16-byte aligned, the integer arrays 4-byte; limits on
+ * t, topk and num_experts as hm_moe_sort.  t = 0 is a no-op.  xs must not
+ * overlap x.  ws: hm_moe_dispatch_workspace_size bytes. */
+hm_status hm_moe_dispatch(const uint16_t* x, const int32_t* topk_ids, int64_t t, int32_t topk,
+                          int32_t num_experts, int64_t n, uint16_t* xs, int32_t* counts, int32_t* offsets,
+                          int32_t* sorted_pairs, int32_t* positions, void* ws, size_t ws_bytes,
+                          hipStream_t stream);
+
+/* The gradient of hm_moe_dispatch to its rows:
+ *   dx[t'][c] = bf16( sum_j dxs[positions[t'][j]][c] ),
+ * summed in fp32 in ascending j; positions outside [0, t*topk) (dropped
+ * pairs) add nothing, a token with none routed gets zeros.
+ *   dxs bf16 [t*topk][n] (rows that no position names are not read);
+ *   positions int32 [t][topk]; dx bf16 [t][n], must not overlap dxs. */
+hm_status hm_moe_dispatch_grad(const uint16_t* dxs, const int32_t* positions, int64_t t, int32_t topk,
+                               int64_t n, uint16_t* dx, hipStream_t stream);
+
+/* Expert-ordered rows back to their tokens with the routing weights applied
+ * (hm_moe_combine for rows in expert order):
+ *   out[t'][c] = bf16( sum_j w[t'][j] * ys[positions[t'][j]][c] ),
+ * summed in fp32 in ascending j, dropped pairs left out.
+ *   ys bf16 [t*topk][n]; w fp32 [t][topk]; out bf16 [t][n], must not overlap
+ *   ys. */
+hm_status hm_moe_collect(const uint16_t* ys, const float* w, const int32_t* positions, int64_t t,
+                         int32_t topk, int64_t n, uint16_t* out, hipStream_t stream);
+
+/* The gradient of hm_moe_collect:
+ *   dys[positions[t'][j]][c] = bf16( w[t'][j] * dout[t'][c] ),
+ *   dw[t'][j] = sum_c dout[t'][c] * ys[positions[t'][j]][c]   (fp32),
+ * dw = 0 for a dropped pair; rows of dys that no position names are left as
+ * they were.  No two positions in [0, t*topk) may be equal (hm_moe_dispatch
+ * gives none), else which pair's row stays is unspecified.
+ *   dout bf16 [t][n]; ys, dys bf16 [t*topk][n]; w, dw fp32 [t][topk].  dys may
+ *   be ys itself (each row is read before it is written); otherwise no
+ *   overlaps.
+ * For all three: any n >= 1, t = 0 is a no-op, bf16 arrays 16-byte aligned,
+ * fp32 and int32 arrays 4-byte; topk >= 1, t*topk < 2^31. */
+hm_status hm_moe_collect_grad(const uint16_t* dout, const uint16_t* ys, const float* w,
+                              const int32_t* positions, int64_t t, int32_t topk, int64_t n, uint16_t* dys,
+                              float* dw, hipStream_t stream);
+
+/* ------------------------------------------------------ low-rank adapters */
+
+/* Low-rank adapters beside one linear layer (n output, k input features, as
+ * its hm_wdesc): adapter e adds B_e A_e x, scaled, to the layer's output.
+ * num_adapters are held side by side, and every row of a batch names its own. */
+typedef struct hm_lora_desc {
+  int32_t abi;          /* HM_ABI_VERSION */
+  int32_t rank;         /* a multiple of 8, 8 .. 128 (smaller adapters are padded with zeros) */
+  int32_t num_adapters; /* 1 .. 512 */
+  int32_t reserved;     /* 0 */
+  int64_t n;            /* output features, >= 1 */
+  int64_t k;            /* input features, a multiple of 128, >= 128 */
+} hm_lora_desc;
+
+/* Workspace bytes hm_lora needs for m rows (may be 0). */
+hm_status hm_lora_workspace_size(const hm_lora_desc* d, int64_t m, size_t* bytes);
+
+/* Adapters of many requests at once beside a shared projection:
+ *   h[m][:] = scales[e] * A_e x[m],  y[m][:] = bf16( base[m][:] + B_e h[m] ),
+ * e = adapter_ids[m]; a row whose id is outside [0, num_adapters) has no
+ * adapter: h = 0 and y = base.  Both products accumulate in fp32 and h enters
+ * the second one with 16 significant bits or more (two bf16 terms).
+ *   x           bf16 [m][k];  adapter_ids int32 [m], in any order.
+ *   a           bf16 [num_adapters][rank][k];  b bf16 [num_adapters][n][rank].
+ *   scales      fp32 [num_adapters].
+ *   base        bf16 [m][n], the shared projection's output (hm_gemm), or NULL
+ *               for zeros.  May be y itself: the adapters are then added in
+ *               place, and rows without an adapter are not touched.
+ *   y           bf16 [m][n]; must not overlap base in any other way.
+ *   h           fp32 [m][rank], what hm_lora_grad needs; NULL if not wanted.
+ *   ws          hm_lora_workspace_size bytes, overwritten.
+ * m = 0 is a no-op; m up to 1048576 (HM_ERR_SHAPE above). */
+hm_status hm_lora(const hm_lora_desc* d, const uint16_t* x, const int32_t* adapter_ids, const uint16_t* a,
+                  const uint16_t* b, const float* scales, int64_t m, const uint16_t* base, uint16_t* y,
+                  float* h, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes hm_lora_grad needs for m rows. */
+hm_status hm_lora_grad_workspace_size(const hm_lora_desc* d, int64_t m, size_t* bytes);
+
+/* The gradient of hm_lora to its rows and to both adapter matrices:
+ *   g[m][:] = scales[e] * B_e^T dy[m],   dx[m][:] = bf16( dx_base[m][:] + A_e^T g[m] ),
+ *   da[e] = bf16( sum over the rows m of e of g[m] x[m]^T ),
+ *   db[e] = bf16( sum over the rows m of e of dy[m] h[m]^T ),
+ * sums in fp32 in an order that the shapes and ids fix (equal calls give
+ * equal bits); g and h enter the products as two bf16 terms.  (The gradient
+ * to base is dy itself.)
+ *   dy          bf16 [m][n];  x bf16 [m][k];  h fp32 [m][rank] from hm_lora.
+ *   dx_base     bf16 [m][k], the gradient through the shared projection, or
+ *               NULL for zeros; may be dx itself.
+ *   dx          bf16 [m][k], or NULL if not wanted.  Rows without an adapter
+ *               get dx_base.
+ *   da          bf16 [num_adapters][rank][k];  db bf16 [num_adapters][n][rank];
+ *               adapters that no row names get zeros.
+ *   ws          hm_lora_grad_workspace_size bytes, overwritten.
+ * m = 0 writes zeros to da and db; m up to 1048576. */
+hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const uint16_t* x, const float* h,
+                       const int32_t* adapter_ids, const uint16_t* a, const uint16_t* b, const float* scales,
+                       int64_t m, const uint16_t* dx_base, uint16_t* dx, uint16_t* da, uint16_t* db, void* ws,
+                       size_t ws_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------------ measurement */
 
 /* Plain-read reference: reads `bytes` bytes of `buf` once with the 16-byte

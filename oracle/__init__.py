@@ -16,7 +16,9 @@ title and section; the pages are the only specification):
 * ``gemm``    -- Y = X_hat . W_hat^T in fp64, its error bound sum_k |x w|, the
   acceptance check, and the element-wise check of the MoE block steps.
 * ``moe``     -- expert sort/offsets, the per-expert (grouped) GEMM, and the
-  MoE block steps around it (SiLU-gated product, top-k weighted combine).
+  MoE block steps around it (SiLU-gated product, top-k weighted combine),
+  and token rows to and from expert order with their gradients.
+* ``lora``    -- low-rank adapters of many requests and their gradient.
 * ``layout``  -- an independent implementation of the library's documented
   device weight layout, used to check the repack byte for byte.
 
@@ -24,4 +26,4 @@ Everything is NumPy, float64 unless the pages or the format fix a precision.
 Numbers are processed in the order the definitions state; a BLAS matmul is the
 only library primitive used for the contraction.
 """
-from . import codecs, quant, gemm, moe, layout  # noqa: F401
+from . import codecs, quant, gemm, moe, lora, layout  # noqa: F401

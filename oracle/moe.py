@@ -98,3 +98,50 @@ def combine_ref(y_hat, weights, topk):
     out = np.einsum("tj,tjn->tn", w, y)
     bnd = np.einsum("tj,tjn->tn", np.abs(w), np.abs(y))
     return out, bnd
+
+
+def positions_ref(ids, num_experts):
+    """Row of every pair in expert order (stable; -1 for ids outside
+    [0, num_experts)), counted one pair at a time: the pairs of lower experts,
+    then the earlier pairs of its own."""
+    flat = np.asarray(ids, dtype=np.int64).ravel()
+    ok = (flat >= 0) & (flat < num_experts)
+    start = np.concatenate([[0], np.cumsum(np.bincount(flat[ok], minlength=num_experts))])
+    nxt = start[:-1].copy()
+    pos = np.full(flat.size, -1, dtype=np.int32)
+    for p in np.nonzero(ok)[0]:
+        pos[p] = nxt[flat[p]]
+        nxt[flat[p]] += 1
+    return pos.reshape(np.shape(ids)), start.astype(np.int32)
+
+
+def collect_ref(ys, weights, positions):
+    """out[t] = sum_j w[t, j] ys[positions[t, j]] over the pairs with a
+    position, and the sum of the absolute terms (weights None: 1)."""
+    pos = np.asarray(positions, dtype=np.int64)
+    y = np.asarray(ys, dtype=np.float64)
+    w = np.ones(pos.shape) if weights is None else np.asarray(weights, dtype=np.float64)
+    out = np.zeros((pos.shape[0], y.shape[1]))
+    bnd = np.zeros_like(out)
+    for t in range(pos.shape[0]):
+        for j in range(pos.shape[1]):
+            if 0 <= pos[t, j] < y.shape[0]:
+                out[t] += w[t, j] * y[pos[t, j]]
+                bnd[t] += np.abs(w[t, j] * y[pos[t, j]])
+    return out, bnd
+
+
+def collect_grad_ref(dout, ys, weights, positions):
+    """dys (NaN where no position names the row), dw and dw's sum of absolute terms."""
+    pos = np.asarray(positions, dtype=np.int64)
+    y, d, w = (np.asarray(v, dtype=np.float64) for v in (ys, dout, weights))
+    dys = np.full(y.shape, np.nan)
+    dw, bnd = np.zeros(pos.shape), np.zeros(pos.shape)
+    for t in range(pos.shape[0]):
+        for j in range(pos.shape[1]):
+            p = pos[t, j]
+            if 0 <= p < y.shape[0]:
+                dys[p] = w[t, j] * d[t]
+                dw[t, j] = d[t] @ y[p]
+                bnd[t, j] = np.abs(d[t]) @ np.abs(y[p])
+    return dys, dw, bnd

@@ -8,6 +8,7 @@ libhm.so has not been built (python quantized_gemm_int4_amd/build.py).
 
 The C functions are declared and documented in include/hm.h.
 """
+import contextlib
 import ctypes
 import os
 
@@ -47,6 +48,11 @@ class hm_tuning(ctypes.Structure):
                 ("moe_tile", ctypes.c_int32)]
 
 
+class hm_lora_desc(ctypes.Structure):
+    _fields_ = [("abi", ctypes.c_int32), ("rank", ctypes.c_int32), ("num_adapters", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("n", ctypes.c_int64), ("k", ctypes.c_int64)]
+
+
 TUNING_FIELDS = tuple(f for f, _ in hm_tuning._fields_ if f != "abi")
 
 
@@ -75,6 +81,11 @@ def wdesc(wfmt, n, k, num_experts=1):
                     int(n), int(k))
 
 
+def lora_desc(n, k, rank, num_adapters):
+    """Low-rank adapters beside an n x k layer (hm_lora_desc)."""
+    return hm_lora_desc(HM_ABI_VERSION, int(rank), int(num_adapters), 0, int(n), int(k))
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -83,6 +94,7 @@ def _load():
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     D = ctypes.POINTER(hm_wdesc)
     T = ctypes.POINTER(hm_tuning)
+    LD = ctypes.POINTER(hm_lora_desc)
     sig = {
         "hm_transform_size": [D, ctypes.POINTER(SZ)],
         "hm_transform": [D, P, P, P, P, SZ, P],
@@ -104,6 +116,15 @@ def _load():
         "hm_silu_mul_fp8": [P, I64, I64, P, P, P],
         "hm_moe_combine": [P, P, I64, I32, I64, P, P],
         "hm_read_probe": [P, I64, I32, I32, P, P],
+        "hm_moe_dispatch_workspace_size": [I64, I32, I32, ctypes.POINTER(SZ)],
+        "hm_moe_dispatch": [P, P, I64, I32, I32, I64, P, P, P, P, P, P, SZ, P],
+        "hm_moe_dispatch_grad": [P, P, I64, I32, I64, P, P],
+        "hm_moe_collect": [P, P, P, I64, I32, I64, P, P],
+        "hm_moe_collect_grad": [P, P, P, P, I64, I32, I64, P, P, P],
+        "hm_lora_workspace_size": [LD, I64, ctypes.POINTER(SZ)],
+        "hm_lora": [LD, P, P, P, P, P, I64, P, P, P, P, SZ, P],
+        "hm_lora_grad_workspace_size": [LD, I64, ctypes.POINTER(SZ)],
+        "hm_lora_grad": [LD, P, P, P, P, P, P, P, I64, P, P, P, P, P, SZ, P],
         "hm_moe_gemm_static": [D, P, I32, P, P, I32, I64, I32, P, P, P, T, P],
     }
     for name, args in sig.items():
@@ -380,6 +401,204 @@ def hm_moe_combine(y, weights, topk, out=None, stream=None):
     _ok("hm_moe_combine", lib.hm_moe_combine(_ptr(y), _ptr(weights), t, int(topk), n, _ptr(out),
                                              _stream(stream)))
     return out
+
+
+# ------------------------------------------------------ MoE rows in expert order
+#
+# The calls below run on the device of their first tensor and on `stream` (the
+# current stream of that device when None); buffers they allocate belong to
+# that stream.  Every tensor must be contiguous, of the named shape, and on that device.
+
+@contextlib.contextmanager
+def _other(dev, stream):
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        yield
+
+
+def _on(t, stream):
+    """Context in which t's device and `stream` are the current ones."""
+    if not t.is_cuda:
+        raise ValueError("need CUDA tensors")
+    if stream is not None and stream.device != t.device:
+        raise ValueError("stream: of another device than the tensors")
+    if stream is None and t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return _other(t.device, stream)
+
+
+def _arg(t, dtype, shape, name, dev):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shape} on {dev}")
+    return t
+
+
+def _out(t, dtype, shape, name, dev):
+    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _arg(t, dtype, shape, name, dev)
+
+
+def _ws(ws, need, dev):
+    """(pointer, bytes) of a workspace: the caller's as it is (the library
+    checks its size), or one allocated here when `need` is not 0.  Also the
+    tensor, which must live until the launch."""
+    if ws is None:
+        if need == 0:
+            return None, 0, None
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: need a contiguous tensor on {dev}")
+    return _ptr(ws), ws.numel() * ws.element_size(), ws
+
+
+def hm_moe_dispatch_workspace_size(t, topk, num_experts):
+    out = ctypes.c_size_t()
+    _ok("hm_moe_dispatch_workspace_size",
+        lib.hm_moe_dispatch_workspace_size(int(t), int(topk), int(num_experts), ctypes.byref(out)))
+    return out.value
+
+
+def hm_moe_dispatch(x, topk_ids, num_experts, xs=None, counts=None, offsets=None, sorted_pairs=None, positions=None,
+                    ws=None, stream=None):
+    """Token rows in expert order: x bf16 [t, n], topk_ids int32 [t, topk] ->
+    (xs bf16 [t*topk, n], counts [E], offsets [E+1], sorted_pairs [t*topk],
+    positions [t, topk]).  Rows of xs and entries of sorted_pairs from
+    offsets[E] on (as many as ids lie outside [0, E)) are left as they were:
+    uninitialised when allocated here."""
+    with _on(x, stream):
+        (t, n), topk, dev, i32 = x.shape, topk_ids.shape[1], x.device, torch.int32
+        _arg(x, torch.bfloat16, (t, n), "x", dev)
+        _arg(topk_ids, i32, (t, topk), "topk_ids", dev)
+        E = int(num_experts)
+        need = hm_moe_dispatch_workspace_size(t, topk, E)
+        xs = _out(xs, torch.bfloat16, (t * topk, n), "xs", dev)
+        counts = _out(counts, i32, (E,), "counts", dev)
+        offsets = _out(offsets, i32, (E + 1,), "offsets", dev)
+        sorted_pairs = _out(sorted_pairs, i32, (t * topk,), "sorted_pairs", dev)
+        positions = _out(positions, i32, (t, topk), "positions", dev)
+        wsp, wsb, ws = _ws(ws, need, dev)
+        _ok("hm_moe_dispatch", lib.hm_moe_dispatch(_ptr(x), _ptr(topk_ids), t, topk, E, n, _ptr(xs), _ptr(counts),
+                                                   _ptr(offsets), _ptr(sorted_pairs), _ptr(positions), wsp, wsb,
+                                                   _stream(stream)))
+    return xs, counts, offsets, sorted_pairs, positions
+
+
+def hm_moe_dispatch_grad(dxs, positions, dx=None, stream=None):
+    """dxs bf16 [t*topk, n], positions int32 [t, topk] -> dx bf16 [t, n]: each
+    token's sum over its routed rows."""
+    with _on(dxs, stream):
+        (t, topk), n, dev = positions.shape, dxs.shape[1], dxs.device
+        _arg(dxs, torch.bfloat16, (t * topk, n), "dxs", dev)
+        _arg(positions, torch.int32, (t, topk), "positions", dev)
+        dx = _out(dx, torch.bfloat16, (t, n), "dx", dev)
+        _ok("hm_moe_dispatch_grad", lib.hm_moe_dispatch_grad(_ptr(dxs), _ptr(positions), t, topk, n, _ptr(dx),
+                                                             _stream(stream)))
+    return dx
+
+
+def hm_moe_collect(ys, weights, positions, out=None, stream=None):
+    """ys bf16 [t*topk, n] in expert order, weights fp32 [t, topk], positions
+    int32 [t, topk] -> out bf16 [t, n]: each token's weighted sum."""
+    with _on(ys, stream):
+        (t, topk), n, dev = positions.shape, ys.shape[1], ys.device
+        _arg(ys, torch.bfloat16, (t * topk, n), "ys", dev)
+        _arg(weights, torch.float32, (t, topk), "weights", dev)
+        _arg(positions, torch.int32, (t, topk), "positions", dev)
+        out = _out(out, torch.bfloat16, (t, n), "out", dev)
+        _ok("hm_moe_collect", lib.hm_moe_collect(_ptr(ys), _ptr(weights), _ptr(positions), t, topk, n, _ptr(out),
+                                                 _stream(stream)))
+    return out
+
+
+def hm_moe_collect_grad(dout, ys, weights, positions, dys=None, dweights=None, stream=None):
+    """Gradient of hm_moe_collect: dout bf16 [t, n] -> (dys bf16 [t*topk, n],
+    dweights fp32 [t, topk]).  Rows of dys that no position names are left as
+    they were (zeros when allocated here).  dys may be ys."""
+    with _on(dout, stream):
+        (t, topk), n, dev = positions.shape, dout.shape[1], dout.device
+        _arg(dout, torch.bfloat16, (t, n), "dout", dev)
+        _arg(ys, torch.bfloat16, (t * topk, n), "ys", dev)
+        _arg(weights, torch.float32, (t, topk), "weights", dev)
+        _arg(positions, torch.int32, (t, topk), "positions", dev)
+        if dys is None:
+            dys = torch.zeros(t * topk, n, dtype=torch.bfloat16, device=dev)
+        _arg(dys, torch.bfloat16, (t * topk, n), "dys", dev)
+        dweights = _out(dweights, torch.float32, (t, topk), "dweights", dev)
+        _ok("hm_moe_collect_grad", lib.hm_moe_collect_grad(_ptr(dout), _ptr(ys), _ptr(weights), _ptr(positions), t,
+                                                           topk, n, _ptr(dys), _ptr(dweights), _stream(stream)))
+    return dys, dweights
+
+
+# ------------------------------------------------------------ low-rank adapters
+
+def _lora_ws_size(fn, desc, m):
+    out = ctypes.c_size_t()
+    _ok(fn, getattr(lib, fn)(ctypes.byref(desc), int(m), ctypes.byref(out)))
+    return out.value
+
+
+def hm_lora_workspace_size(desc, m):
+    return _lora_ws_size("hm_lora_workspace_size", desc, m)
+
+
+def hm_lora_grad_workspace_size(desc, m):
+    return _lora_ws_size("hm_lora_grad_workspace_size", desc, m)
+
+
+def _lora_common(desc, x, adapter_ids, a, b, scales):
+    m, dev, bf = x.shape[0], x.device, torch.bfloat16
+    _arg(x, bf, (m, desc.k), "x", dev)
+    _arg(adapter_ids, torch.int32, (m,), "adapter_ids", dev)
+    _arg(a, bf, (desc.num_adapters, desc.rank, desc.k), "a", dev)
+    _arg(b, bf, (desc.num_adapters, desc.n, desc.rank), "b", dev)
+    _arg(scales, torch.float32, (desc.num_adapters,), "scales", dev)
+    return m, dev
+
+
+def hm_lora(desc, x, adapter_ids, a, b, scales, base=None, y=None, h=None, ws=None, stream=None):
+    """Adapters beside a shared projection: x bf16 [m, k], adapter_ids int32
+    [m], a bf16 [L, rank, k], b bf16 [L, n, rank], scales fp32 [L] -> y bf16
+    [m, n] = base + scale * B (A x) per row; base bf16 [m, n] (hm_gemm's
+    output) or None for zeros, and may be y (in place).  h: an fp32 [m, rank]
+    tensor to keep scale * A x in for hm_lora_grad."""
+    with _on(x, stream):
+        m, dev = _lora_common(desc, x, adapter_ids, a, b, scales)
+        if base is not None:
+            _arg(base, torch.bfloat16, (m, desc.n), "base", dev)
+        if h is not None:
+            _arg(h, torch.float32, (m, desc.rank), "h", dev)
+        need = hm_lora_workspace_size(desc, m)
+        y = _out(y, torch.bfloat16, (m, desc.n), "y", dev)
+        wsp, wsb, ws = _ws(ws, need, dev)
+        _ok("hm_lora", lib.hm_lora(ctypes.byref(desc), _ptr(x), _ptr(adapter_ids), _ptr(a), _ptr(b), _ptr(scales), m,
+                                   _ptr(base), _ptr(y), _ptr(h), wsp, wsb, _stream(stream)))
+    return y
+
+
+def hm_lora_grad(desc, dy, x, h, adapter_ids, a, b, scales, dx_base=None, dx=None, da=None, db=None, need_dx=True,
+                 ws=None, stream=None):
+    """Gradient of hm_lora: dy bf16 [m, n], x bf16 [m, k], h fp32 [m, rank] ->
+    (dx bf16 [m, k] or None, da bf16 [L, rank, k], db bf16 [L, n, rank]).
+    dx_base bf16 [m, k]: the gradient through the shared projection, added to
+    dx (may be dx); need_dx=False leaves dx out."""
+    with _on(x, stream):
+        m, dev = _lora_common(desc, x, adapter_ids, a, b, scales)
+        bf = torch.bfloat16
+        _arg(dy, bf, (m, desc.n), "dy", dev)
+        _arg(h, torch.float32, (m, desc.rank), "h", dev)
+        if dx_base is not None:
+            _arg(dx_base, bf, (m, desc.k), "dx_base", dev)
+        if not need_dx:
+            if dx is not None or dx_base is not None:
+                raise ValueError("need_dx=False takes neither dx nor dx_base")
+        else:
+            dx = _out(dx, bf, (m, desc.k), "dx", dev)
+        need = hm_lora_grad_workspace_size(desc, m)
+        da = _out(da, bf, (desc.num_adapters, desc.rank, desc.k), "da", dev)
+        db = _out(db, bf, (desc.num_adapters, desc.n, desc.rank), "db", dev)
+        wsp, wsb, ws = _ws(ws, need, dev)
+        _ok("hm_lora_grad", lib.hm_lora_grad(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(h), _ptr(adapter_ids), _ptr(a),
+                                             _ptr(b), _ptr(scales), m, _ptr(dx_base), _ptr(dx), _ptr(da), _ptr(db),
+                                             wsp, wsb, _stream(stream)))
+    return dx, da, db
 
 
 # ----------------------------------------------------------------- measurement

@@ -36,9 +36,11 @@ __device__ int block_scan512(int v, int* wsum) {
 // counts of earlier waves, and inside a wave each batch of 64 pairs is ranked
 // in lane order with ballot matching.  hist is the block's [16][512] LDS
 // array (zeroed here); base[e] (LDS) is the first position of this range's
-// pairs of expert e.  Must be reached by every thread of the block.
+// pairs of expert e.  POS: also the inverse, positions[p] (-1 for a dropped
+// pair).  Must be reached by every thread of the block.
+template <bool POS>
 __device__ void sort_range(const int32_t* __restrict__ ids, int64_t lo, int64_t hi, int E, const int* base,
-                           int (*hist)[512], int32_t* __restrict__ sorted_pairs) {
+                           int (*hist)[512], int32_t* __restrict__ sorted_pairs, int32_t* __restrict__ positions) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int i = tid; i < kSortWaves * 512; i += kSortThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
@@ -79,6 +81,9 @@ __device__ void sort_range(const int32_t* __restrict__ ids, int64_t lo, int64_t 
       const int rank = __popcll(m & lt);
       const int pos = hist[wave][e] + rank;
       sorted_pairs[pos] = (int32_t)p;
+      if (POS) positions[p] = pos;
+    } else if (POS && p < end) {
+      positions[p] = -1;
     }
     __builtin_amdgcn_wave_barrier();
     if (valid && __popcll(m & lt) == 0) hist[wave][e] += __popcll(m);
@@ -107,9 +112,10 @@ __device__ void expert_offsets(const int* tot, int* base, int E, int* wsum, bool
 
 // Deterministic, stable counting sort of pair ids by expert in one block
 // (few pairs).
+template <bool POS>
 __global__ void __launch_bounds__(kSortThreads)
 k_moe_sort(const int32_t* __restrict__ ids, int64_t P, int E, int32_t* __restrict__ counts,
-           int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pairs) {
+           int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pairs, int32_t* __restrict__ positions) {
   __shared__ int hist[kSortWaves][512];
   __shared__ int tot[512], base[512];
   __shared__ int wsum[8];
@@ -122,7 +128,7 @@ k_moe_sort(const int32_t* __restrict__ ids, int64_t P, int E, int32_t* __restric
   }
   __syncthreads();
   expert_offsets(tot, base, E, wsum, true, counts, offsets);
-  sort_range(ids, 0, P, E, base, hist, sorted_pairs);
+  sort_range<POS>(ids, 0, P, E, base, hist, sorted_pairs, positions);
 }
 
 // GPU-wide sort, pass 1: block b counts the pairs of its chunk
@@ -147,10 +153,11 @@ k_moe_sort_count(const int32_t* __restrict__ ids, int64_t P, int E, int64_t C, i
 // of the chunks before its own, scans the totals into the expert offsets
 // (block 0 writes counts and offsets), and places its chunk's pairs after
 // those of the earlier chunks: the order is stable over the whole input.
+template <bool POS>
 __global__ void __launch_bounds__(kSortThreads)
 k_moe_sort_place(const int32_t* __restrict__ ids, int64_t P, int E, int64_t C, int nb,
                  const int32_t* __restrict__ cnt, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
-                 int32_t* __restrict__ sorted_pairs) {
+                 int32_t* __restrict__ sorted_pairs, int32_t* __restrict__ positions) {
   __shared__ int hist[kSortWaves][512];
   __shared__ int tot[512], base[512];
   __shared__ int wsum[8];
@@ -171,7 +178,7 @@ k_moe_sort_place(const int32_t* __restrict__ ids, int64_t P, int E, int64_t C, i
   expert_offsets(tot, base, E, wsum, b == 0, counts, offsets);
   const int64_t lo = (int64_t)b * C;
   const int64_t hi = (lo + C < P) ? lo + C : P;
-  sort_range(ids, lo, hi, E, base, hist, sorted_pairs);
+  sort_range<POS>(ids, lo, hi, E, base, hist, sorted_pairs, positions);
 }
 
 // Work units of a grouped GEMM from the expert offsets (one thread per
@@ -241,21 +248,32 @@ k_moe_schedule(const int32_t* __restrict__ offsets, int E, int64_t P, int s_rows
 }
 
 
-hipError_t launch_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* counts, int32_t* offsets,
-                           int32_t* sorted_pairs, int32_t* cnt, hipStream_t st) {
+template <bool POS>
+static hipError_t run_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* counts, int32_t* offsets,
+                               int32_t* sorted_pairs, int32_t* positions, int32_t* cnt, hipStream_t st) {
   int64_t C = 0;
   const int nb = moe_sort_blocks(P, &C);
   if (nb == 1) {
-    hipLaunchKernelGGL(k_moe_sort, dim3(1), dim3(kSortThreads), 0, st, ids, P, E, counts, offsets,
-                       sorted_pairs);
+    hipLaunchKernelGGL(k_moe_sort<POS>, dim3(1), dim3(kSortThreads), 0, st, ids, P, E, counts, offsets,
+                       sorted_pairs, positions);
     return hipGetLastError();
   }
   hipLaunchKernelGGL(k_moe_sort_count, dim3(nb), dim3(kSortThreads), 0, st, ids, P, E, C, cnt);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_moe_sort_place, dim3(nb), dim3(kSortThreads), 0, st, ids, P, E, C, nb, cnt, counts,
-                     offsets, sorted_pairs);
+  hipLaunchKernelGGL(k_moe_sort_place<POS>, dim3(nb), dim3(kSortThreads), 0, st, ids, P, E, C, nb, cnt, counts,
+                     offsets, sorted_pairs, positions);
   return hipGetLastError();
+}
+
+hipError_t launch_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* counts, int32_t* offsets,
+                           int32_t* sorted_pairs, int32_t* cnt, hipStream_t st) {
+  return run_moe_sort<false>(ids, P, E, counts, offsets, sorted_pairs, nullptr, cnt, st);
+}
+
+hipError_t launch_moe_sort_pos(const int32_t* ids, int64_t P, int E, int32_t* counts, int32_t* offsets,
+                               int32_t* sorted_pairs, int32_t* positions, int32_t* cnt, hipStream_t st) {
+  return run_moe_sort<true>(ids, P, E, counts, offsets, sorted_pairs, positions, cnt, st);
 }
 
 hipError_t launch_moe_schedule(const int32_t* offsets, int E, int64_t P, int s_rows, int s_max, int bm,

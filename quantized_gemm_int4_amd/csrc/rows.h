@@ -1,0 +1,46 @@
+// Launchers of the operators on rows in expert order (k_rows.hip) and of the
+// low-rank adapters (k_lora.hip, k_lora_grad.hip), and what their planners
+// share with them.
+#pragma once
+#include "common.h"
+#include "launch.h"
+
+namespace hm {
+
+// bf16 rows of any length: eight values at any 2-byte address (one 16-byte
+// access; unaligned ones are legal for global memory on gfx950).
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+__device__ __forceinline__ u32x4_t ld8(const uint16_t* p) {
+  return *reinterpret_cast<const u32x4_any_t*>(p);
+}
+__device__ __forceinline__ void st8(uint16_t* p, u32x4_t v) { *reinterpret_cast<u32x4_any_t*>(p) = v; }
+
+// Values c .. c + 7 of a row of n (zeros from n on); c < n.
+__device__ __forceinline__ u32x4_t ld8_tail(const uint16_t* row, int64_t c, int64_t n) {
+  if (c + 8 <= n) return ld8(row + c);
+  u32x4_t v = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c + e < n) v[e >> 1] |= (uint32_t)row[c + e] << (16 * (e & 1));
+  return v;
+}
+__device__ __forceinline__ void st8_tail(uint16_t* row, int64_t c, int64_t n, u32x4_t v) {
+  if (c + 8 <= n) {
+    st8(row + c, v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c + e < n) row[c + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+}
+
+// xs[positions[p]] = x[p / topk] for positions in [0, t topk)
+hipError_t launch_dispatch_rows(const uint16_t* x, const int32_t* positions, int64_t t, int topk, int64_t n,
+                                uint16_t* xs, hipStream_t st);
+// out[t] = sum_j w[t][j] ys[positions[t][j]] (w null: 1)
+hipError_t launch_collect(const uint16_t* ys, const float* w, const int32_t* positions, int64_t t, int topk,
+                          int64_t n, uint16_t* out, hipStream_t st);
+hipError_t launch_collect_grad(const uint16_t* dout, const uint16_t* ys, const float* w, const int32_t* positions,
+                               int64_t t, int topk, int64_t n, uint16_t* dys, float* dw, hipStream_t st);
+
+}  // namespace hm
