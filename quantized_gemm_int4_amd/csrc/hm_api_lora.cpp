@@ -27,54 +27,85 @@ hm_status check_lora(const hm_lora_desc* d, int64_t m) {
   return HM_OK;
 }
 
-// Blocks along a contraction of `len` for `units` units: enough to fill the
-// chip, each wave keeping 64 values of the axis or more.
-int contraction_splits(int64_t units, int64_t len) {
-  const int64_t want = (1024 + units - 1) / units, most = std::max<int64_t>(1, len / 256);
-  return (int)std::max<int64_t>(1, std::min(std::min(want, most), (int64_t)16));
-}
+// Blocks of one launch stay under 2^24 (2^32 threads).
+constexpr int64_t kMaxBlocks = (1ll << 24) - 1;
 
-LoraWs lora_ws(const hm_lora_desc* d, int64_t m) {
-  LoraWs w{};
-  const int64_t L = d->num_adapters;
-  w.max_units = m / kLoraUnit + std::min<int64_t>(L, m);
-  w.splits = contraction_splits(std::max<int64_t>(w.max_units, 1), d->k);
-  w.splits_n = contraction_splits(std::max<int64_t>(w.max_units, 1), d->n);
+// Byte offsets in the workspace (total a multiple of 256) and launch shape.
+struct LoraPlan {
+  size_t units, rows, first, part, gt, ht, sums, total;
+  int64_t max_units;
+  int unit_rows, splits, group, chunks;
+  bool direct;
+};
+
+// Rows per unit: 64 where the adapters have that many rows each on average
+// (every loaded value of A and B then serves four MFMAs), fewer where units
+// would be mostly empty.
+int rows_per_unit(int64_t m, int64_t L) { return m <= 16 * L ? 16 : (m <= 32 * L ? 32 : 64); }
+
+hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) {
+  LoraPlan w{};
+  const int64_t L = d->num_adapters, len = grad ? d->n : d->k, cols = grad ? d->k : d->n;
+  w.direct = !grad && m <= kLoraDirect;
+  w.unit_rows = grad ? kLoraUnit : (w.direct ? 16 : rows_per_unit(m, L));
+  w.max_units = w.direct ? m : m / w.unit_rows + std::min<int64_t>(L, m);
+  // blocks along the contraction: about 1024 blocks of four waves (16-row
+  // units) or 512 of eight in all, each wave keeping two steps of 32 or more
+  const int64_t blocks = w.unit_rows == 16 ? w.max_units : w.max_units * (w.unit_rows / 32);
+  const int64_t want = w.unit_rows == 16 ? 1024 / blocks : 512 / blocks;
+  const int64_t most = std::min<int64_t>(w.unit_rows == 16 ? kLoraMaxSplits : 4, len / (w.unit_rows == 16 ? 128 : 512));
+  w.splits = (int)std::max<int64_t>(1, std::min(want, most));
+  const int64_t slabs = 8 * ((cols + 8 * kLoraCols - 1) / (8 * kLoraCols));
+  w.group = w.direct || w.unit_rows < 64 ? 1 : (w.max_units * slabs >= 4096 ? 4 : (w.max_units * slabs >= 2048 ? 2 : 1));
+  if (slabs * ((w.max_units + w.group - 1) / w.group + (m + 63) / 64) > kMaxBlocks) return HM_ERR_SHAPE;
   size_t at = 0;
   auto take = [&at](size_t bytes) {
     const size_t o = at;
     at = align256(at + bytes);
     return o;
   };
-  w.hdr = take(256);
-  w.units = take((size_t)w.max_units * 16);
-  w.counts = take((size_t)L * 4);
-  w.offsets = take((size_t)(L + 1) * 4);
-  w.rows = take((size_t)m * 4);
-  const int nb = moe_sort_blocks(m, nullptr);
-  w.cnt = take(nb > 1 ? (size_t)nb * (size_t)L * 4 : 0);
-  w.part = take((size_t)std::max(w.splits, w.splits_n) * (size_t)m * (size_t)d->rank * 4);
+  if (!w.direct) {
+    w.units = take((size_t)w.max_units * 8);
+    w.rows = take((size_t)w.max_units * (size_t)w.unit_rows * 4);
+    w.first = take((size_t)(L + 1) * 4);
+  }
+  w.part = take((size_t)w.splits * (size_t)m * (size_t)d->rank * 4);
+  if (grad) {
+    const size_t packed = (size_t)w.max_units * 2 * (size_t)lora_rp(d->rank) * kLoraUnit * 2;
+    w.gt = take(packed);
+    w.ht = take(packed);
+    const int64_t tiles = ((d->n + 127) / 128 + d->k / 128) * (d->rank > 64 ? 2 : 1);
+    w.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(16, std::min((512 + tiles - 1) / tiles, w.max_units / 4)));
+    w.sums = take(w.chunks > 1 ? (size_t)(2 * w.chunks) * (size_t)d->rank * (size_t)(d->k + d->n) * 4 : 0);
+  }
   w.total = at;
-  return w;
+  *out = w;
+  return HM_OK;
 }
 
-hipError_t group_rows(const hm_lora_desc* d, const int32_t* ids, int64_t m, const LoraWs& w, uint8_t* ws,
-                      LoraArgs* g, hipStream_t st) {
-  int32_t* hdr = (int32_t*)(ws + w.hdr);
+hm_status workspace_size(const hm_lora_desc* d, int64_t m, bool grad, size_t* bytes) {
+  if (hm_status s = check_lora(d, m)) return s;
+  if (!bytes) return HM_ERR_NULL;
+  LoraPlan w{};
+  if (m)
+    if (hm_status s = plan_lora(d, m, grad, &w)) return s;
+  *bytes = w.total;
+  return HM_OK;
+}
+
+hipError_t group_rows(const hm_lora_desc* d, const int32_t* ids, int64_t m, const LoraPlan& w, uint8_t* ws,
+                      LoraRows* R, hipStream_t st) {
   int32_t* units = (int32_t*)(ws + w.units);
-  int32_t* offsets = (int32_t*)(ws + w.offsets);
   int32_t* rows = (int32_t*)(ws + w.rows);
-  hipError_t e = launch_moe_sort(ids, m, d->num_adapters, (int32_t*)(ws + w.counts), offsets, rows,
-                                 (int32_t*)(ws + w.cnt), st);
-  if (e == hipSuccess) e = launch_lora_units(offsets, d->num_adapters, hdr, units, st);
-  g->R = LoraRows{hdr, units, offsets, rows, w.max_units};
-  return e;
+  int32_t* first = (int32_t*)(ws + w.first);
+  *R = LoraRows{units, rows, first, w.max_units, w.unit_rows};
+  return launch_lora_plan(ids, m, d->num_adapters, w.unit_rows, w.max_units, units, rows, first, st);
 }
 
-LoraArgs args_of(const hm_lora_desc* d, const uint16_t* x, const int32_t* ids, const uint16_t* a, const uint16_t* b,
-                 const float* scales, int64_t m) {
+LoraArgs args_of(const hm_lora_desc* d, const uint16_t* z, const int32_t* ids, const uint16_t* a, const uint16_t* b,
+                 const float* scales, int64_t m, const uint16_t* base, uint16_t* y, const LoraPlan& w, uint8_t* ws) {
   LoraArgs g{};
-  g.x = x;
+  g.z = z;
   g.a = a;
   g.b = b;
   g.scales = scales;
@@ -84,16 +115,18 @@ LoraArgs args_of(const hm_lora_desc* d, const uint16_t* x, const int32_t* ids, c
   g.K = d->k;
   g.rank = d->rank;
   g.L = d->num_adapters;
+  g.base = base;
+  g.y = y;
+  g.part = (float*)(ws + w.part);
+  g.splits = w.splits;
+  g.group = w.group;
   return g;
 }
 
 }  // namespace
 
 HM_API hm_status hm_lora_workspace_size(const hm_lora_desc* d, int64_t m, size_t* bytes) {
-  if (hm_status s = check_lora(d, m)) return s;
-  if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? lora_ws(d, m).total : 0;
-  return HM_OK;
+  return workspace_size(d, m, false, bytes);
 }
 
 HM_API hm_status hm_lora(const hm_lora_desc* d, const uint16_t* x, const int32_t* adapter_ids, const uint16_t* a,
@@ -105,27 +138,22 @@ HM_API hm_status hm_lora(const hm_lora_desc* d, const uint16_t* x, const int32_t
   if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) || !aligned(base, 16) ||
       !aligned(h, 16) || !aligned(adapter_ids, 4) || !aligned(scales, 4))
     return HM_ERR_ALIGN;
-  const LoraWs w = lora_ws(d, m);
+  LoraPlan w;
+  if (hm_status s = plan_lora(d, m, false, &w)) return s;
   if (!ws) return HM_ERR_NULL;
   if (ws_bytes < w.total) return HM_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return HM_ERR_ALIGN;
-  LoraArgs g = args_of(d, x, adapter_ids, a, b, scales, m);
-  g.base = base;
-  g.y = y;
+  LoraArgs g = args_of(d, x, adapter_ids, a, b, scales, m, base, y, w, (uint8_t*)ws);
   g.h = h;
-  g.splits = w.splits;
-  g.part = (h && w.splits == 1) ? h : (float*)((uint8_t*)ws + w.part);
-  hipError_t e = group_rows(d, adapter_ids, m, w, (uint8_t*)ws, &g, stream);
-  if (e == hipSuccess) e = launch_lora_shrink(g, stream);
-  if (e == hipSuccess) e = launch_lora_expand(g, stream);
+  if (h && w.splits == 1) g.part = h;
+  hipError_t e = w.direct ? hipSuccess : group_rows(d, adapter_ids, m, w, (uint8_t*)ws, &g.R, stream);
+  if (e == hipSuccess) e = launch_lora_shrink(g, w.direct, false, stream);
+  if (e == hipSuccess) e = launch_lora_expand(g, w.direct, false, stream);
   return e == hipSuccess ? HM_OK : HM_ERR_HIP;
 }
 
 HM_API hm_status hm_lora_grad_workspace_size(const hm_lora_desc* d, int64_t m, size_t* bytes) {
-  if (hm_status s = check_lora(d, m)) return s;
-  if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? lora_ws(d, m).total : 0;
-  return HM_OK;
+  return workspace_size(d, m, true, bytes);
 }
 
 HM_API hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const uint16_t* x, const float* h,
@@ -135,27 +163,41 @@ HM_API hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const u
   if (hm_status s = check_lora(d, m)) return s;
   if (!da || !db) return HM_ERR_NULL;
   if (!aligned(da, 16) || !aligned(db, 16)) return HM_ERR_ALIGN;
-  LoraArgs g = args_of(d, x, adapter_ids, a, b, scales, m);
-  g.dy = dy;
-  g.h = const_cast<float*>(h);
-  g.da = da;
-  g.db = db;
-  if (m == 0) return launch_lora_outer(g, stream) == hipSuccess ? HM_OK : HM_ERR_HIP;
+  LoraGradArgs o{};
+  o.x = x;
+  o.dy = dy;
+  o.h = h;
+  o.M = m;
+  o.N = d->n;
+  o.K = d->k;
+  o.rank = d->rank;
+  o.L = d->num_adapters;
+  o.da = da;
+  o.db = db;
+  if (m == 0) return launch_lora_sums(o, stream) == hipSuccess ? HM_OK : HM_ERR_HIP;
   if (!dy || !x || !h || !adapter_ids || !a || !b || !scales) return HM_ERR_NULL;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(h, 16) || !aligned(a, 16) || !aligned(b, 16) ||
       !aligned(dx_base, 16) || !aligned(dx, 16) || !aligned(adapter_ids, 4) || !aligned(scales, 4))
     return HM_ERR_ALIGN;
-  const LoraWs w = lora_ws(d, m);
+  LoraPlan w;
+  if (hm_status s = plan_lora(d, m, true, &w)) return s;
   if (!ws) return HM_ERR_NULL;
   if (ws_bytes < w.total) return HM_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return HM_ERR_ALIGN;
-  g.base = dx_base;
-  g.y = dx;
-  g.splits = w.splits_n;
-  g.part = (float*)((uint8_t*)ws + w.part);
-  hipError_t e = group_rows(d, adapter_ids, m, w, (uint8_t*)ws, &g, stream);
-  if (e == hipSuccess) e = launch_lora_shrink_b(g, stream);
-  if (e == hipSuccess && dx) e = launch_lora_expand_a(g, stream);
-  if (e == hipSuccess) e = launch_lora_outer(g, stream);
+  uint8_t* at = (uint8_t*)ws;
+  LoraArgs g = args_of(d, dy, adapter_ids, a, b, scales, m, dx_base, dx, w, at);
+  hipError_t e = group_rows(d, adapter_ids, m, w, at, &g.R, stream);
+  if (e == hipSuccess) e = launch_lora_shrink(g, false, true, stream);
+  if (e == hipSuccess && dx) e = launch_lora_expand(g, false, true, stream);
+  o.part = g.part;
+  o.splits = w.splits;
+  o.gt = (uint16_t*)(at + w.gt);
+  o.ht = (uint16_t*)(at + w.ht);
+  o.sums = (float*)(at + w.sums);
+  o.chunks = w.chunks;
+  o.R = g.R;
+  if (e == hipSuccess) e = launch_lora_pack(o, stream);
+  if (e == hipSuccess) e = launch_lora_outer(o, stream);
+  if (e == hipSuccess) e = launch_lora_sums(o, stream);
   return e == hipSuccess ? HM_OK : HM_ERR_HIP;
 }

@@ -1,279 +1,224 @@
-// Gradient of the low-rank adapters.  For the rows m of adapter e:
-//   g[m] = s_e B_e^T dy[m]                    contraction over N
-//   dx[m] = dx_base[m] + A_e^T g[m]           contraction over the rank
-//   da_e = sum_m g[m] x[m]^T,  db_e = sum_m dy[m] h[m]^T    over the rows
-// Every product runs on the bf16 MFMA, whose operands want eight consecutive
-// values of the contracted axis per lane.  Where that axis is the strided one
-// in memory (the rank of A, the columns of B, the rows of x and dy) a lane
-// loads eight rows of a few neighbouring columns and transposes them in its
-// registers; each of those columns is one MFMA's.
+// Gradient of the low-rank adapters to their matrices: for every adapter e
+// the sums over its rows m
+//   da_e = sum_m g[m] x[m]^T,   db_e = sum_m dy[m] h[m]^T
+// (g and dx are k_lora.hip's).  The contraction runs over the rows, which are
+// the strided axis of x and dy: a lane loads eight rows of eight neighbouring
+// columns and transposes them in its registers, each column being one MFMA's
+// operand.  g and h are small; a packing pass brings them into operand order
+// once (as two bf16 terms), because every column tile reads them again.
 #include "lora.h"
 
 namespace hm {
 
-// Values c .. c + W - 1 (W = 1, 2, 4, 8) of eight rows, transposed: value i
-// of out[j] is column c + j of row i (0 for rows not in `ok`).
-template <int W>
-__device__ __forceinline__ void load_cols8(const uint16_t* p, int64_t stride, int ok, u32x4_t out[W]) {
-  if constexpr (W == 8) {
-    u32x4_t in[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) in[i] = i < ok ? ld16(p + i * stride) : (u32x4_t){0u, 0u, 0u, 0u};
-    transpose8(in, out);
-  } else {
-    uint32_t in[8][(W + 1) / 2];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (W == 4) {
-        const u32x2_t v = i < ok ? *reinterpret_cast<const u32x2_t*>(p + i * stride) : (u32x2_t){0u, 0u};
-        in[i][0] = v[0];
-        in[i][1] = v[1];
-      } else if constexpr (W == 2) {
-        in[i][0] = i < ok ? *reinterpret_cast<const uint32_t*>(p + i * stride) : 0u;
-      } else {
-        in[i][0] = i < ok ? p[i * stride] : 0u;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        out[j][k] = __builtin_amdgcn_perm(in[2 * k + 1][j >> 1], in[2 * k][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
-  }
-}
-
-// grid (splits, units): g = s_e B_e^T dy, the contraction over N split as
-// k_lora_shrink splits K.  Lane (c, q) supplies rank columns W c + j of B.
+// One block per unit: g (the splits' sums) and h of its rows as [hi, lo][rank
+// row][row of the unit], zeros beyond the rank and the unit's rows.
 template <int RP>
-__global__ void __launch_bounds__(256) k_lora_shrink_b(LoraArgs g) {
-  constexpr int W = RP / 16, LD = RP + 4;
-  __shared__ float red[4][kLoraUnit][LD];
-  const int u = blockIdx.y;
-  if (u >= g.R.hdr[0]) return;
-  const int32_t* un = g.R.units + 4 * (int64_t)u;
-  const int e = un[0], first = un[1], count = un[2];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
-  const int64_t steps = (g.N + 31) / 32, waves = 4 * (int64_t)g.splits, wi = (int64_t)blockIdx.x * 4 + wave;
-  const int64_t s0 = steps * wi / waves, s1 = steps * (wi + 1) / waves;
-  const uint16_t* dp[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) dp[t] = g.dy + (int64_t)g.R.rows[first + min(16 * t + c, count - 1)] * g.N;
-  const uint16_t* bp = g.b + (int64_t)e * g.N * g.rank + W * c;
-  const bool in_rank = W * c < g.rank;
-  f32x4_t acc[2][W];
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int j = 0; j < W; ++j) acc[t][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-  for (int64_t s = s0; s < s1; ++s) {
-    const int64_t n = 32 * s + 8 * q;
-    u32x4_t dv[2], bv[W];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) dv[t] = n < g.N ? ld8_tail(dp[t], n, g.N) : (u32x4_t){0u, 0u, 0u, 0u};
-    const int64_t left = g.N - n;
-    load_cols8<W>(bp + n * g.rank, g.rank, in_rank ? (int)(left < 8 ? left : 8) : 0, bv);
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) acc[t][j] = mfma_bf16(bv[j], dv[t], acc[t][j]);
-  }
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-#pragma unroll
-      for (int j = 0; j < W; ++j) red[wave][16 * t + c][W * (4 * q + v) + j] = acc[t][j][v];
-  __syncthreads();
-  const float sc = g.scales[e];
-  float* out = g.part + (int64_t)blockIdx.x * g.M * g.rank;
-  for (int i = threadIdx.x; i < count * RP; i += 256) {
-    const int row = i / RP, r = i % RP;
-    if (r < g.rank)
-      out[(int64_t)g.R.rows[first + row] * g.rank + r] =
-          sc * ((red[0][row][r] + red[1][row][r]) + (red[2][row][r] + red[3][row][r]));
-  }
-}
-
-// grid (column slabs of K, units + groups of rows without an adapter): dx =
-// dx_base + A_e^T g.  A wave's 128 columns: lane (c, q) supplies column k0 +
-// 8 c + j to MFMA j and ends up with columns k0 + 8 (4 q + v) + j of row c.
-template <int RP>
-__global__ void __launch_bounds__(256) k_lora_expand_a(LoraArgs g) {
-  using RS = RankSteps<RP>;
-  constexpr int half = RP == 16 ? 1 : RP / 32;
-  const int64_t c0 = (int64_t)blockIdx.x * kLoraSlab, c1 = min(c0 + kLoraSlab, g.K);
-  if (blockIdx.y >= g.R.max_units) {
-    copy_rest(g, (blockIdx.y - g.R.max_units) * kLoraUnit, g.K, c0, c1, false);
-    return;
-  }
-  const int u = blockIdx.y;
-  if (u >= g.R.hdr[0]) return;
-  const int32_t* un = g.R.units + 4 * (int64_t)u;
-  const int e = un[0], first = un[1], count = un[2];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
-  int64_t m[2];
-  u32x4_t gf[2][RS::S];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    m[t] = g.R.rows[first + min(16 * t + c, count - 1)];
-    load_h_operand<RP>(g.part, g.splits, g.M, g.rank, m[t], q, gf[t]);
-  }
-  const uint16_t* A = g.a + (int64_t)e * g.rank * g.K;
-  for (int64_t k0 = c0 + 128 * wave; k0 < c1; k0 += 512) {
-    f32x4_t acc[2][8];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[t][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < half; ++s) {
-      const int r0 = RS::r0(s, q);
-      u32x4_t av[8];
-      load_cols8<8>(A + (int64_t)r0 * g.K + k0 + 8 * c, g.K, r0 < g.rank ? 8 : 0, av);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          acc[t][j] = mfma_bf16(av[j], gf[t][s], acc[t][j]);
-          if (RP != 16) acc[t][j] = mfma_bf16(av[j], gf[t][half + s], acc[t][j]);
+__global__ void __launch_bounds__(256) k_lora_pack(LoraGradArgs g) {
+  __shared__ float v[kLoraUnit][RP + 1];
+  const int u = blockIdx.x, count = g.R.units[2 * u + 1];
+  if (count == 0) return;
+  const int32_t* rows = g.R.rows + (int64_t)u * kLoraUnit;
+  for (int which = 0; which < 2; ++which) {
+    for (int i = threadIdx.x; i < kLoraUnit * (RP / 4); i += 256) {
+      const int row = i / (RP / 4), r = 4 * (i % (RP / 4));
+      f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+      if (row < count && r < g.rank) {
+        const int64_t at = (int64_t)rows[row] * g.rank + r;
+        if (which) {
+          s = *reinterpret_cast<const f32x4_t*>(g.h + at);
+        } else {
+#pragma unroll 4
+          for (int k = 0; k < g.splits; ++k)
+            s += *reinterpret_cast<const f32x4_t*>(g.part + (int64_t)k * g.M * g.rank + at);
         }
-    }
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      if (16 * t + c >= count) continue;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float o[8] = {acc[t][0][v], acc[t][1][v], acc[t][2][v], acc[t][3][v],
-                            acc[t][4][v], acc[t][5][v], acc[t][6][v], acc[t][7][v]};
-        add_store8(g.base ? g.base + m[t] * g.K : nullptr, g.y + m[t] * g.K, k0 + 32 * q + 8 * v, g.K, o);
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[row][r + k] = s[k];
     }
+    __syncthreads();
+    uint16_t* out = (which ? g.ht : g.gt) + (int64_t)u * 2 * RP * kLoraUnit;
+    for (int i = threadIdx.x; i < RP * (kLoraUnit / 8); i += 256) {
+      const int r = i / (kLoraUnit / 8), m = 8 * (i % (kLoraUnit / 8));
+      u32x4_t hi, lo;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t h2, l2;
+        split2(v[m + 2 * k][r], v[m + 2 * k + 1][r], &h2, &l2);
+        hi[k] = h2;
+        lo[k] = l2;
+      }
+      st16(out + r * kLoraUnit + m, hi);
+      st16(out + (RP + r) * kLoraUnit + m, lo);
+    }
+    __syncthreads();
   }
 }
 
-// grid (128-column tiles, rank chunks of 16 RB, adapters): the contraction
-// over an adapter's rows.  COLS rows of z (x or dy) of `n` columns against f
-// (g summed over its splits, or h): out[r][col] (da) or out[col][r] (db).
-// The block's waves split the rows; their sums meet in LDS, in wave order.
-template <int RB, bool DB>
-__global__ void __launch_bounds__(256) k_lora_outer(LoraArgs g) {
+__device__ __forceinline__ int chunk_units(const LoraGradArgs& g) {
+  return (g.R.first[g.L] + g.chunks - 1) / g.chunks;
+}
+
+// grid (128-column tiles of dy, then of x; chunks of units; rank chunks of 16
+// RB): one adapter of the chunk after the other.  The waves take its 32-row
+// steps in turn; their sums meet in LDS, in wave order.  An adapter that
+// reaches beyond the chunk leaves a partial sum: slot 2 j if it began before
+// chunk j, else 2 j + 1.
+template <int RP, int RB, bool db>
+__device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, float (*red)[132]) {
   constexpr int RC = 16 * RB;
-  __shared__ float red[RC][132];
-  const int e = blockIdx.z, r00 = blockIdx.y * RC;
-  const int64_t n = DB ? g.N : g.K, k0 = 128 * (int64_t)blockIdx.x;
-  const uint16_t* z = DB ? g.dy : g.x;
-  const float* f = DB ? g.h : g.part;
-  const int splits = DB ? 1 : g.splits;
+  const int64_t n = db ? g.N : g.K;
+  const uint16_t* z = db ? g.dy : g.x;
+  const int r00 = blockIdx.z * RC;
+  const uint16_t* f = (db ? g.ht : g.gt) + r00 * kLoraUnit;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
-  const int beg = g.M ? g.R.offsets[e] : 0, end = g.M ? g.R.offsets[e + 1] : 0;
+  const int per = chunk_units(g), lo_u = blockIdx.y * per, hi_u = min(lo_u + per, g.R.first[g.L]);
   const int64_t col = k0 + 8 * c;
-  f32x4_t acc[8][RB];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int i = 0; i < RB; ++i) acc[j][i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-  for (int b = beg + 32 * wave; b < end; b += 128) {
-    u32x4_t in[8], zv[8], hi[RB], lo[RB];
-    float fv[RB][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool ok = b + 8 * q + i < end;
-      const int64_t m = ok ? g.R.rows[b + 8 * q + i] : 0;
-      in[i] = ok && col < n ? ld8_tail(z + m * n, col, n) : (u32x4_t){0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int k = 0; k < RB; ++k) {
-        const int r = r00 + 16 * k + c;
-        float v = 0.f;
-        if (ok && r < g.rank)
-          for (int s = 0; s < splits; ++s) v += f[((int64_t)s * g.M + m) * g.rank + r];
-        fv[k][i] = v;
-      }
-    }
-    transpose8(in, zv);
-#pragma unroll
-    for (int k = 0; k < RB; ++k) split8(fv[k], &hi[k], &lo[k]);
+  for (int ua = lo_u; ua < hi_u;) {
+    const int e = g.R.units[2 * ua], e0 = g.R.first[e], e1 = g.R.first[e + 1], ub = min(e1, hi_u);
+    f32x4_t acc[8][RB];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
+      for (int i = 0; i < RB; ++i) acc[j][i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    for (int s = 2 * ua + wave; s < 2 * ub; s += 4) {
+      const int u = s >> 1, first = 32 * (s & 1), count = g.R.units[2 * u + 1] - first;
+      if (count <= 0) continue;
+      const int32_t* rows = g.R.rows + (int64_t)u * kLoraUnit + first;
+      Cols8<8> zv;
+      u32x4_t fh[RB], fl[RB];
+      const uint16_t* fu = f + ((int64_t)u * 2 * RP + c) * kLoraUnit + first + 8 * q;
+#pragma unroll
       for (int k = 0; k < RB; ++k) {
-        if (DB) {
-          acc[j][k] = mfma_bf16(hi[k], zv[j], acc[j][k]);
-          acc[j][k] = mfma_bf16(lo[k], zv[j], acc[j][k]);
-        } else {
-          acc[j][k] = mfma_bf16(zv[j], hi[k], acc[j][k]);
-          acc[j][k] = mfma_bf16(zv[j], lo[k], acc[j][k]);
+        fh[k] = ld16(fu + 16 * k * kLoraUnit);
+        fl[k] = ld16(fu + (RP + 16 * k) * kLoraUnit);
+      }
+      // rows behind the unit's last repeat its first: their g and h are 0
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t m = rows[8 * q + i < count ? 8 * q + i : 0];
+        u32x4_t v = {0u, 0u, 0u, 0u};
+        if (col < n) v = ld8_tail(z + m * n, col, n);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) zv.w[i][k] = v[k];
+      }
+      loads_first();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const u32x4_t zo = zv.operand(j);
+#pragma unroll
+        for (int k = 0; k < RB; ++k) {
+          if (db) {
+            acc[j][k] = mfma_bf16(fh[k], zo, acc[j][k]);
+            acc[j][k] = mfma_bf16(fl[k], zo, acc[j][k]);
+          } else {
+            acc[j][k] = mfma_bf16(zo, fh[k], acc[j][k]);
+            acc[j][k] = mfma_bf16(zo, fl[k], acc[j][k]);
+          }
         }
       }
-  }
-  // DB: lane holds columns 8 c + j, rank 16 k + 4 q + v; else rank 16 k + c, columns 8 (4 q + v) + j
-  for (int w = 0; w < 4; ++w) {
-    if (w == wave)
+    }
+    // db: the lane holds column 8 c + j, rank 16 k + 4 q + v; da: rank 16 k + c, column 8 (4 q + v) + j
+    for (int w = 0; w < 4; ++w) {
+      if (w == wave)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int k = 0; k < RB; ++k)
+          for (int k = 0; k < RB; ++k)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            float* p = DB ? &red[16 * k + 4 * q + v][8 * c + j] : &red[16 * k + c][8 * (4 * q + v) + j];
-            *p = w == 0 ? acc[j][k][v] : *p + acc[j][k][v];
-          }
-    __syncthreads();
-  }
-  if (DB) {
+            for (int v = 0; v < 4; ++v) {
+              float* p = db ? &red[16 * k + 4 * q + v][8 * c + j] : &red[16 * k + c][8 * (4 * q + v) + j];
+              *p = w == 0 ? acc[j][k][v] : *p + acc[j][k][v];
+            }
+      __syncthreads();
+    }
+    const bool whole = e0 >= lo_u && e1 <= hi_u;
+    float* part = g.sums + (int64_t)(2 * blockIdx.y + (e0 < lo_u ? 0 : 1)) * g.rank * (g.K + g.N);
     for (int i = threadIdx.x; i < 128 * RC / 8; i += 256) {
-      const int cc = i / (RC / 8), r = 8 * (i % (RC / 8));
-      if (k0 + cc >= n || r00 + r >= g.rank) continue;
-      u32x4_t o;
+      int64_t at;
+      float o[8];
+      if (db) {
+        const int cc = i / (RC / 8), r = 8 * (i % (RC / 8));
+        if (k0 + cc >= n || r00 + r >= g.rank) continue;
+        at = (k0 + cc) * g.rank + r00 + r;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) o[p] = pack_bf16(red[r + 2 * p][cc], red[r + 2 * p + 1][cc]);
-      st16(g.db + ((int64_t)e * n + k0 + cc) * g.rank + r00 + r, o);
-    }
-  } else {
-    for (int i = threadIdx.x; i < 16 * RC; i += 256) {
-      const int r = i / 16, cc = 8 * (i % 16);
-      if (r00 + r >= g.rank) continue;
-      u32x4_t o;
+        for (int k = 0; k < 8; ++k) o[k] = red[r + k][cc];
+      } else {
+        const int r = i / 16, cc = 8 * (i % 16);
+        if (r00 + r >= g.rank) continue;
+        at = (int64_t)(r00 + r) * n + k0 + cc;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) o[p] = pack_bf16(red[r][cc + 2 * p], red[r][cc + 2 * p + 1]);
-      st16(g.da + ((int64_t)e * g.rank + r00 + r) * n + k0 + cc, o);
+        for (int k = 0; k < 8; ++k) o[k] = red[r][cc + k];
+      }
+      if (whole) {
+        st16((db ? g.db : g.da) + (int64_t)e * n * g.rank + at,
+             (u32x4_t){pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7])});
+      } else {
+        float* p = part + (db ? (int64_t)g.rank * g.K : 0) + at;
+        *reinterpret_cast<f32x4_t*>(p) = (f32x4_t){o[0], o[1], o[2], o[3]};
+        *reinterpret_cast<f32x4_t*>(p + 4) = (f32x4_t){o[4], o[5], o[6], o[7]};
+      }
     }
+    __syncthreads();
+    ua = ub;
   }
 }
 
-#define HM_LORA_RANKS(K, grid)                                                        \
-  switch (lora_rp(g.rank)) {                                                          \
-    case 16: hipLaunchKernelGGL(K<16>, grid, dim3(256), 0, st, g); break;             \
-    case 32: hipLaunchKernelGGL(K<32>, grid, dim3(256), 0, st, g); break;             \
-    case 64: hipLaunchKernelGGL(K<64>, grid, dim3(256), 0, st, g); break;             \
-    default: hipLaunchKernelGGL(K<128>, grid, dim3(256), 0, st, g);                   \
+template <int RP, int RB>
+__global__ void __launch_bounds__(256, 2) k_lora_outer(LoraGradArgs g) {
+  __shared__ float red[16 * RB][132];
+  const int tiles_n = (int)((g.N + 127) / 128);
+  if ((int)blockIdx.x < tiles_n) outer_tile<RP, RB, true>(g, 128 * (int64_t)blockIdx.x, red);
+  else outer_tile<RP, RB, false>(g, 128 * (int64_t)(blockIdx.x - tiles_n), red);
+}
+
+// grid (eight values per thread of an adapter's da and db, adapters): sums of
+// the partial sums in chunk order, zeros for adapters without rows.
+__global__ void __launch_bounds__(256) k_lora_sums(LoraGradArgs g) {
+  const int e = blockIdx.y;
+  const int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x), na = (int64_t)g.rank * g.K, nb = (int64_t)g.rank * g.N;
+  if (i >= na + nb) return;
+  f32x4_t a = {0.f, 0.f, 0.f, 0.f}, b = {0.f, 0.f, 0.f, 0.f};
+  const int u0 = g.M ? g.R.first[e] : 0, u1 = g.M ? g.R.first[e + 1] : 0;
+  if (u1 > u0) {
+    const int per = chunk_units(g), j0 = u0 / per, j1 = (u1 - 1) / per;
+    if (j0 == j1) return;                                     // written whole
+    for (int j = j0; j <= j1; ++j) {
+      const float* p = g.sums + (int64_t)(2 * j + (j == j0 ? 1 : 0)) * (na + nb) + i;
+      a += *reinterpret_cast<const f32x4_t*>(p);
+      b += *reinterpret_cast<const f32x4_t*>(p + 4);
+    }
   }
+  st16(i < na ? g.da + e * na + i : g.db + e * nb + i - na,
+       (u32x4_t){pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])});
+}
 
-hipError_t launch_lora_shrink_b(const LoraArgs& g, hipStream_t st) {
-  const dim3 grid((unsigned)g.splits, (unsigned)g.R.max_units);
-  HM_LORA_RANKS(k_lora_shrink_b, grid)
+hipError_t launch_lora_pack(const LoraGradArgs& g, hipStream_t st) {
+  const dim3 grid((unsigned)g.R.max_units);
+  switch (lora_rp(g.rank)) {
+    case 16: hipLaunchKernelGGL(k_lora_pack<16>, grid, dim3(256), 0, st, g); break;
+    case 32: hipLaunchKernelGGL(k_lora_pack<32>, grid, dim3(256), 0, st, g); break;
+    case 64: hipLaunchKernelGGL(k_lora_pack<64>, grid, dim3(256), 0, st, g); break;
+    default: hipLaunchKernelGGL(k_lora_pack<128>, grid, dim3(256), 0, st, g);
+  }
   return hipGetLastError();
 }
 
-hipError_t launch_lora_expand_a(const LoraArgs& g, hipStream_t st) {
-  const dim3 grid((unsigned)((g.K + kLoraSlab - 1) / kLoraSlab),
-                  (unsigned)(g.R.max_units + (g.base != g.y ? (g.M + kLoraUnit - 1) / kLoraUnit : 0)));
-  HM_LORA_RANKS(k_lora_expand_a, grid)
+hipError_t launch_lora_outer(const LoraGradArgs& g, hipStream_t st) {
+  dim3 grid((unsigned)((g.N + 127) / 128 + g.K / 128), (unsigned)g.chunks, 1);
+  switch (lora_rp(g.rank)) {
+    case 16: hipLaunchKernelGGL((k_lora_outer<16, 1>), grid, dim3(256), 0, st, g); break;
+    case 32: hipLaunchKernelGGL((k_lora_outer<32, 2>), grid, dim3(256), 0, st, g); break;
+    case 64: hipLaunchKernelGGL((k_lora_outer<64, 4>), grid, dim3(256), 0, st, g); break;
+    default:
+      grid.z = 2;
+      hipLaunchKernelGGL((k_lora_outer<128, 4>), grid, dim3(256), 0, st, g);
+  }
   return hipGetLastError();
 }
 
-template <bool DB>
-static void outer(const LoraArgs& g, hipStream_t st) {
-  const unsigned tiles = (unsigned)(((DB ? g.N : g.K) + 127) / 128);
-  if (g.rank <= 16) hipLaunchKernelGGL((k_lora_outer<1, DB>), dim3(tiles, 1, g.L), dim3(256), 0, st, g);
-  else if (g.rank <= 32) hipLaunchKernelGGL((k_lora_outer<2, DB>), dim3(tiles, 1, g.L), dim3(256), 0, st, g);
-  else hipLaunchKernelGGL((k_lora_outer<4, DB>), dim3(tiles, (g.rank + 63) / 64, g.L), dim3(256), 0, st, g);
-}
-
-hipError_t launch_lora_outer(const LoraArgs& g, hipStream_t st) {
-  outer<false>(g, st);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  outer<true>(g, st);
+hipError_t launch_lora_sums(const LoraGradArgs& g, hipStream_t st) {
+  const int64_t per = g.rank * (g.K + g.N) / 8;
+  hipLaunchKernelGGL(k_lora_sums, dim3((unsigned)((per + 255) / 256), (unsigned)g.L), dim3(256), 0, st, g);
   return hipGetLastError();
 }
 

@@ -1,6 +1,6 @@
-// Low-rank adapters of many requests: kernel arguments, the workspace layout
-// and the device helpers that the forward kernels (k_lora.hip) and the
-// gradient's (k_lora_grad.hip) share.
+// Low-rank adapters of many requests: kernel arguments, workspace layout and
+// the device helpers that the products (k_lora.hip) and the sums over rows
+// (k_lora_grad.hip) share.
 #pragma once
 #include "common.h"
 #include "launch.h"
@@ -8,145 +8,118 @@
 
 namespace hm {
 
-constexpr int kLoraUnit = 32;        // rows per unit: rows of one adapter that share its matrices' loads
-constexpr int kLoraSlab = 512;       // output columns per block of the expanding kernels
 constexpr int64_t kLoraMaxRows = 1 << 20;
+constexpr int kLoraDirect = 64;      // most rows of a call whose blocks find their unit from the ids themselves
+constexpr int kLoraPlanBlocks = 256; // most blocks of the grouping kernel
+constexpr int kLoraMaxSplits = 16;   // most blocks along a contraction
+constexpr int kLoraUnit = 64;        // rows per unit of the gradient
+constexpr int kLoraCols = 256;       // output columns per block of the expanding kernel
 
-// Rows of a call grouped by adapter: hdr[0] units of {adapter, first index
-// into rows, count, 0}, the rows ascending within an adapter.
+// Rows grouped by adapter.  A unit is up to unit_rows rows of one adapter,
+// which share the loads of its matrices: units[u] = {adapter, count}, count 0
+// from the last used unit on, its rows (ascending) in rows[u unit_rows ..].
+// The units of an adapter are consecutive, first[e] .. first[e + 1] - 1.
 struct LoraRows {
-  const int32_t* hdr;
   const int32_t* units;
-  const int32_t* offsets;    // [L + 1] into rows
   const int32_t* rows;
+  const int32_t* first;
   int64_t max_units;
+  int unit_rows;             // 16, 32 or 64
 };
 
 struct LoraArgs {
-  const uint16_t *x, *dy;    // bf16 [M][K], [M][N]
+  const uint16_t* z;         // bf16 [M][len]: the contracted rows (x, or dy)
   const uint16_t *a, *b;     // bf16 [L][rank][K], [L][N][rank]
   const float* scales;
   const int32_t* ids;
   int64_t M, N, K;
   int rank, L;
-  const uint16_t* base;      // [M][N] (forward), [M][K] (gradient) or null
-  uint16_t* y;               // [M][N] (forward), [M][K] (gradient)
-  float* h;                  // [M][rank]: written by the forward, read by the gradient
-  float* part;               // fp32 [splits][M][rank] sums of the contracting kernels
+  const uint16_t* base;      // [M][cols] or null
+  uint16_t* y;               // [M][cols]: the expanded rows (y, or dx)
+  float* h;                  // [M][rank]: written by the forward if not null
+  float* part;               // fp32 [splits][M][rank] contracted values
   int splits;
+  int group;                 // units per expanding block
+  LoraRows R;
+};
+
+// Sums over an adapter's rows: da = g x^T, db = dy h^T.
+struct LoraGradArgs {
+  const uint16_t *x, *dy;
+  const float *h, *part;     // h [M][rank]; g as fp32 [splits][M][rank]
+  int splits;
+  int64_t M, N, K;
+  int rank, L;
+  uint16_t *gt, *ht;         // packed g and h: [unit][2 (hi, lo)][RP][kLoraUnit]
+  float* sums;               // partial sums [2 chunks][rank (K + N)]
+  int chunks;
   uint16_t *da, *db;
   LoraRows R;
 };
 
-// Byte offsets of the row grouping in the workspace; total a multiple of 256.
-struct LoraWs {
-  size_t hdr, units, counts, offsets, rows, cnt, part, total;
-  int64_t max_units;
-  int splits, splits_n;
-};
-
 inline int lora_rp(int rank) { return rank <= 16 ? 16 : (rank <= 32 ? 32 : (rank <= 64 ? 64 : 128)); }
 
-hipError_t launch_lora_units(const int32_t* offsets, int L, int32_t* hdr, int32_t* units, hipStream_t st);
-hipError_t launch_lora_shrink(const LoraArgs& g, hipStream_t st);
-hipError_t launch_lora_expand(const LoraArgs& g, hipStream_t st);
-hipError_t launch_lora_shrink_b(const LoraArgs& g, hipStream_t st);
-hipError_t launch_lora_expand_a(const LoraArgs& g, hipStream_t st);
-hipError_t launch_lora_outer(const LoraArgs& g, hipStream_t st);
+// Grouping of M rows by adapter id (ids outside [0, L) are left out).
+hipError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, int unit_rows, int64_t max_units, int32_t* units,
+                            int32_t* rows, int32_t* first, hipStream_t st);
+// part = scale * (A z) or, trans, scale * (B^T z).  direct: units found from
+// the ids by every block (M <= kLoraDirect, 16 rows a unit).
+hipError_t launch_lora_shrink(const LoraArgs& g, bool direct, bool trans, hipStream_t st);
+// y = base + B h or, trans, base + A^T g.
+hipError_t launch_lora_expand(const LoraArgs& g, bool direct, bool trans, hipStream_t st);
+hipError_t launch_lora_pack(const LoraGradArgs& g, hipStream_t st);
+hipError_t launch_lora_outer(const LoraGradArgs& g, hipStream_t st);
+hipError_t launch_lora_sums(const LoraGradArgs& g, hipStream_t st);
 
 #ifdef __HIPCC__
-// fp32 -> two bf16 terms hi + lo: hi = bf16(v), lo = bf16(v - hi).  The sum
-// carries v to 2^-16 of its size, far below the bf16 rounding of the results
-// (2^-8), where hi alone would add an error as large as that rounding.
-__device__ __forceinline__ void split8(const float v[8], u32x4_t* hi, u32x4_t* lo) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t h = pack_bf16(v[2 * j], v[2 * j + 1]);
-    (*hi)[j] = h;
-    (*lo)[j] = pack_bf16(v[2 * j] - lo_bf16(h), v[2 * j + 1] - hi_bf16(h));
-  }
+template <int N> struct Int { static constexpr int value = N; };
+
+// fp32 pair -> two bf16 terms hi + lo: hi = bf16(v), lo = bf16(v - hi).  The
+// sum carries v to 2^-16 of its size, far below the bf16 rounding of the
+// results (2^-8), where hi alone would add an error as large as that rounding.
+__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo) {
+  *hi = pack_bf16(a, b);
+  *lo = pack_bf16(a - lo_bf16(*hi), b - hi_bf16(*hi));
 }
 
-// 8 x 8 transpose of 16-bit values inside a lane: value i of out[j] is value
-// j of in[i].
-__device__ __forceinline__ void transpose8(const u32x4_t in[8], u32x4_t out[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-      out[j][p] = __builtin_amdgcn_perm(in[2 * p + 1][j >> 1], in[2 * p][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+// Keeps the loads written before this point before it (the compiler would
+// otherwise move each next to its use, one round trip to memory per load).
+__device__ __forceinline__ void loads_first() {
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
-// Sum over the splits of row m's contracted values r0 .. r0 + 7, in split order.
-__device__ __forceinline__ void load_h8(const float* __restrict__ part, int splits, int64_t M, int rank, int64_t m,
-                                        int r0, float v[8]) {
+// Words of eight rows of W (1, 2, 4, 8) neighbouring 16-bit columns, and
+// their transpose: value i of column j's operand is row i.
+template <int W> struct Cols8 {
+  uint32_t w[8][(W + 1) / 2];
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t stride, int ok) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  if (r0 >= rank) return;
-  for (int s = 0; s < splits; ++s) {
-    const float4* p = reinterpret_cast<const float4*>(part + ((int64_t)s * M + m) * rank + r0);
-    const float4 a = p[0], b = p[1];
-    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-  }
-}
-
-// K steps (of 32) of the second product over [hi | lo] of RP rank columns,
-// and the rank column lane quarter q supplies first in step s.  RP = 16: one
-// step, quarters 0-1 hi, 2-3 lo.
-template <int RP> struct RankSteps {
-  static constexpr int S = RP == 16 ? 1 : RP / 16;
-  __device__ static int r0(int s, int q) { return RP == 16 ? 8 * (q & 1) : 32 * (s % (RP / 32)) + 8 * q; }
-  __device__ static bool lo(int s, int q) { return RP == 16 ? q >= 2 : s >= RP / 32; }
-};
-
-// MFMA operand (column = the lane's row m) of the second product.
-template <int RP>
-__device__ __forceinline__ void load_h_operand(const float* __restrict__ part, int splits, int64_t M, int rank, int64_t m,
-                                               int q, u32x4_t hf[RankSteps<RP>::S]) {
-  using RS = RankSteps<RP>;
-  constexpr int half = RP == 16 ? 1 : RP / 32;
+    for (int i = 0; i < 8; ++i) {
+      const uint16_t* r = p + i * stride;
+      if constexpr (W == 8) {
+        const u32x4_t v = i < ok ? ld16(r) : (u32x4_t){0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int s = 0; s < half; ++s) {
-    float v[8];
-    load_h8(part, splits, M, rank, m, RS::r0(s, q), v);
-    u32x4_t hi, lo;
-    split8(v, &hi, &lo);
-    if (RP == 16) {
-      hf[0] = q >= 2 ? lo : hi;
-    } else {
-      hf[s] = hi;
-      hf[half + s] = lo;
+        for (int k = 0; k < 4; ++k) w[i][k] = v[k];
+      } else if constexpr (W == 4) {
+        const u32x2_t v = i < ok ? *reinterpret_cast<const u32x2_t*>(r) : (u32x2_t){0u, 0u};
+        w[i][0] = v[0];
+        w[i][1] = v[1];
+      } else if constexpr (W == 2) {
+        w[i][0] = i < ok ? *reinterpret_cast<const uint32_t*>(r) : 0u;
+      } else {
+        w[i][0] = i < ok ? *r : 0u;
+      }
     }
   }
-}
-
-// Adds base to eight consecutive results and writes them (columns c .. c + 7
-// of a row of n).
-__device__ __forceinline__ void add_store8(const uint16_t* base, uint16_t* y, int64_t c, int64_t n, const float v[8]) {
-  u32x4_t o = {0u, 0u, 0u, 0u};
-  if (base) o = ld8_tail(base, c, n);
+  __device__ __forceinline__ u32x4_t operand(int j) const {
+    u32x4_t o;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = pack_bf16(lo_bf16(o[e]) + v[2 * e], hi_bf16(o[e]) + v[2 * e + 1]);
-  st8_tail(y, c, n, o);
-}
-
-// Rows of [m0, m0 + kLoraUnit) without an adapter, columns [c0, c1): y = base
-// (zeros without one).  One wave per row.
-__device__ __forceinline__ void copy_rest(const LoraArgs& g, int64_t m0, int64_t n, int64_t c0, int64_t c1, bool zero_h) {
-  const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
-  for (int i = threadIdx.x >> 6; i < kLoraUnit; i += nw) {
-    const int64_t m = m0 + i;
-    if (m >= g.M) break;
-    const int e = g.ids[m];
-    if (e >= 0 && e < g.L) continue;
-    if (g.base != g.y)
-      for (int64_t c = c0 + 8 * lane; c < c1; c += 512)
-        st8_tail(g.y + m * n, c, n, g.base ? ld8_tail(g.base + m * n, c, n) : (u32x4_t){0u, 0u, 0u, 0u});
-    if (zero_h)
-      for (int r = lane; r < g.rank; r += 64) g.h[m * g.rank + r] = 0.f;
+    for (int k = 0; k < 4; ++k)
+      o[k] = __builtin_amdgcn_perm(w[2 * k + 1][j >> 1], w[2 * k][j >> 1], (j & 1) ? 0x07060302u : 0x05040100u);
+    return o;
   }
-}
+};
 #endif
 
 }  // namespace hm
