@@ -32,18 +32,27 @@ k_lora_plan(const int32_t* __restrict__ ids, int64_t M, int L, int64_t C, int U,
   for (int i = tid; i < 512; i += kSortThreads) before[i] = after[i] = 0;
   __syncthreads();
   const int64_t lo = (int64_t)blockIdx.x * C, hi = min(lo + C, M);
-  for (int64_t p0 = 0; p0 < M; p0 += kSortThreads) {          // C is a multiple of kSortThreads
-    int* cnt = p0 < lo ? before : after;
-    const int e = p0 + tid < M ? ids[p0 + tid] : -1;
-    const bool ok = e >= 0 && e < L;
-    const uint64_t m = __ballot(ok);
-    if (!m) continue;
-    // rows of a prompt carry one id: one addition for the wave
-    const int first = __shfl(e, __builtin_ctzll(m), 64);
-    if (__ballot(ok && e == first) == m) {
-      if (lane == 0) atomicAdd(&cnt[first], __popcll(m));
-    } else if (ok) {
-      atomicAdd(&cnt[e], 1);
+  for (int64_t p0 = 0; p0 < M; p0 += 8 * kSortThreads) {
+    int id[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t p = p0 + i * kSortThreads + tid;
+      id[i] = p < M ? ids[p] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      int* cnt = p0 + i * kSortThreads < lo ? before : after; // C is a multiple of kSortThreads
+      const int e = id[i];
+      const bool ok = e >= 0 && e < L;
+      const uint64_t m = __ballot(ok);
+      if (!m) continue;
+      // rows of a prompt carry one id: one addition for the wave
+      const int first = __shfl(e, __builtin_ctzll(m), 64);
+      if (__ballot(ok && e == first) == m) {
+        if (lane == 0) atomicAdd(&cnt[first], __popcll(m));
+      } else if (ok) {
+        atomicAdd(&cnt[e], 1);
+      }
     }
   }
   __syncthreads();
@@ -99,89 +108,105 @@ __device__ __forceinline__ int find_unit(const LoraArgs& g, int u, int first, in
 }
 
 // Waves of a contracting block.
-constexpr int shrink_waves(int t) { return t == 1 ? 4 : 8; }
+constexpr int shrink_waves(int rp, int t) { return t == 1 || rp == 128 ? 4 : 8; }
+
+// A wave's private LDS image of 64 values of 16 rows: row r's 16-byte chunk k
+// (0 .. 7) sits at place k ^ (r & 7) of its 128 bytes, so that both the
+// writes (eight lanes per row) and the reads (sixteen rows' chunk) spread over
+// the banks.
+__device__ __forceinline__ int chunk_at(int r, int k) { return r * 128 + ((k ^ (r & 7)) << 4); }
 
 // grid (splits, units x blocks of 16 T rows): the block's waves split the
-// block's range of the contracted axis; their sums meet in LDS and are added
-// in wave order.  A wave loads NB steps of 32 values before the first MFMA.
+// block's range of the contracted axis into steps of 64; their sums meet in
+// LDS and are added in wave order.  A load instruction is cheapest when
+// neighbouring lanes read neighbouring bytes, while an MFMA operand has a row
+// per lane: loaded in operand order, sixteen lanes touch sixteen cache lines
+// of 16 bytes each and the address unit, not HBM, sets the pace (m = 8192, k =
+// 4096, rank 64: 50 us).  So a wave loads eight whole lines per instruction
+// into registers, one step ahead, and passes them through its own LDS image;
+// no block barrier.
 template <int RP, int T, bool DIRECT, bool TRANS>
-__global__ void __launch_bounds__(64 * shrink_waves(T)) k_lora_shrink(LoraArgs g) {
-  constexpr int RB = RP / 16, LD = RP + 4, U = 16 * T, NW = shrink_waves(T);
-  constexpr int NB = TRANS ? (RP >= 64 ? 2 : 4) : (T + RB > 8 ? 2 : (T + RB > 4 ? 4 : 8));
-  // LDS images of the sums: one per wave while that is small, else one for several waves in turn
-  constexpr int FIT = 70 * 1024 / (U * LD * 4);
+__global__ void __launch_bounds__(64 * shrink_waves(RP, T)) k_lora_shrink(LoraArgs g) {
+  constexpr int RB = RP / 16, LD = RP + 4, U = 16 * T, NW = shrink_waves(RP, T);
+  constexpr int TILES = TRANS ? T : T + RB;                   // 16-row tiles staged per step
+  // LDS: the waves' images, then the sums (one per wave while that is small, else one for several waves in turn)
+  constexpr int IMG = TILES * 2048, FIT = 72 * 1024 / (U * LD * 4);
   constexpr int BUF = FIT >= NW ? NW : (FIT >= NW / 2 ? NW / 2 : (FIT >= NW / 4 ? NW / 4 : 1));
-  __shared__ float red[BUF][U][LD];
+  constexpr int BYTES = NW * IMG > BUF * U * LD * 4 ? NW * IMG : BUF * U * LD * 4;
+  __shared__ __align__(16) uint8_t lds[BYTES];
   __shared__ int rows[U];
   const int sub = DIRECT ? 1 : g.R.unit_rows / U;
   int e;
   const int count = find_unit<U, DIRECT>(g, blockIdx.y / sub, blockIdx.y % sub * U, &e, rows);
   if (count <= 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
+  const int lr = lane >> 3, lk = lane & 7;                    // loads: row of eight, chunk of its line
   const int64_t len = TRANS ? g.N : g.K;
-  const int steps = (int)(len / 32), waves = NW * g.splits, wi = (int)blockIdx.x * NW + wave;
+  const int steps = (int)((len + 63) / 64), waves = NW * g.splits, wi = (int)blockIdx.x * NW + wave;
   const int s0 = (int)((int64_t)steps * wi / waves), s1 = (int)((int64_t)steps * (wi + 1) / waves);
-  const uint16_t* zp[T];
+  uint8_t* img = lds + wave * IMG;
+  // rows of z, then (A) the rank's rows of A; rows past the last repeat it (their results are not kept)
+  const uint16_t* zp[2 * TILES];
 #pragma unroll
-  for (int t = 0; t < T; ++t) zp[t] = g.z + (int64_t)rows[min(16 * t + c, count - 1)] * len + 8 * q;
-  // A: lane c supplies rank row 16 i + c to MFMA i (rows past the rank repeat its last one; their results are not
-  // kept).  B, transposed: rank column RB c + i.
-  const uint16_t* ap[TRANS ? 1 : RB];
-  if constexpr (TRANS) {
-    ap[0] = g.b + ((int64_t)e * g.N + 8 * q) * g.rank + RB * c;
-  } else {
-#pragma unroll
-    for (int i = 0; i < RB; ++i) ap[i] = g.a + ((int64_t)e * g.rank + min(16 * i + c, g.rank - 1)) * g.K + 8 * q;
+  for (int i = 0; i < 2 * TILES; ++i) {
+    const int r = 8 * i + lr;
+    if (i < 2 * T) zp[i] = g.z + (int64_t)rows[min(r, count - 1)] * len + 8 * lk;
+    else zp[i] = g.a + ((int64_t)e * g.rank + min(r - U, g.rank - 1)) * len + 8 * lk;
   }
+  // B, transposed: lane c supplies rank column RB c + i to MFMA i
+  const uint16_t* bp = TRANS ? g.b + ((int64_t)e * g.N + 8 * q) * g.rank + RB * c : nullptr;
   const int in_rank = RB * c < g.rank ? 8 : 0;
   f32x4_t acc[T][RB];
 #pragma unroll
   for (int t = 0; t < T; ++t)
 #pragma unroll
     for (int i = 0; i < RB; ++i) acc[t][i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-  auto batch = [&](int s, auto steps_c) __attribute__((always_inline)) {
-    constexpr int n = decltype(steps_c)::value;
-    u32x4_t zv[n][T], av[n][TRANS ? 1 : RB];
-    Cols8<TRANS ? RB : 1> bv[n];
+  u32x4_t next[2 * TILES];
+  Cols8<TRANS ? RB : 1> bn[2];
+  auto load = [&](int s) __attribute__((always_inline)) {
+    const int64_t at = 64 * (int64_t)s;
+    const bool whole = !TRANS || at + 64 <= len;
 #pragma unroll
-    for (int j = 0; j < n; ++j) {
+    for (int i = 0; i < 2 * TILES; ++i) {
+      if (whole) next[i] = TRANS ? ld8(zp[i] + at) : ld16(zp[i] + at);
+      else next[i] = at + 8 * lk < len ? ld8_tail(zp[i] - 8 * lk, at + 8 * lk, len) : (u32x4_t){0u, 0u, 0u, 0u};
+    }
+    if constexpr (TRANS) {
 #pragma unroll
-      for (int t = 0; t < T; ++t) zv[j][t] = TRANS ? ld8(zp[t] + 32 * (s + j)) : ld16(zp[t] + 32 * (s + j));
-      if constexpr (TRANS) {
-        bv[j].load(ap[0] + (int64_t)32 * (s + j) * g.rank, g.rank, in_rank);
-      } else {
-#pragma unroll
-        for (int i = 0; i < RB; ++i) av[j][i] = ld16(ap[i] + 32 * (s + j));
+      for (int j = 0; j < 2; ++j) {
+        const int64_t left = len - (at + 32 * j + 8 * q);
+        bn[j].load(bp + (at + 32 * j) * g.rank, g.rank, whole ? in_rank : (int)max(min(left, (int64_t)in_rank), (int64_t)0));
       }
     }
-    loads_first();
+  };
+  if (s0 < s1) load(s0);
+  for (int s = s0; s < s1; ++s) {
 #pragma unroll
-    for (int j = 0; j < n; ++j)
+    for (int i = 0; i < 2 * TILES; ++i) st16(img + chunk_at(8 * i + lr, lk), next[i]);
+    Cols8<TRANS ? RB : 1> bv[2];
+    if constexpr (TRANS) {
+      bv[0] = bn[0];
+      bv[1] = bn[1];
+    }
+    __asm__ volatile("" ::: "memory");                        // a wave's LDS accesses stay in order
+    if (s + 1 < s1) load(s + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      u32x4_t zv[T];
+#pragma unroll
+      for (int t = 0; t < T; ++t) zv[t] = ld16(img + chunk_at(16 * t + c, 4 * j + q));
 #pragma unroll
       for (int i = 0; i < RB; ++i) {
-        const u32x4_t a = TRANS ? bv[j].operand(i) : av[j][TRANS ? 0 : i];
+        const u32x4_t a = TRANS ? bv[j].operand(TRANS ? i : 0) : ld16(img + chunk_at(U + 16 * i + c, 4 * j + q));
 #pragma unroll
-        for (int t = 0; t < T; ++t) acc[t][i] = mfma_bf16(a, zv[j][t], acc[t][i]);
+        for (int t = 0; t < T; ++t) acc[t][i] = mfma_bf16(a, zv[t], acc[t][i]);
       }
-  };
-  int s = s0;
-  for (; s + NB <= s1; s += NB) batch(s, Int<NB>{});
-  if constexpr (NB > 4)
-    if (s + 4 <= s1) { batch(s, Int<4>{}); s += 4; }
-  if constexpr (NB > 2)
-    if (s + 2 <= s1) { batch(s, Int<2>{}); s += 2; }
-  if (s < s1) batch(s, Int<1>{});
-  if (TRANS && wi == waves - 1 && len % 32) {                 // the columns behind the last whole step
-    const int64_t n = 32 * (int64_t)steps + 8 * q, left = len - n;
-    Cols8<TRANS ? RB : 1> bv;
-    bv.load(ap[0] + (int64_t)32 * steps * g.rank, g.rank, min(in_rank, (int)max(left, (int64_t)0)));
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const u32x4_t zv = left > 0 ? ld8_tail(zp[t] - 8 * q, n, len) : (u32x4_t){0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int i = 0; i < RB; ++i) acc[t][i] = mfma_bf16(bv.operand(i), zv, acc[t][i]);
     }
+    __asm__ volatile("" ::: "memory");
   }
+  __syncthreads();                                            // the images give way to the sums
+  float(*red)[U][LD] = reinterpret_cast<float(*)[U][LD]>(lds);
 #pragma unroll
   for (int w = 0; w < NW / BUF; ++w) {
     if (wave / BUF == w) {
@@ -223,17 +248,17 @@ __device__ __forceinline__ void copy_row(const LoraArgs& g, int64_t m, int64_t n
 // One block per (256 columns, group of units, or 64 rows of which those
 // without an adapter are copied): y = base + B_e h.  A wave holds 64 columns
 // of B_e in registers while its group's units have the same adapter and takes
-// their rows 16 at a time.  Lane c supplies column 32 (b / 2) + 8 (c / 4) + 4
-// (b % 2) + c % 4 to MFMA b (TRANS: column 32 (c % 4 / 2) + 8 (c / 4) + 4 (c %
-// 2) + b) and so ends up, in quarter q, with columns 8 q .. + 7 and 32 + 8 q
-// .. + 7 of row c: four lanes write 64 consecutive bytes.  Blocks go round
-// the XCDs one by one, so block id i takes columns i % 8 + 8 k: each XCD sees
+// their rows 16 at a time.  Lane c supplies column 4 c + b to MFMA b and so
+// ends up with columns 4 c .. 4 c + 3 of rows 4 q + v: sixteen lanes read base
+// and write y 128 consecutive bytes at a time (with the rows along the lanes
+// instead, 16 bytes each, the address unit bound the kernel: m = 8192, n =
+// 14336, rank 64 132 us).  Blocks go round the XCDs one by one, so block id i takes columns i % 8 + 8 k: each XCD sees
 // an eighth of B_e, which stays in its L2 from group to group.
 template <int RP, int T, bool DIRECT, bool TRANS>
 __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
   constexpr int S = RP == 16 ? 1 : RP / 16, HALF = RP == 16 ? 1 : RP / 32, U = 16 * T, LDH = 2 * RP + 8;
   __shared__ __align__(16) uint16_t hs[2][U][LDH];            // a row's h: RP values hi, RP values lo
-  __shared__ int rows[2][U];
+  __shared__ __align__(16) int rows[2][U];
   const int64_t N = TRANS ? g.K : g.N;
   const int per = (int)((N + 8 * kLoraCols - 1) / (8 * kLoraCols));       // column slabs per XCD
   const uint32_t id = blockIdx.x >> 3;
@@ -251,10 +276,11 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
     }
     return;
   }
-  const int64_t n0 = c0 + 64 * wave;
+  const int64_t n0 = c0 + 64 * wave, n = n0 + 4 * c;          // the wave's and the lane's first column
   // rank column of MFMA step s (of 32 over [hi | lo]) that quarter q supplies first; RP = 16: one step, 0-1 hi, 2-3 lo
   auto rank0 = [q](int s) { return RP == 16 ? 8 * (q & 1) : 32 * s + 8 * q; };
-  u32x4_t bv[TRANS ? 1 : 4][HALF], yv[T][2];
+  u32x4_t bv[TRANS ? 1 : 4][HALF];
+  u32x2_t yv[T][4];
   Cols8<4> cv[TRANS ? HALF : 1];
   int have = -1;
   const int u0 = DIRECT ? gi : gi * g.group, un = DIRECT ? gi + 1 : (int)min((int64_t)u0 + g.group, g.R.max_units);
@@ -270,30 +296,30 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
       if (e != have) {
         have = e;
         if constexpr (TRANS) {
-          const uint16_t* A = g.a + (int64_t)e * g.rank * g.K + n0 + 32 * ((c >> 1) & 1) + 8 * (c >> 2) + 4 * (c & 1);
+          const uint16_t* A = g.a + (int64_t)e * g.rank * g.K + n0 + 4 * c;
 #pragma unroll
           for (int s = 0; s < HALF; ++s) cv[s].load(A + (int64_t)rank0(s) * g.K, g.K, rank0(s) < g.rank ? 8 : 0);
         } else {
           const uint16_t* B = g.b + (int64_t)e * g.N * g.rank;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
-            const int64_t n = min(n0 + 32 * (b >> 1) + 8 * (c >> 2) + 4 * (b & 1) + (c & 3), N - 1);
+            const int64_t nb = min(n + b, N - 1);
 #pragma unroll
             for (int s = 0; s < HALF; ++s) {
               bv[b][s] = (u32x4_t){0u, 0u, 0u, 0u};
-              if (rank0(s) < g.rank) bv[b][s] = ld16(B + n * g.rank + rank0(s));
+              if (rank0(s) < g.rank) bv[b][s] = ld16(B + nb * g.rank + rank0(s));
             }
           }
         }
       }
 #pragma unroll
       for (int t = 0; t < T; ++t) {
-        const uint16_t* br = g.base + (int64_t)rw[min(16 * t + c, count - 1)] * N;
+        const int4 m4 = *reinterpret_cast<const int4*>(rw + 16 * t + 4 * q);
+        const int m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int64_t n = n0 + 32 * p + 8 * q;
-          yv[t][p] = (u32x4_t){0u, 0u, 0u, 0u};
-          if (g.base && n < N) yv[t][p] = ld8_tail(br, n, N);
+        for (int v = 0; v < 4; ++v) {
+          yv[t][v] = (u32x2_t){0u, 0u};
+          if (g.base && 16 * t + 4 * q + v < count && n < N) yv[t][v] = ld4_tail(g.base + (int64_t)m[v] * N, n, N);
         }
       }
     }
@@ -347,23 +373,19 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           const u32x4_t a = TRANS ? cv[TRANS ? s % HALF : 0].operand(b) : bv[TRANS ? 0 : b][s % HALF];
-          acc[b] = mfma_bf16(a, hf[s], acc[b]);
+          acc[b] = mfma_bf16(hf[s], a, acc[b]);
         }
       }
-      if (16 * t + c < count) {
-        uint16_t* yr = g.y + (int64_t)rw[16 * t + c] * N;
+      const int4 m4 = *reinterpret_cast<const int4*>(rw + 16 * t + 4 * q);
+      const int m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int64_t n = n0 + 32 * p + 8 * q;
-          u32x4_t o;
+      for (int v = 0; v < 4; ++v) {
+        if (16 * t + 4 * q + v >= count || n >= N) continue;
+        u32x2_t o;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float lo = TRANS ? acc[2 * (k & 1)][2 * p + (k >> 1)] : acc[2 * p + (k >> 1)][2 * (k & 1)];
-            const float hi = TRANS ? acc[2 * (k & 1) + 1][2 * p + (k >> 1)] : acc[2 * p + (k >> 1)][2 * (k & 1) + 1];
-            o[k] = pack_bf16(lo_bf16(yv[t][p][k]) + lo, hi_bf16(yv[t][p][k]) + hi);
-          }
-          if (n < N) st8_tail(yr, n, N, o);
-        }
+        for (int k = 0; k < 2; ++k)
+          o[k] = pack_bf16(lo_bf16(yv[t][v][k]) + acc[2 * k][v], hi_bf16(yv[t][v][k]) + acc[2 * k + 1][v]);
+        st4_tail(g.y + (int64_t)m[v] * N, n, N, o);
       }
     }
   }
@@ -382,7 +404,7 @@ template <int RP, bool TRANS>
 static void run_shrink(const LoraArgs& g, bool direct, hipStream_t st) {
   const int t = direct || g.R.unit_rows == 16 ? 1 : 2;
   const dim3 grid((unsigned)g.splits, (unsigned)(direct ? g.M : g.R.max_units * (g.R.unit_rows / (16 * t))));
-  const dim3 block(64u * (unsigned)shrink_waves(t));
+  const dim3 block(64u * (unsigned)shrink_waves(RP, t));
   if constexpr (!TRANS) {
     if (direct) hipLaunchKernelGGL((k_lora_shrink<RP, 1, true, false>), grid, block, 0, st, g);
     else if (t == 1) hipLaunchKernelGGL((k_lora_shrink<RP, 1, false, false>), grid, block, 0, st, g);

@@ -10,47 +10,50 @@
 
 namespace hm {
 
-// One block per unit: g (the splits' sums) and h of its rows as [hi, lo][rank
-// row][row of the unit], zeros beyond the rank and the unit's rows.
+// grid (units, 2): g (the splits' sums; y = 0) or h (y = 1) of a unit's rows
+// in the order of the outer product's operands, so that a wave loads each
+// with one contiguous access: [32-row step][hi, lo][16-rank block][lane][8],
+// lane (c, q) holding rank 16 k + c of rows 32 s + 8 q .. + 7; zeros beyond
+// the rank and the unit's rows.
 template <int RP>
 __global__ void __launch_bounds__(256) k_lora_pack(LoraGradArgs g) {
   __shared__ float v[kLoraUnit][RP + 1];
   const int u = blockIdx.x, count = g.R.units[2 * u + 1];
+  const bool is_h = blockIdx.y != 0;
   if (count == 0) return;
   const int32_t* rows = g.R.rows + (int64_t)u * kLoraUnit;
-  for (int which = 0; which < 2; ++which) {
-    for (int i = threadIdx.x; i < kLoraUnit * (RP / 4); i += 256) {
-      const int row = i / (RP / 4), r = 4 * (i % (RP / 4));
-      f32x4_t s = {0.f, 0.f, 0.f, 0.f};
-      if (row < count && r < g.rank) {
-        const int64_t at = (int64_t)rows[row] * g.rank + r;
-        if (which) {
-          s = *reinterpret_cast<const f32x4_t*>(g.h + at);
-        } else {
-#pragma unroll 4
-          for (int k = 0; k < g.splits; ++k)
-            s += *reinterpret_cast<const f32x4_t*>(g.part + (int64_t)k * g.M * g.rank + at);
-        }
-      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[row][r + k] = s[k];
-    }
-    __syncthreads();
-    uint16_t* out = (which ? g.ht : g.gt) + (int64_t)u * 2 * RP * kLoraUnit;
-    for (int i = threadIdx.x; i < RP * (kLoraUnit / 8); i += 256) {
-      const int r = i / (kLoraUnit / 8), m = 8 * (i % (kLoraUnit / 8));
-      u32x4_t hi, lo;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t h2, l2;
-        split2(v[m + 2 * k][r], v[m + 2 * k + 1][r], &h2, &l2);
-        hi[k] = h2;
-        lo[k] = l2;
+  for (int i0 = 0; i0 < kLoraUnit * (RP / 4); i0 += 256) {
+    const int i = i0 + threadIdx.x, row = i / (RP / 4), r = 4 * (i % (RP / 4));
+    f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+    if (row < count && r < g.rank) {
+      const int64_t at = (int64_t)rows[row] * g.rank + r;
+      if (is_h) {
+        s = *reinterpret_cast<const f32x4_t*>(g.h + at);
+      } else {
+        for (int k = 0; k < g.splits; ++k)
+          s += *reinterpret_cast<const f32x4_t*>(g.part + (int64_t)k * g.M * g.rank + at);
       }
-      st16(out + r * kLoraUnit + m, hi);
-      st16(out + (RP + r) * kLoraUnit + m, lo);
     }
-    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[row][r + k] = s[k];
+  }
+  __syncthreads();
+  uint16_t* out = (is_h ? g.ht : g.gt) + (int64_t)u * 2 * RP * kLoraUnit;
+  for (int i = threadIdx.x; i < RP * (kLoraUnit / 8); i += 256) {
+    const int lane = i & 63, k = (i >> 6) % (RP / 16), s = (i >> 6) / (RP / 16);
+    const int r = 16 * k + (lane & 15), m = 32 * s + 8 * (lane >> 4);
+    u32x4_t hi, lo;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      uint32_t h2, l2;
+      split2(v[m + 2 * p][r], v[m + 2 * p + 1][r], &h2, &l2);
+      hi[p] = h2;
+      lo[p] = l2;
+    }
+    uint16_t* o = out + s * (2 * RP * 32) + (k * 64 + lane) * 8;
+    st16(o, hi);
+    st16(o + RP * 32, lo);
   }
 }
 
@@ -69,7 +72,7 @@ __device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, fl
   const int64_t n = db ? g.N : g.K;
   const uint16_t* z = db ? g.dy : g.x;
   const int r00 = blockIdx.z * RC;
-  const uint16_t* f = (db ? g.ht : g.gt) + r00 * kLoraUnit;
+  const uint16_t* f = (db ? g.ht : g.gt) + r00 * 32 + 8 * (threadIdx.x & 63);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
   const int per = chunk_units(g), lo_u = blockIdx.y * per, hi_u = min(lo_u + per, g.R.first[g.L]);
   const int64_t col = k0 + 8 * c;
@@ -86,11 +89,11 @@ __device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, fl
       const int32_t* rows = g.R.rows + (int64_t)u * kLoraUnit + first;
       Cols8<8> zv;
       u32x4_t fh[RB], fl[RB];
-      const uint16_t* fu = f + ((int64_t)u * 2 * RP + c) * kLoraUnit + first + 8 * q;
+      const uint16_t* fu = f + (int64_t)s * 2 * RP * 32;
 #pragma unroll
       for (int k = 0; k < RB; ++k) {
-        fh[k] = ld16(fu + 16 * k * kLoraUnit);
-        fl[k] = ld16(fu + (RP + 16 * k) * kLoraUnit);
+        fh[k] = ld16(fu + 512 * k);
+        fl[k] = ld16(fu + RP * 32 + 512 * k);
       }
       // rows behind the unit's last repeat its first: their g and h are 0
 #pragma unroll
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(256) k_lora_sums(LoraGradArgs g) {
 }
 
 hipError_t launch_lora_pack(const LoraGradArgs& g, hipStream_t st) {
-  const dim3 grid((unsigned)g.R.max_units);
+  const dim3 grid((unsigned)g.R.max_units, 2);
   switch (lora_rp(g.rank)) {
     case 16: hipLaunchKernelGGL(k_lora_pack<16>, grid, dim3(256), 0, st, g); break;
     case 32: hipLaunchKernelGGL(k_lora_pack<32>, grid, dim3(256), 0, st, g); break;

@@ -50,7 +50,7 @@ struct LoraGradArgs {
   int splits;
   int64_t M, N, K;
   int rank, L;
-  uint16_t *gt, *ht;         // packed g and h: [unit][2 (hi, lo)][RP][kLoraUnit]
+  uint16_t *gt, *ht;         // packed g and h, 2 RP kLoraUnit values a unit (k_lora_pack)
   float* sums;               // partial sums [2 chunks][rank (K + N)]
   int chunks;
   uint16_t *da, *db;

@@ -34,6 +34,26 @@ __device__ __forceinline__ void st8_tail(uint16_t* row, int64_t c, int64_t n, u3
     if (c + e < n) row[c + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
 }
 
+// The same four values at a time.
+typedef u32x2_t u32x2_any_t __attribute__((aligned(2)));
+__device__ __forceinline__ u32x2_t ld4_tail(const uint16_t* row, int64_t c, int64_t n) {
+  if (c + 4 <= n) return *reinterpret_cast<const u32x2_any_t*>(row + c);
+  u32x2_t v = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c + e < n) v[e >> 1] |= (uint32_t)row[c + e] << (16 * (e & 1));
+  return v;
+}
+__device__ __forceinline__ void st4_tail(uint16_t* row, int64_t c, int64_t n, u32x2_t v) {
+  if (c + 4 <= n) {
+    *reinterpret_cast<u32x2_any_t*>(row + c) = v;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c + e < n) row[c + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+}
+
 // xs[positions[p]] = x[p / topk] for positions in [0, t topk)
 hipError_t launch_dispatch_rows(const uint16_t* x, const int32_t* positions, int64_t t, int topk, int64_t n,
                                 uint16_t* xs, hipStream_t st);
