@@ -146,8 +146,10 @@ def _ptr(t):
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the handle alone: building torch's Stream object takes 2.7 us of a call's 3 us launch
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _ok(fn, code):
@@ -415,19 +417,20 @@ def _other(dev, stream):
         yield
 
 
-def _on(t, stream):
-    """Context in which t's device and `stream` are the current ones."""
+def _elsewhere(t, stream):
+    """None where t's device is the current one and `stream` None; else a
+    context that makes t's device and `stream` the current ones."""
     if not t.is_cuda:
         raise ValueError("need CUDA tensors")
-    if stream is not None and stream.device != t.device:
+    if stream is None:
+        return None if t.get_device() == torch.cuda.current_device() else _other(t.device, None)
+    if stream.device != t.device:
         raise ValueError("stream: of another device than the tensors")
-    if stream is None and t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
     return _other(t.device, stream)
 
 
 def _arg(t, dtype, shape, name, dev):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shape} on {dev}")
     return t
 
@@ -436,11 +439,12 @@ def _out(t, dtype, shape, name, dev):
     return torch.empty(shape, dtype=dtype, device=dev) if t is None else _arg(t, dtype, shape, name, dev)
 
 
-def _ws(ws, need, dev):
+def _ws(ws, size, args, dev):
     """(pointer, bytes) of a workspace: the caller's as it is (the library
-    checks its size), or one allocated here when `need` is not 0.  Also the
-    tensor, which must live until the launch."""
+    checks its size), or one of size(*args) bytes allocated here when that is
+    not 0.  Also the tensor, which must live until the launch."""
     if ws is None:
+        need = size(*args)
         if need == 0:
             return None, 0, None
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -463,48 +467,56 @@ def hm_moe_dispatch(x, topk_ids, num_experts, xs=None, counts=None, offsets=None
     positions [t, topk]).  Rows of xs and entries of sorted_pairs from
     offsets[E] on (as many as ids lie outside [0, E)) are left as they were:
     uninitialised when allocated here."""
-    with _on(x, stream):
-        (t, n), topk, dev, i32 = x.shape, topk_ids.shape[1], x.device, torch.int32
-        _arg(x, torch.bfloat16, (t, n), "x", dev)
-        _arg(topk_ids, i32, (t, topk), "topk_ids", dev)
-        E = int(num_experts)
-        need = hm_moe_dispatch_workspace_size(t, topk, E)
-        xs = _out(xs, torch.bfloat16, (t * topk, n), "xs", dev)
-        counts = _out(counts, i32, (E,), "counts", dev)
-        offsets = _out(offsets, i32, (E + 1,), "offsets", dev)
-        sorted_pairs = _out(sorted_pairs, i32, (t * topk,), "sorted_pairs", dev)
-        positions = _out(positions, i32, (t, topk), "positions", dev)
-        wsp, wsb, ws = _ws(ws, need, dev)
-        _ok("hm_moe_dispatch", lib.hm_moe_dispatch(_ptr(x), _ptr(topk_ids), t, topk, E, n, _ptr(xs), _ptr(counts),
-                                                   _ptr(offsets), _ptr(sorted_pairs), _ptr(positions), wsp, wsb,
-                                                   _stream(stream)))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_moe_dispatch(x, topk_ids, num_experts, xs, counts, offsets, sorted_pairs, positions, ws)
+    (t, n), topk, dev, i32 = x.shape, topk_ids.shape[1], x.device, torch.int32
+    _arg(x, torch.bfloat16, (t, n), "x", dev)
+    _arg(topk_ids, i32, (t, topk), "topk_ids", dev)
+    E = int(num_experts)
+    xs = _out(xs, torch.bfloat16, (t * topk, n), "xs", dev)
+    counts = _out(counts, i32, (E,), "counts", dev)
+    offsets = _out(offsets, i32, (E + 1,), "offsets", dev)
+    sorted_pairs = _out(sorted_pairs, i32, (t * topk,), "sorted_pairs", dev)
+    positions = _out(positions, i32, (t, topk), "positions", dev)
+    wsp, wsb, ws = _ws(ws, hm_moe_dispatch_workspace_size, (t, topk, E), dev)
+    _ok("hm_moe_dispatch", lib.hm_moe_dispatch(_ptr(x), _ptr(topk_ids), t, topk, E, n, _ptr(xs), _ptr(counts),
+                                               _ptr(offsets), _ptr(sorted_pairs), _ptr(positions), wsp, wsb,
+                                               _stream()))
     return xs, counts, offsets, sorted_pairs, positions
 
 
 def hm_moe_dispatch_grad(dxs, positions, dx=None, stream=None):
     """dxs bf16 [t*topk, n], positions int32 [t, topk] -> dx bf16 [t, n]: each
     token's sum over its routed rows."""
-    with _on(dxs, stream):
-        (t, topk), n, dev = positions.shape, dxs.shape[1], dxs.device
-        _arg(dxs, torch.bfloat16, (t * topk, n), "dxs", dev)
-        _arg(positions, torch.int32, (t, topk), "positions", dev)
-        dx = _out(dx, torch.bfloat16, (t, n), "dx", dev)
-        _ok("hm_moe_dispatch_grad", lib.hm_moe_dispatch_grad(_ptr(dxs), _ptr(positions), t, topk, n, _ptr(dx),
-                                                             _stream(stream)))
+    ctx = _elsewhere(dxs, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_moe_dispatch_grad(dxs, positions, dx)
+    (t, topk), n, dev = positions.shape, dxs.shape[1], dxs.device
+    _arg(dxs, torch.bfloat16, (t * topk, n), "dxs", dev)
+    _arg(positions, torch.int32, (t, topk), "positions", dev)
+    dx = _out(dx, torch.bfloat16, (t, n), "dx", dev)
+    _ok("hm_moe_dispatch_grad", lib.hm_moe_dispatch_grad(_ptr(dxs), _ptr(positions), t, topk, n, _ptr(dx),
+                                                         _stream(stream)))
     return dx
 
 
 def hm_moe_collect(ys, weights, positions, out=None, stream=None):
     """ys bf16 [t*topk, n] in expert order, weights fp32 [t, topk], positions
     int32 [t, topk] -> out bf16 [t, n]: each token's weighted sum."""
-    with _on(ys, stream):
-        (t, topk), n, dev = positions.shape, ys.shape[1], ys.device
-        _arg(ys, torch.bfloat16, (t * topk, n), "ys", dev)
-        _arg(weights, torch.float32, (t, topk), "weights", dev)
-        _arg(positions, torch.int32, (t, topk), "positions", dev)
-        out = _out(out, torch.bfloat16, (t, n), "out", dev)
-        _ok("hm_moe_collect", lib.hm_moe_collect(_ptr(ys), _ptr(weights), _ptr(positions), t, topk, n, _ptr(out),
-                                                 _stream(stream)))
+    ctx = _elsewhere(ys, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_moe_collect(ys, weights, positions, out)
+    (t, topk), n, dev = positions.shape, ys.shape[1], ys.device
+    _arg(ys, torch.bfloat16, (t * topk, n), "ys", dev)
+    _arg(weights, torch.float32, (t, topk), "weights", dev)
+    _arg(positions, torch.int32, (t, topk), "positions", dev)
+    out = _out(out, torch.bfloat16, (t, n), "out", dev)
+    _ok("hm_moe_collect", lib.hm_moe_collect(_ptr(ys), _ptr(weights), _ptr(positions), t, topk, n, _ptr(out),
+                                             _stream(stream)))
     return out
 
 
@@ -512,18 +524,21 @@ def hm_moe_collect_grad(dout, ys, weights, positions, dys=None, dweights=None, s
     """Gradient of hm_moe_collect: dout bf16 [t, n] -> (dys bf16 [t*topk, n],
     dweights fp32 [t, topk]).  Rows of dys that no position names are left as
     they were (zeros when allocated here).  dys may be ys."""
-    with _on(dout, stream):
-        (t, topk), n, dev = positions.shape, dout.shape[1], dout.device
-        _arg(dout, torch.bfloat16, (t, n), "dout", dev)
-        _arg(ys, torch.bfloat16, (t * topk, n), "ys", dev)
-        _arg(weights, torch.float32, (t, topk), "weights", dev)
-        _arg(positions, torch.int32, (t, topk), "positions", dev)
-        if dys is None:
-            dys = torch.zeros(t * topk, n, dtype=torch.bfloat16, device=dev)
-        _arg(dys, torch.bfloat16, (t * topk, n), "dys", dev)
-        dweights = _out(dweights, torch.float32, (t, topk), "dweights", dev)
-        _ok("hm_moe_collect_grad", lib.hm_moe_collect_grad(_ptr(dout), _ptr(ys), _ptr(weights), _ptr(positions), t,
-                                                           topk, n, _ptr(dys), _ptr(dweights), _stream(stream)))
+    ctx = _elsewhere(dout, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_moe_collect_grad(dout, ys, weights, positions, dys, dweights)
+    (t, topk), n, dev = positions.shape, dout.shape[1], dout.device
+    _arg(dout, torch.bfloat16, (t, n), "dout", dev)
+    _arg(ys, torch.bfloat16, (t * topk, n), "ys", dev)
+    _arg(weights, torch.float32, (t, topk), "weights", dev)
+    _arg(positions, torch.int32, (t, topk), "positions", dev)
+    if dys is None:
+        dys = torch.zeros(t * topk, n, dtype=torch.bfloat16, device=dev)
+    _arg(dys, torch.bfloat16, (t * topk, n), "dys", dev)
+    dweights = _out(dweights, torch.float32, (t, topk), "dweights", dev)
+    _ok("hm_moe_collect_grad", lib.hm_moe_collect_grad(_ptr(dout), _ptr(ys), _ptr(weights), _ptr(positions), t,
+                                                       topk, n, _ptr(dys), _ptr(dweights), _stream(stream)))
     return dys, dweights
 
 
@@ -559,17 +574,19 @@ def hm_lora(desc, x, adapter_ids, a, b, scales, base=None, y=None, h=None, ws=No
     [m, n] = base + scale * B (A x) per row; base bf16 [m, n] (hm_gemm's
     output) or None for zeros, and may be y (in place).  h: an fp32 [m, rank]
     tensor to keep scale * A x in for hm_lora_grad."""
-    with _on(x, stream):
-        m, dev = _lora_common(desc, x, adapter_ids, a, b, scales)
-        if base is not None:
-            _arg(base, torch.bfloat16, (m, desc.n), "base", dev)
-        if h is not None:
-            _arg(h, torch.float32, (m, desc.rank), "h", dev)
-        need = hm_lora_workspace_size(desc, m)
-        y = _out(y, torch.bfloat16, (m, desc.n), "y", dev)
-        wsp, wsb, ws = _ws(ws, need, dev)
-        _ok("hm_lora", lib.hm_lora(ctypes.byref(desc), _ptr(x), _ptr(adapter_ids), _ptr(a), _ptr(b), _ptr(scales), m,
-                                   _ptr(base), _ptr(y), _ptr(h), wsp, wsb, _stream(stream)))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_lora(desc, x, adapter_ids, a, b, scales, base, y, h, ws)
+    m, dev = _lora_common(desc, x, adapter_ids, a, b, scales)
+    if base is not None:
+        _arg(base, torch.bfloat16, (m, desc.n), "base", dev)
+    if h is not None:
+        _arg(h, torch.float32, (m, desc.rank), "h", dev)
+    y = _out(y, torch.bfloat16, (m, desc.n), "y", dev)
+    wsp, wsb, ws = _ws(ws, hm_lora_workspace_size, (desc, m), dev)
+    _ok("hm_lora", lib.hm_lora(ctypes.byref(desc), _ptr(x), _ptr(adapter_ids), _ptr(a), _ptr(b), _ptr(scales), m,
+                               _ptr(base), _ptr(y), _ptr(h), wsp, wsb, _stream(stream)))
     return y
 
 
@@ -579,25 +596,27 @@ def hm_lora_grad(desc, dy, x, h, adapter_ids, a, b, scales, dx_base=None, dx=Non
     (dx bf16 [m, k] or None, da bf16 [L, rank, k], db bf16 [L, n, rank]).
     dx_base bf16 [m, k]: the gradient through the shared projection, added to
     dx (may be dx); need_dx=False leaves dx out."""
-    with _on(x, stream):
-        m, dev = _lora_common(desc, x, adapter_ids, a, b, scales)
-        bf = torch.bfloat16
-        _arg(dy, bf, (m, desc.n), "dy", dev)
-        _arg(h, torch.float32, (m, desc.rank), "h", dev)
-        if dx_base is not None:
-            _arg(dx_base, bf, (m, desc.k), "dx_base", dev)
-        if not need_dx:
-            if dx is not None or dx_base is not None:
-                raise ValueError("need_dx=False takes neither dx nor dx_base")
-        else:
-            dx = _out(dx, bf, (m, desc.k), "dx", dev)
-        need = hm_lora_grad_workspace_size(desc, m)
-        da = _out(da, bf, (desc.num_adapters, desc.rank, desc.k), "da", dev)
-        db = _out(db, bf, (desc.num_adapters, desc.n, desc.rank), "db", dev)
-        wsp, wsb, ws = _ws(ws, need, dev)
-        _ok("hm_lora_grad", lib.hm_lora_grad(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(h), _ptr(adapter_ids), _ptr(a),
-                                             _ptr(b), _ptr(scales), m, _ptr(dx_base), _ptr(dx), _ptr(da), _ptr(db),
-                                             wsp, wsb, _stream(stream)))
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_lora_grad(desc, dy, x, h, adapter_ids, a, b, scales, dx_base, dx, da, db, need_dx, ws)
+    m, dev = _lora_common(desc, x, adapter_ids, a, b, scales)
+    bf = torch.bfloat16
+    _arg(dy, bf, (m, desc.n), "dy", dev)
+    _arg(h, torch.float32, (m, desc.rank), "h", dev)
+    if dx_base is not None:
+        _arg(dx_base, bf, (m, desc.k), "dx_base", dev)
+    if not need_dx:
+        if dx is not None or dx_base is not None:
+            raise ValueError("need_dx=False takes neither dx nor dx_base")
+    else:
+        dx = _out(dx, bf, (m, desc.k), "dx", dev)
+    da = _out(da, bf, (desc.num_adapters, desc.rank, desc.k), "da", dev)
+    db = _out(db, bf, (desc.num_adapters, desc.n, desc.rank), "db", dev)
+    wsp, wsb, ws = _ws(ws, hm_lora_grad_workspace_size, (desc, m), dev)
+    _ok("hm_lora_grad", lib.hm_lora_grad(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(h), _ptr(adapter_ids), _ptr(a),
+                                         _ptr(b), _ptr(scales), m, _ptr(dx_base), _ptr(dx), _ptr(da), _ptr(db),
+                                         wsp, wsb, _stream(stream)))
     return dx, da, db
 
 

@@ -30,11 +30,16 @@ hm_status check_lora(const hm_lora_desc* d, int64_t m) {
 // Blocks of one launch stay under 2^24 (2^32 threads).
 constexpr int64_t kMaxBlocks = (1ll << 24) - 1;
 
+// Largest A (values) that every block of a call reads by itself.
+constexpr int64_t kSmallA = 131072;
+constexpr int64_t kSmallRows = 16;
+
 // Byte offsets in the workspace (total a multiple of 256) and launch shape.
 struct LoraPlan {
   size_t units, rows, first, part, gt, ht, sums, total;
   int64_t max_units;
-  int unit_rows, splits, group, chunks;
+  int unit_rows, splits, group, cols, chunks;
+  int parts;                 // column parts of the one-launch kernel, 0: not taken
   bool direct;
 };
 
@@ -49,15 +54,29 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
   w.direct = !grad && m <= kLoraDirect;
   w.unit_rows = grad ? kLoraUnit : (w.direct ? 16 : rows_per_unit(m, L));
   w.max_units = w.direct ? m : m / w.unit_rows + std::min<int64_t>(L, m);
-  // blocks along the contraction: about 1024 blocks of four waves (16-row
-  // units) or 512 of eight in all, each wave keeping two steps of 32 or more
-  const int64_t blocks = w.unit_rows == 16 ? w.max_units : w.max_units * (w.unit_rows / 32);
-  const int64_t want = w.unit_rows == 16 ? 1024 / blocks : 512 / blocks;
-  const int64_t most = std::min<int64_t>(w.unit_rows == 16 ? kLoraMaxSplits : 4, len / (w.unit_rows == 16 ? 128 : 512));
+  // blocks along the contraction: about 4096 waves in all (16-row units) or
+  // 640 blocks (32-row blocks), each wave keeping a step of 64 or more
+  const bool few = w.unit_rows == 16;
+  const int rp = lora_rp(d->rank);
+  const int64_t blocks = few ? w.max_units : w.max_units * (w.unit_rows / 32), waves = few ? (rp == 128 ? 4 : (rp == 64 ? 8 : 16)) : 4;
+  const int64_t want = few ? 4096 / (blocks * waves) : 640 / blocks, most = std::min<int64_t>(rp == 128 && few ? 8 : 4, len / (64 * waves));
   w.splits = (int)std::max<int64_t>(1, std::min(want, most));
-  const int64_t slabs = 8 * ((cols + 8 * kLoraCols - 1) / (8 * kLoraCols));
+  // expanding blocks: several units against one part of B where there are many, several parts of the columns where
+  // there are many units of few rows
+  int64_t slabs = 8 * ((cols + 8 * kLoraCols - 1) / (8 * kLoraCols));
   w.group = w.direct || w.unit_rows < 64 ? 1 : (w.max_units * slabs >= 4096 ? 4 : (w.max_units * slabs >= 2048 ? 2 : 1));
+  w.cols = kLoraCols;
+  while (few && w.max_units * slabs > 1024 && w.cols < 4 * kLoraCols && cols > 8 * w.cols) {
+    w.cols *= 2;
+    slabs = 8 * ((cols + 8 * w.cols - 1) / (8 * w.cols));
+  }
   if (slabs * ((w.max_units + w.group - 1) / w.group + (m + 63) / 64) > kMaxBlocks) return HM_ERR_SHAPE;
+  if (!grad && m <= kSmallRows && d->rank <= 64 && (int64_t)lora_rp(d->rank) * d->k <= kSmallA) {
+    const int64_t waves = d->rank > 32 ? 8 : 16, most = (d->n + 64 * waves - 1) / (64 * waves);
+    w.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, 256 / m));
+    *out = w;
+    return HM_OK;
+  }
   size_t at = 0;
   auto take = [&at](size_t bytes) {
     const size_t o = at;
@@ -120,6 +139,7 @@ LoraArgs args_of(const hm_lora_desc* d, const uint16_t* z, const int32_t* ids, c
   g.part = (float*)(ws + w.part);
   g.splits = w.splits;
   g.group = w.group;
+  g.cols = w.cols;
   return g;
 }
 
@@ -140,11 +160,14 @@ HM_API hm_status hm_lora(const hm_lora_desc* d, const uint16_t* x, const int32_t
     return HM_ERR_ALIGN;
   LoraPlan w;
   if (hm_status s = plan_lora(d, m, false, &w)) return s;
-  if (!ws) return HM_ERR_NULL;
-  if (ws_bytes < w.total) return HM_ERR_WORKSPACE;
-  if (!aligned(ws, 256)) return HM_ERR_ALIGN;
+  if (w.total) {
+    if (!ws) return HM_ERR_NULL;
+    if (ws_bytes < w.total) return HM_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return HM_ERR_ALIGN;
+  }
   LoraArgs g = args_of(d, x, adapter_ids, a, b, scales, m, base, y, w, (uint8_t*)ws);
   g.h = h;
+  if (w.parts) return launch_lora_small(g, w.parts, stream) == hipSuccess ? HM_OK : HM_ERR_HIP;
   if (h && w.splits == 1) g.part = h;
   hipError_t e = w.direct ? hipSuccess : group_rows(d, adapter_ids, m, w, (uint8_t*)ws, &g.R, stream);
   if (e == hipSuccess) e = launch_lora_shrink(g, w.direct, false, stream);

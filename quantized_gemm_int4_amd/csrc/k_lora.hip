@@ -22,16 +22,20 @@ namespace hm {
 // chunk without a pass in between; block 0 writes the units.  Counting is
 // cheap next to the call (4 bytes a row and block, at most kLoraPlanBlocks
 // blocks, against rows of thousands of bytes) and a second launch is not.
+// A row's place within 1024 rows is its rank among its wave's equal ids, by
+// matching ballots, after the counts of the waves before.
 __global__ void __launch_bounds__(kSortThreads)
 k_lora_plan(const int32_t* __restrict__ ids, int64_t M, int L, int64_t C, int U, int64_t max_units,
             int32_t* __restrict__ units, int32_t* __restrict__ rows, int32_t* __restrict__ firsts) {
   __shared__ int hist[kSortWaves][512];
   __shared__ int before[512], after[512], base[512], uend[512];
   __shared__ int wsum[8];
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t lo = (int64_t)blockIdx.x * C, hi = min(lo + C, M);       // C is a multiple of kSortThreads
+  int own = lo + tid < hi ? ids[lo + tid] : -1;
   for (int i = tid; i < 512; i += kSortThreads) before[i] = after[i] = 0;
+  for (int i = tid; i < kSortWaves * 512; i += kSortThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  const int64_t lo = (int64_t)blockIdx.x * C, hi = min(lo + C, M);
   for (int64_t p0 = 0; p0 < M; p0 += 8 * kSortThreads) {
     int id[8];
 #pragma unroll
@@ -41,7 +45,7 @@ k_lora_plan(const int32_t* __restrict__ ids, int64_t M, int L, int64_t C, int U,
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      int* cnt = p0 + i * kSortThreads < lo ? before : after; // C is a multiple of kSortThreads
+      int* cnt = p0 + i * kSortThreads < lo ? before : after;
       const int e = id[i];
       const bool ok = e >= 0 && e < L;
       const uint64_t m = __ballot(ok);
@@ -76,7 +80,33 @@ k_lora_plan(const int32_t* __restrict__ ids, int64_t M, int L, int64_t C, int U,
       units[2 * u + 1] = used ? min(before[e] + after[e] - i * U, U) : 0;
     }
   }
-  sort_range<false>(ids, lo, hi, L, base, hist, rows, nullptr);
+  int nbits = 0;
+  while ((1 << nbits) < L) ++nbits;
+  const uint64_t lt = lane ? (~0ull >> (64 - lane)) : 0ull;
+  for (int64_t p0 = lo; p0 < hi; p0 += kSortThreads) {
+    const int e = own;
+    const bool ok = e >= 0 && e < L;
+    if (p0 + kSortThreads < hi) own = p0 + kSortThreads + tid < hi ? ids[p0 + kSortThreads + tid] : -1;
+    uint64_t m = __ballot(ok);
+    for (int bit = 0; bit < nbits; ++bit) {
+      const uint64_t x = __ballot(ok && ((e >> bit) & 1));
+      m &= ((e >> bit) & 1) ? x : ~x;
+    }
+    const int rank = __popcll(m & lt);
+    if (ok && rank == 0) hist[wave][e] = __popcll(m);
+    __syncthreads();
+    int at = ok ? base[e] + rank : 0;
+    if (ok)
+      for (int w = 0; w < wave; ++w) at += hist[w][e];
+    if (ok) rows[at] = (int32_t)(p0 + tid);
+    if (p0 + kSortThreads >= hi) break;
+    __syncthreads();
+    if (ok && rank == 0) {
+      atomicAdd(&base[e], __popcll(m));
+      hist[wave][e] = 0;
+    }
+    __syncthreads();
+  }
 }
 
 // Rows first .. first + U - 1 of unit u: its adapter, and those rows in LDS.
@@ -99,16 +129,49 @@ __device__ __forceinline__ int find_unit(const LoraArgs& g, int u, int first, in
     __syncthreads();
     return min(__popcll(m) - before, 16);
   } else {
+    // the unit's slots are read with its head, not after it; those behind its count are not used
+    if (threadIdx.x < U) rows[threadIdx.x] = g.R.rows[(int64_t)u * g.R.unit_rows + first + threadIdx.x];
     *e = g.R.units[2 * u];
     const int count = min(g.R.units[2 * u + 1] - first, U);
-    if ((int)threadIdx.x < count) rows[threadIdx.x] = g.R.rows[(int64_t)u * g.R.unit_rows + first + threadIdx.x];
     __syncthreads();
     return count;
   }
 }
 
+// 64 columns of B (rows of `rank` values, contiguous) through a wave's LDS
+// image: whole lines are loaded and each MFMA's operand (lane (c, q): column 4
+// c + b, rank values 32 s + 8 q ..) is read back from there.  Column 4 c + b
+// has slot 16 b + c, whose 16-byte parts are rotated so that sixteen lanes'
+// reads spread over the banks.
+template <int RP> struct BGroup {
+  static constexpr int P = RP / 8, BYTES = 64 * RP * 2;
+  u32x4_t v[P];
+  __device__ __forceinline__ void load(const uint16_t* B, int64_t n0, int64_t N, int rank, int lane) {
+    const int per = rank / 8;
+    const int64_t last = N * per - 1;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (i < per) v[i] = ld16(B + 8 * min(n0 * per + i * 64 + lane, last));
+  }
+  __device__ static int place(int slot, int part) { return (slot * P + ((part + slot * P / 16) & (P - 1))) * 16; }
+  __device__ __forceinline__ void store(uint8_t* img, int rank, int lane) const {
+    const int per = rank / 8;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (i < per) {
+        const int ch = i * 64 + lane, col = ch / per;
+        st16(img + place(16 * (col & 3) + (col >> 2), ch - col * per), v[i]);
+      }
+    __asm__ volatile("" ::: "memory");                        // a wave's LDS accesses stay in order
+  }
+  // part: r0 / 8 of the operand's first rank value
+  __device__ __forceinline__ static u32x4_t operand(const uint8_t* img, int b, int c, int part, int rank) {
+    return 8 * part < rank ? ld16(img + place(16 * b + c, part)) : (u32x4_t){0u, 0u, 0u, 0u};
+  }
+};
+
 // Waves of a contracting block.
-constexpr int shrink_waves(int rp, int t) { return t == 1 || rp == 128 ? 4 : 8; }
+constexpr int shrink_waves(int rp, int t) { return t > 1 || rp == 128 ? 4 : (rp == 64 ? 8 : 16); }
 
 // A wave's private LDS image of 64 values of 16 rows: row r's 16-byte chunk k
 // (0 .. 7) sits at place k ^ (r & 7) of its 128 bytes, so that both the
@@ -245,7 +308,38 @@ __device__ __forceinline__ void copy_row(const LoraArgs& g, int64_t m, int64_t n
     for (int r = lane; r < g.rank; r += 64) g.h[m * g.rank + r] = 0.f;
 }
 
-// One block per (256 columns, group of units, or 64 rows of which those
+// Those of rows m0 .. m0 + 63 that have no adapter, columns [c0, c1); a block
+// of 256 threads.  list: 64 ints of LDS.  Eight rows of 256 columns at a time,
+// two loads in flight a thread.
+__device__ __forceinline__ void copy_rest(const LoraArgs& g, int64_t m0, int64_t n, int64_t c0, int64_t c1, bool zero_h,
+                                          int* list) {
+  const int lane = threadIdx.x & 63;
+  const bool in = m0 + lane < g.M;
+  const int e = in ? g.ids[m0 + lane] : 0;
+  const bool none = in && (e < 0 || e >= g.L);
+  const uint64_t m = __ballot(none);
+  const int count = __popcll(m);
+  if (count == 0) return;
+  if (threadIdx.x < 64 && none) list[__popcll(m & (lane ? (~0ull >> (64 - lane)) : 0ull))] = lane;
+  __syncthreads();
+  if (g.base != g.y)
+    for (int64_t cb = c0 + 8 * (threadIdx.x & 31); cb < c1; cb += 256)
+      for (int i = threadIdx.x >> 5; i < count; i += 16) {
+        u32x4_t v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          v[k] = (u32x4_t){0u, 0u, 0u, 0u};
+          if (g.base && i + 8 * k < count) v[k] = ld8_tail(g.base + (m0 + list[i + 8 * k]) * n, cb, n);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (i + 8 * k < count) st8_tail(g.y + (m0 + list[i + 8 * k]) * n, cb, n, v[k]);
+      }
+  if (zero_h)
+    for (int i = threadIdx.x; i < count * g.rank; i += 256) g.h[(m0 + list[i / g.rank]) * g.rank + i % g.rank] = 0.f;
+}
+
+// One block per (cols columns, group of units, or 64 rows of which those
 // without an adapter are copied): y = base + B_e h.  A wave holds 64 columns
 // of B_e in registers while its group's units have the same adapter and takes
 // their rows 16 at a time.  Lane c supplies column 4 c + b to MFMA b and so
@@ -257,26 +351,22 @@ __device__ __forceinline__ void copy_row(const LoraArgs& g, int64_t m, int64_t n
 template <int RP, int T, bool DIRECT, bool TRANS>
 __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
   constexpr int S = RP == 16 ? 1 : RP / 16, HALF = RP == 16 ? 1 : RP / 32, U = 16 * T, LDH = 2 * RP + 8;
-  __shared__ __align__(16) uint16_t hs[2][U][LDH];            // a row's h: RP values hi, RP values lo
-  __shared__ __align__(16) int rows[2][U];
+  constexpr int HB = T < 4 ? 1 : 2;                           // units of fewer rows come one to a block
+  __shared__ __align__(16) uint16_t hs[HB][U][LDH];           // a row's h: RP values hi, RP values lo
+  __shared__ __align__(16) int rows[2][U < 32 ? 32 : U];      // 64 in all: copy_rest's list
   const int64_t N = TRANS ? g.K : g.N;
-  const int per = (int)((N + 8 * kLoraCols - 1) / (8 * kLoraCols));       // column slabs per XCD
+  const int per = (int)((N + 8 * g.cols - 1) / (8 * g.cols));             // column slabs per XCD
   const uint32_t id = blockIdx.x >> 3;
   const int gi = (int)(id / per), slab = (int)(blockIdx.x & 7) + 8 * (int)(id % per);
-  const int64_t c0 = (int64_t)slab * kLoraCols, c1 = min(c0 + kLoraCols, N);
+  const int64_t c0 = (int64_t)slab * g.cols, c1 = min(c0 + g.cols, N);
   if (c0 >= N) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
   const bool keep = !TRANS && g.h && slab == 0;
   const int groups = DIRECT ? (int)g.M : (int)((g.R.max_units + g.group - 1) / g.group);
   if (!DIRECT && gi >= groups) {
-    const int64_t m0 = (int64_t)(gi - groups) * 64;
-    for (int64_t m = m0 + wave; m < min(m0 + 64, g.M); m += 4) {
-      const int e = g.ids[m];
-      if (e < 0 || e >= g.L) copy_row(g, m, N, c0, c1, keep);
-    }
+    copy_rest(g, (int64_t)(gi - groups) * 64, N, c0, c1, keep, rows[0]);
     return;
   }
-  const int64_t n0 = c0 + 64 * wave, n = n0 + 4 * c;          // the wave's and the lane's first column
   // rank column of MFMA step s (of 32 over [hi | lo]) that quarter q supplies first; RP = 16: one step, 0-1 hi, 2-3 lo
   auto rank0 = [q](int s) { return RP == 16 ? 8 * (q & 1) : 32 * s + 8 * q; };
   u32x4_t bv[TRANS ? 1 : 4][HALF];
@@ -286,17 +376,18 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
   const int u0 = DIRECT ? gi : gi * g.group, un = DIRECT ? gi + 1 : (int)min((int64_t)u0 + g.group, g.R.max_units);
   for (int u = u0; u < un; ++u) {
     int e, *rw = rows[u & 1];
-    uint16_t(*hu)[LDH] = hs[u & 1];
+    uint16_t(*hu)[LDH] = hs[u & (HB - 1)];
     const int count = find_unit<U, DIRECT>(g, u, 0, &e, rw);
     if (count <= 0) {
       if (DIRECT && count < 0 && wave == 0) copy_row(g, u, N, c0, c1, keep);
       return;                                                 // units behind the last used one are empty too
     }
-    if (n0 < N) {
-      if (e != have) {
+    int64_t n0 = c0 + 64 * wave, n = n0 + 4 * c;              // the wave's and the lane's first column
+    auto load_group = [&]() __attribute__((always_inline)) {
+      if (e != have || T < 4) {
         have = e;
         if constexpr (TRANS) {
-          const uint16_t* A = g.a + (int64_t)e * g.rank * g.K + n0 + 4 * c;
+          const uint16_t* A = g.a + (int64_t)e * g.rank * g.K + n;
 #pragma unroll
           for (int s = 0; s < HALF; ++s) cv[s].load(A + (int64_t)rank0(s) * g.K, g.K, rank0(s) < g.rank ? 8 : 0);
         } else {
@@ -322,7 +413,8 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
           if (g.base && 16 * t + 4 * q + v < count && n < N) yv[t][v] = ld4_tail(g.base + (int64_t)m[v] * N, n, N);
         }
       }
-    }
+    };
+    if (n0 < c1) load_group();
     loads_first();
     // h of the unit's rows: the splits' sums in split order, as two bf16 terms
     auto stage = [&](auto max_splits) __attribute__((always_inline)) {
@@ -356,9 +448,9 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
     };
     if (g.splits == 1) stage(Int<1>{});
     else if (T > 1 || g.splits <= 4) stage(Int<4>{});
-    else stage(Int<kLoraMaxSplits>{});
+    else stage(Int<8>{});
     __syncthreads();
-    if (n0 >= N) continue;
+    while (n0 < c1) {
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       if (16 * t >= count) break;
@@ -372,7 +464,9 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
         acc[b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-          const u32x4_t a = TRANS ? cv[TRANS ? s % HALF : 0].operand(b) : bv[TRANS ? 0 : b][s % HALF];
+          u32x4_t a;
+          if constexpr (TRANS) a = cv[s % HALF].operand(b);
+          else a = bv[b][s % HALF];
           acc[b] = mfma_bf16(hf[s], a, acc[b]);
         }
       }
@@ -388,7 +482,154 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
         st4_tail(g.y + (int64_t)m[v] * N, n, N, o);
       }
     }
+      if constexpr (T == 4) break;                            // one part of the columns, several units
+      n0 += kLoraCols;
+      n += kLoraCols;
+      if (n0 < c1) load_group();
+    }
   }
+}
+
+// Both products of a call of few rows in one launch: every block contracts
+// its unit's rows over all of K by itself and expands a part of the columns.
+// A is read once per part, from the L2 after the first, which costs less than
+// a second launch and the round trips at its start while A is small.
+// grid (column parts, rows); NW waves.
+constexpr int small_waves(int rp) { return rp == 64 ? 8 : 16; }
+template <int RP>
+__global__ void __launch_bounds__(64 * small_waves(RP)) k_lora_small(LoraArgs g) {
+  constexpr int RB = RP / 16, NW = small_waves(RP), LD = RP + 4, S = RP == 16 ? 1 : RP / 16, HALF = RP == 16 ? 1 : RP / 32;
+  constexpr int NB = RB == 1 ? 4 : 2, IMG = (1 + RB) * 2048, LDH = 2 * RP + 8;
+  constexpr int BYTES = NW * IMG > NW * 16 * LD * 4 ? NW * IMG : NW * 16 * LD * 4;
+  __shared__ __align__(16) uint8_t lds[BYTES];
+  __shared__ __align__(16) uint16_t hs[16][LDH];
+  __shared__ __align__(16) int rows[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
+  const int64_t N = g.N, K = g.K;
+  const int64_t groups = (N + 63) / 64, g0 = groups * blockIdx.x / gridDim.x, g1 = groups * (blockIdx.x + 1) / gridDim.x;
+  const bool keep = g.h && blockIdx.x == 0;
+  int e;
+  const int count = find_unit<16, true>(g, blockIdx.y, 0, &e, rows);
+  if (count <= 0) {
+    if (count < 0 && wave == 0) copy_row(g, blockIdx.y, N, 64 * g0, min(64 * g1, N), keep);
+    return;
+  }
+  auto rank0 = [q](int s) { return RP == 16 ? 8 * (q & 1) : 32 * s + 8 * q; };
+  const uint16_t* B = g.b + (int64_t)e * N * g.rank;
+  const int4 m4 = *reinterpret_cast<const int4*>(rows + 4 * q);
+  const int m[4] = {m4.x, m4.y, m4.z, m4.w};
+  BGroup<RP> bg;
+  u32x2_t yv[4];
+  auto load_group = [&](int64_t n0) __attribute__((always_inline)) {
+    const int64_t n = n0 + 4 * c;
+    bg.load(B, n0, N, g.rank, lane);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      yv[v] = (u32x2_t){0u, 0u};
+      if (g.base && 4 * q + v < count && n < N) yv[v] = ld4_tail(g.base + (int64_t)m[v] * N, n, N);
+    }
+  };
+  // h: the waves split K into steps of 64, NB steps' loads in flight
+  const int steps = (int)(K / 64), s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
+  uint8_t* img = lds + wave * IMG;
+  const int lr = lane >> 3, lk = lane & 7;
+  const uint16_t* zp[2 * (1 + RB)];
+#pragma unroll
+  for (int i = 0; i < 2 * (1 + RB); ++i) {
+    const int r = 8 * i + lr;
+    zp[i] = i < 2 ? g.z + (int64_t)rows[min(r, count - 1)] * K + 8 * lk
+                  : g.a + ((int64_t)e * g.rank + min(r - 16, g.rank - 1)) * K + 8 * lk;
+  }
+  f32x4_t acc[RB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i) acc[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  if (g0 + wave < g1) load_group(64 * (g0 + wave));
+  for (int s = s0; s < s1; s += NB) {
+    u32x4_t v[NB][2 * (1 + RB)];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      if (s + j < s1)
+#pragma unroll
+        for (int i = 0; i < 2 * (1 + RB); ++i)
+          if (i != 1 || count > 8) v[j][i] = ld16(zp[i] + 64 * (s + j));
+    loads_first();
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      if (s + j >= s1) break;
+#pragma unroll
+      for (int i = 0; i < 2 * (1 + RB); ++i)
+        if (i != 1 || count > 8) st16(img + chunk_at(8 * i + lr, lk), v[j][i]);
+      __asm__ volatile("" ::: "memory");
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4_t zv = ld16(img + chunk_at(min(c, count - 1), 4 * h + q));
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+          acc[i] = mfma_bf16(ld16(img + chunk_at(16 + 16 * i + c, 4 * h + q)), zv, acc[i]);
+      }
+      __asm__ volatile("" ::: "memory");
+    }
+  }
+  __syncthreads();                                            // the images give way to the sums
+  float(*red)[16][LD] = reinterpret_cast<float(*)[16][LD]>(lds);
+#pragma unroll
+  for (int i = 0; i < RB; ++i) *reinterpret_cast<f32x4_t*>(&red[wave][c][16 * i + 4 * q]) = acc[i];
+  __syncthreads();
+  const float sc = g.scales[e];
+  for (int i = threadIdx.x; i < count * (RP / 2); i += 64 * NW) {
+    const int row = i / (RP / 2), r = 2 * (i % (RP / 2));
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      a += red[w][row][r];
+      b += red[w][row][r + 1];
+    }
+    a = r < g.rank ? a * sc : 0.f;
+    b = r < g.rank ? b * sc : 0.f;
+    if (keep && r < g.rank) {
+      g.h[(int64_t)rows[row] * g.rank + r] = a;
+      g.h[(int64_t)rows[row] * g.rank + r + 1] = b;
+    }
+    split2(a, b, reinterpret_cast<uint32_t*>(&hs[row][r]), reinterpret_cast<uint32_t*>(&hs[row][RP + r]));
+  }
+  __syncthreads();
+  u32x4_t hf[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) hf[s] = ld16(&hs[min(c, count - 1)][32 * s + 8 * q]);
+  for (int64_t gi = g0 + wave; gi < g1; gi += NW) {
+    const int64_t n = 64 * gi + 4 * c;
+    bg.store(img, g.rank, lane);
+    f32x4_t o[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      o[b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        o[b] = mfma_bf16(hf[s], BGroup<RP>::operand(img, b, c, rank0(s % HALF) / 8, g.rank), o[b]);
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if (4 * q + v >= count || n >= N) continue;
+      u32x2_t w;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        w[k] = pack_bf16(lo_bf16(yv[v][k]) + o[2 * k][v], hi_bf16(yv[v][k]) + o[2 * k + 1][v]);
+      st4_tail(g.y + (int64_t)m[v] * N, n, N, w);
+    }
+    __asm__ volatile("" ::: "memory");
+    if (gi + NW < g1) load_group(64 * (gi + NW));
+  }
+}
+
+hipError_t launch_lora_small(const LoraArgs& g, int parts, hipStream_t st) {
+  const dim3 grid((unsigned)parts, (unsigned)g.M);
+  switch (lora_rp(g.rank)) {
+    case 16: hipLaunchKernelGGL(k_lora_small<16>, grid, dim3(64 * small_waves(16)), 0, st, g); break;
+    case 32: hipLaunchKernelGGL(k_lora_small<32>, grid, dim3(64 * small_waves(32)), 0, st, g); break;
+    case 64: hipLaunchKernelGGL(k_lora_small<64>, grid, dim3(64 * small_waves(64)), 0, st, g); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
 }
 
 hipError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, int unit_rows, int64_t max_units, int32_t* units,
@@ -415,7 +656,7 @@ static void run_shrink(const LoraArgs& g, bool direct, hipStream_t st) {
 template <int RP, bool TRANS>
 static void run_expand(const LoraArgs& g, bool direct, hipStream_t st) {
   const int64_t cols = TRANS ? g.K : g.N;
-  const int64_t per = (cols + 8 * kLoraCols - 1) / (8 * kLoraCols);
+  const int64_t per = (cols + 8 * g.cols - 1) / (8 * g.cols);
   const bool rest = g.base != g.y || (!TRANS && g.h);
   const int64_t groups = direct ? g.M : (g.R.max_units + g.group - 1) / g.group + (rest ? (g.M + 63) / 64 : 0);
   const dim3 grid((unsigned)(8 * per * groups));

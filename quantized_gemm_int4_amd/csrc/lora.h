@@ -11,9 +11,8 @@ namespace hm {
 constexpr int64_t kLoraMaxRows = 1 << 20;
 constexpr int kLoraDirect = 64;      // most rows of a call whose blocks find their unit from the ids themselves
 constexpr int kLoraPlanBlocks = 256; // most blocks of the grouping kernel
-constexpr int kLoraMaxSplits = 16;   // most blocks along a contraction
 constexpr int kLoraUnit = 64;        // rows per unit of the gradient
-constexpr int kLoraCols = 256;       // output columns per block of the expanding kernel
+constexpr int kLoraCols = 256;       // output columns that an expanding block takes at a time
 
 // Rows grouped by adapter.  A unit is up to unit_rows rows of one adapter,
 // which share the loads of its matrices: units[u] = {adapter, count}, count 0
@@ -39,7 +38,7 @@ struct LoraArgs {
   float* h;                  // [M][rank]: written by the forward if not null
   float* part;               // fp32 [splits][M][rank] contracted values
   int splits;
-  int group;                 // units per expanding block
+  int group, cols;           // units and columns per expanding block; one of them is more than a unit, kLoraCols
   LoraRows R;
 };
 
@@ -67,6 +66,8 @@ hipError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, int unit_rows,
 hipError_t launch_lora_shrink(const LoraArgs& g, bool direct, bool trans, hipStream_t st);
 // y = base + B h or, trans, base + A^T g.
 hipError_t launch_lora_expand(const LoraArgs& g, bool direct, bool trans, hipStream_t st);
+// both forward products in one launch (M <= kLoraDirect, rank <= 64)
+hipError_t launch_lora_small(const LoraArgs& g, int parts, hipStream_t st);
 hipError_t launch_lora_pack(const LoraGradArgs& g, hipStream_t st);
 hipError_t launch_lora_outer(const LoraGradArgs& g, hipStream_t st);
 hipError_t launch_lora_sums(const LoraGradArgs& g, hipStream_t st);

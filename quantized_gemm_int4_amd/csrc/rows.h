@@ -46,7 +46,7 @@ __device__ __forceinline__ u32x2_t ld4_tail(const uint16_t* row, int64_t c, int6
 }
 __device__ __forceinline__ void st4_tail(uint16_t* row, int64_t c, int64_t n, u32x2_t v) {
   if (c + 4 <= n) {
-    *reinterpret_cast<u32x2_any_t*>(row + c) = v;
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x2_any_t*>(row + c));
     return;
   }
 #pragma unroll

@@ -167,8 +167,10 @@ def test_lora_no_rows_and_refusals():
                 lambda: hm.hm_lora_grad(d, z(3, 24), x, h, ids, a, b, s, need_dx=False, dx_base=x)):
         with pytest.raises(ValueError):
             bad()
+    ids100, need = torch.zeros(100, dtype=torch.int32, device=dev), hm.hm_lora_workspace_size(d, 100)
+    assert need > 0
     with pytest.raises(hm.HmError):
-        hm.hm_lora(d, x, ids, a, b, s, y=z(3, 24), ws=torch.empty(0, dtype=torch.uint8, device=dev))
+        hm.hm_lora(d, z(100, 128), ids100, a, b, s, ws=torch.empty(need - 1, dtype=torch.uint8, device=dev))
     with pytest.raises(hm.HmError):
         hm.hm_lora_workspace_size(hm.lora_desc(24, 128, 12, 2), 4)
 
