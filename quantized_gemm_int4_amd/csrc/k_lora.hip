@@ -225,7 +225,6 @@ __global__ void __launch_bounds__(64 * shrink_waves(RP, T)) k_lora_shrink(LoraAr
 #pragma unroll
     for (int i = 0; i < RB; ++i) acc[t][i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   u32x4_t next[2 * TILES];
-  Cols8<TRANS ? RB : 1> bn[2];
   auto load = [&](int s) __attribute__((always_inline)) {
     const int64_t at = 64 * (int64_t)s;
     const bool whole = !TRANS || at + 64 <= len;
@@ -234,28 +233,29 @@ __global__ void __launch_bounds__(64 * shrink_waves(RP, T)) k_lora_shrink(LoraAr
       if (whole) next[i] = TRANS ? ld8(zp[i] + at) : ld16(zp[i] + at);
       else next[i] = at + 8 * lk < len ? ld8_tail(zp[i] - 8 * lk, at + 8 * lk, len) : (u32x4_t){0u, 0u, 0u, 0u};
     }
-    if constexpr (TRANS) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t left = len - (at + 32 * j + 8 * q);
-        bn[j].load(bp + (at + 32 * j) * g.rank, g.rank, whole ? in_rank : (int)max(min(left, (int64_t)in_rank), (int64_t)0));
-      }
-    }
   };
-  if (s0 < s1) load(s0);
+  // B's operands of half a step, loaded half a step ahead
+  Cols8<TRANS ? RB : 1> bv[2];
+  auto load_b = [&](int s, int j) __attribute__((always_inline)) {
+    const int64_t at = 64 * (int64_t)s + 32 * j, left = len - (at + 8 * q);
+    bv[j].load(bp + at * g.rank, g.rank, at + 32 <= len ? in_rank : (int)max(min(left, (int64_t)in_rank), (int64_t)0));
+  };
+  if (s0 < s1) {
+    load(s0);
+    if constexpr (TRANS) load_b(s0, 0);
+  }
   for (int s = s0; s < s1; ++s) {
 #pragma unroll
     for (int i = 0; i < 2 * TILES; ++i) st16(img + chunk_at(8 * i + lr, lk), next[i]);
-    Cols8<TRANS ? RB : 1> bv[2];
-    if constexpr (TRANS) {
-      bv[0] = bn[0];
-      bv[1] = bn[1];
-    }
     __asm__ volatile("" ::: "memory");                        // a wave's LDS accesses stay in order
     if (s + 1 < s1) load(s + 1);
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
+      if constexpr (TRANS) {
+        if (j == 0) load_b(s, 1);
+        else if (s + 1 < s1) load_b(s + 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
       u32x4_t zv[T];
 #pragma unroll
       for (int t = 0; t < T; ++t) zv[t] = ld16(img + chunk_at(16 * t + c, 4 * j + q));

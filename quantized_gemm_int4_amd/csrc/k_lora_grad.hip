@@ -10,39 +10,42 @@
 
 namespace hm {
 
-// grid (units, 2): g (the splits' sums; y = 0) or h (y = 1) of a unit's rows
+// grid (units, 2, 2): g (the splits' sums; y = 0) or h (y = 1) of 32 of a unit's rows
 // in the order of the outer product's operands, so that a wave loads each
 // with one contiguous access: [32-row step][hi, lo][16-rank block][lane][8],
 // lane (c, q) holding rank 16 k + c of rows 32 s + 8 q .. + 7; zeros beyond
 // the rank and the unit's rows.
 template <int RP>
 __global__ void __launch_bounds__(256) k_lora_pack(LoraGradArgs g) {
-  __shared__ float v[kLoraUnit][RP + 1];
-  const int u = blockIdx.x, count = g.R.units[2 * u + 1];
+  __shared__ float v[32][RP + 1];
+  const int u = blockIdx.x, half = blockIdx.z, count = g.R.units[2 * u + 1] - 32 * half;
   const bool is_h = blockIdx.y != 0;
-  if (count == 0) return;
-  const int32_t* rows = g.R.rows + (int64_t)u * kLoraUnit;
+  if (count <= 0) return;                                     // unused units and steps are not read
+  const int32_t* rows = g.R.rows + (int64_t)u * kLoraUnit + 32 * half;
+  const float* src = is_h ? g.h : g.part;
+  const int splits = is_h ? 1 : g.splits;
 #pragma unroll
-  for (int i0 = 0; i0 < kLoraUnit * (RP / 4); i0 += 256) {
+  for (int i0 = 0; i0 < 32 * (RP / 4); i0 += 256) {
     const int i = i0 + threadIdx.x, row = i / (RP / 4), r = 4 * (i % (RP / 4));
-    f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+    if (i >= 32 * (RP / 4)) break;
+    f32x4_t s = {0.f, 0.f, 0.f, 0.f}, p[4];
     if (row < count && r < g.rank) {
       const int64_t at = (int64_t)rows[row] * g.rank + r;
-      if (is_h) {
-        s = *reinterpret_cast<const f32x4_t*>(g.h + at);
-      } else {
-        for (int k = 0; k < g.splits; ++k)
-          s += *reinterpret_cast<const f32x4_t*>(g.part + (int64_t)k * g.M * g.rank + at);
-      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)                             // at most four splits
+        p[k] = *reinterpret_cast<const f32x4_t*>(src + (int64_t)min(k, splits - 1) * g.M * g.rank + at);
+      loads_first();
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < splits) s += p[k];
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[row][r + k] = s[k];
   }
   __syncthreads();
-  uint16_t* out = (is_h ? g.ht : g.gt) + (int64_t)u * 2 * RP * kLoraUnit;
-  for (int i = threadIdx.x; i < RP * (kLoraUnit / 8); i += 256) {
-    const int lane = i & 63, k = (i >> 6) % (RP / 16), s = (i >> 6) / (RP / 16);
-    const int r = 16 * k + (lane & 15), m = 32 * s + 8 * (lane >> 4);
+  uint16_t* out = (is_h ? g.ht : g.gt) + ((int64_t)u * 2 + half) * 2 * RP * 32;
+  for (int i = threadIdx.x; i < RP * 4; i += 256) {
+    const int lane = i & 63, k = i >> 6, r = 16 * k + (lane & 15), m = 8 * (lane >> 4);
     u32x4_t hi, lo;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
@@ -51,9 +54,8 @@ __global__ void __launch_bounds__(256) k_lora_pack(LoraGradArgs g) {
       hi[p] = h2;
       lo[p] = l2;
     }
-    uint16_t* o = out + s * (2 * RP * 32) + (k * 64 + lane) * 8;
-    st16(o, hi);
-    st16(o + RP * 32, lo);
+    st16(out + 8 * i, hi);
+    st16(out + RP * 32 + 8 * i, lo);
   }
 }
 
@@ -83,11 +85,41 @@ __device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, fl
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int i = 0; i < RB; ++i) acc[j][i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    for (int s = 2 * ua + wave; s < 2 * ub; s += 4) {
-      const int u = s >> 1, first = 32 * (s & 1), count = g.R.units[2 * u + 1] - first;
-      if (count <= 0) continue;
-      const int32_t* rows = g.R.rows + (int64_t)u * kLoraUnit + first;
-      Cols8<8> zv;
+    // Two steps ahead the row numbers are on their way, one step ahead the rows: a gathered load waits for two trips
+    // to memory otherwise (m = 8192: 113 us).
+    struct Rows { int r[8], count; };
+    auto fetch_rows = [&](int s) __attribute__((always_inline)) {
+      Rows R;
+      const int32_t* p = g.R.rows + 32 * (int64_t)s;          // a unit's slots: two steps of 32
+      const int4 lo = *reinterpret_cast<const int4*>(p + 8 * q), hi = *reinterpret_cast<const int4*>(p + 8 * q + 4);
+      R.r[0] = lo.x; R.r[1] = lo.y; R.r[2] = lo.z; R.r[3] = lo.w;
+      R.r[4] = hi.x; R.r[5] = hi.y; R.r[6] = hi.z; R.r[7] = hi.w;
+      R.count = g.R.units[2 * (s >> 1) + 1] - 32 * (s & 1);
+      return R;
+    };
+    Cols8<8> next;
+    auto fetch_z = [&](const Rows& R) __attribute__((always_inline)) {
+      const int first = __builtin_amdgcn_readfirstlane(R.r[0]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // rows behind the unit's last repeat the step's first: their g and h are 0
+        const int64_t m = 8 * q + i < R.count ? R.r[i] : first;
+        u32x4_t v = {0u, 0u, 0u, 0u};
+        if (R.count > 0 && col < n) v = ld8_tail(z + m * n, col, n);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) next.w[i][k] = v[k];
+      }
+    };
+    const int s_end = 2 * ub;
+    int s = 2 * ua + wave;
+    Rows R{};
+    if (s < s_end) {
+      R = fetch_rows(s);
+      fetch_z(R);
+      if (s + 4 < s_end) R = fetch_rows(s + 4);
+    }
+    for (; s < s_end; s += 4) {
+      const Cols8<8> zv = next;
       u32x4_t fh[RB], fl[RB];
       const uint16_t* fu = f + (int64_t)s * 2 * RP * 32;
 #pragma unroll
@@ -95,16 +127,13 @@ __device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, fl
         fh[k] = ld16(fu + 512 * k);
         fl[k] = ld16(fu + RP * 32 + 512 * k);
       }
-      // rows behind the unit's last repeat its first: their g and h are 0
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t m = rows[8 * q + i < count ? 8 * q + i : 0];
-        u32x4_t v = {0u, 0u, 0u, 0u};
-        if (col < n) v = ld8_tail(z + m * n, col, n);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) zv.w[i][k] = v[k];
+      const int count = g.R.units[2 * (s >> 1) + 1] - 32 * (s & 1);
+      if (s + 4 < s_end) {
+        fetch_z(R);
+        if (s + 8 < s_end) R = fetch_rows(s + 8);
       }
       loads_first();
+      if (count <= 0) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const u32x4_t zo = zv.operand(j);
@@ -196,7 +225,7 @@ __global__ void __launch_bounds__(256) k_lora_sums(LoraGradArgs g) {
 }
 
 hipError_t launch_lora_pack(const LoraGradArgs& g, hipStream_t st) {
-  const dim3 grid((unsigned)g.R.max_units, 2);
+  const dim3 grid((unsigned)g.R.max_units, 2, 2);
   switch (lora_rp(g.rank)) {
     case 16: hipLaunchKernelGGL(k_lora_pack<16>, grid, dim3(256), 0, st, g); break;
     case 32: hipLaunchKernelGGL(k_lora_pack<32>, grid, dim3(256), 0, st, g); break;
