@@ -58,8 +58,8 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
   // 640 blocks (32-row blocks), each wave keeping a step of 64 or more
   const bool few = w.unit_rows == 16;
   const int rp = lora_rp(d->rank);
-  const int64_t blocks = few ? w.max_units : w.max_units * (w.unit_rows / 32), waves = few ? (rp == 128 ? 4 : (rp == 64 ? 8 : 16)) : 4;
-  const int64_t want = few ? 4096 / (blocks * waves) : 640 / blocks, most = std::min<int64_t>(rp == 128 && few ? 8 : 4, len / (64 * waves));
+  const int64_t blocks = few ? w.max_units : w.max_units * (w.unit_rows / 32), waves = grad ? 8 : (few ? (rp == 128 ? 4 : (rp == 64 ? 8 : 16)) : 4);
+  const int64_t want = few ? 4096 / (blocks * waves) : 640 / blocks, most = std::min<int64_t>(grad || (few && rp == 128) ? kLoraMaxSplits : 4, len / (64 * waves));
   w.splits = (int)std::max<int64_t>(1, std::min(want, most));
   // expanding blocks: several units against one part of B where there are many, several parts of the columns where
   // there are many units of few rows
@@ -93,8 +93,8 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
     const size_t packed = (size_t)w.max_units * 2 * (size_t)lora_rp(d->rank) * kLoraUnit * 2;
     w.gt = take(packed);
     w.ht = take(packed);
-    const int64_t tiles = ((d->n + 127) / 128 + d->k / 128) * (d->rank > 64 ? 2 : 1);
-    w.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(16, std::min((512 + tiles - 1) / tiles, w.max_units / 4)));
+    const int64_t tiles = ((d->n + 127) / 128 + d->k / 128) * std::max(1, lora_rp(d->rank) / 32);
+    w.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(16, std::min((767 + tiles) / tiles, w.max_units / 4)));
     w.sums = take(w.chunks > 1 ? (size_t)(2 * w.chunks) * (size_t)d->rank * (size_t)(d->k + d->n) * 4 : 0);
   }
   w.total = at;

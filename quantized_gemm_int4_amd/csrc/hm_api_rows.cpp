@@ -19,6 +19,7 @@ constexpr int64_t kMaxBlocks = (1ll << 24) - 1;
 hm_status check_rows(int64_t t, int32_t topk, int64_t n) {
   if (t < 0 || topk < 1 || n < 1) return HM_ERR_SHAPE;
   if (t > kMaxBlocks || t * (int64_t)topk >= (1ll << 31) || n > (1ll << 24)) return HM_ERR_SHAPE;
+  if (t * ((n + 511) / 512) > 4 * kMaxBlocks) return HM_ERR_SHAPE;        // a wave per 512 columns of a row
   return HM_OK;
 }
 
@@ -29,6 +30,7 @@ hm_status check_dispatch(int64_t t, int32_t topk, int32_t num_experts) {
 }
 
 size_t dispatch_ws(int64_t t, int32_t topk, int32_t num_experts) {
+  if (t * topk <= kSortDispatch) return 0;
   const int nb = moe_sort_blocks(t * topk, nullptr);
   return nb > 1 ? (size_t)nb * (size_t)num_experts * sizeof(int32_t) : 0;
 }
@@ -61,8 +63,14 @@ HM_API hm_status hm_moe_dispatch(const uint16_t* x, const int32_t* topk_ids, int
     if (ws_bytes < need) return HM_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return HM_ERR_ALIGN;
   }
-  hipError_t e = launch_moe_sort_pos(topk_ids, t * topk, num_experts, counts, offsets, sorted_pairs, positions,
-                                     static_cast<int32_t*>(ws), stream);
+  if (t * topk <= kSmallPairs)
+    return done(launch_dispatch_small(x, topk_ids, t, topk, num_experts, n, xs, counts, offsets, sorted_pairs, positions,
+                                      stream));
+  hipError_t e = t * topk <= kSortDispatch
+                     ? launch_dispatch_sort(topk_ids, t * topk, num_experts, counts, offsets, sorted_pairs, positions,
+                                            stream)
+                     : launch_moe_sort_pos(topk_ids, t * topk, num_experts, counts, offsets, sorted_pairs, positions,
+                                           static_cast<int32_t*>(ws), stream);
   if (e == hipSuccess) e = launch_dispatch_rows(x, positions, t, topk, n, xs, stream);
   return done(e);
 }

@@ -171,7 +171,9 @@ template <int RP> struct BGroup {
 };
 
 // Waves of a contracting block.
-constexpr int shrink_waves(int rp, int t) { return t > 1 || rp == 128 ? 4 : (rp == 64 ? 8 : 16); }
+constexpr int shrink_waves(int rp, int t, bool trans) {
+  return trans ? 8 : (t > 1 || rp == 128 ? 4 : (rp == 64 ? 8 : 16));
+}
 
 // A wave's private LDS image of 64 values of 16 rows: row r's 16-byte chunk k
 // (0 .. 7) sits at place k ^ (r & 7) of its 128 bytes, so that both the
@@ -189,8 +191,8 @@ __device__ __forceinline__ int chunk_at(int r, int k) { return r * 128 + ((k ^ (
 // into registers, one step ahead, and passes them through its own LDS image;
 // no block barrier.
 template <int RP, int T, bool DIRECT, bool TRANS>
-__global__ void __launch_bounds__(64 * shrink_waves(RP, T)) k_lora_shrink(LoraArgs g) {
-  constexpr int RB = RP / 16, LD = RP + 4, U = 16 * T, NW = shrink_waves(RP, T);
+__global__ void __launch_bounds__(64 * shrink_waves(RP, T, TRANS)) k_lora_shrink(LoraArgs g) {
+  constexpr int RB = RP / 16, LD = RP + 4, U = 16 * T, NW = shrink_waves(RP, T, TRANS);
   constexpr int TILES = TRANS ? T : T + RB;                   // 16-row tiles staged per step
   // LDS: the waves' images, then the sums (one per wave while that is small, else one for several waves in turn)
   constexpr int IMG = TILES * 2048, FIT = 72 * 1024 / (U * LD * 4);
@@ -447,8 +449,8 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
       }
     };
     if (g.splits == 1) stage(Int<1>{});
-    else if (T > 1 || g.splits <= 4) stage(Int<4>{});
-    else stage(Int<8>{});
+    else if ((T > 1 && !TRANS) || g.splits <= 4) stage(Int<4>{});   // the planner's limits
+    else stage(Int<kLoraMaxSplits>{});
     __syncthreads();
     while (n0 < c1) {
 #pragma unroll
@@ -645,7 +647,7 @@ template <int RP, bool TRANS>
 static void run_shrink(const LoraArgs& g, bool direct, hipStream_t st) {
   const int t = direct || g.R.unit_rows == 16 ? 1 : 2;
   const dim3 grid((unsigned)g.splits, (unsigned)(direct ? g.M : g.R.max_units * (g.R.unit_rows / (16 * t))));
-  const dim3 block(64u * (unsigned)shrink_waves(RP, t));
+  const dim3 block(64u * (unsigned)shrink_waves(RP, t, TRANS));
   if constexpr (!TRANS) {
     if (direct) hipLaunchKernelGGL((k_lora_shrink<RP, 1, true, false>), grid, block, 0, st, g);
     else if (t == 1) hipLaunchKernelGGL((k_lora_shrink<RP, 1, false, false>), grid, block, 0, st, g);

@@ -28,15 +28,15 @@ __global__ void __launch_bounds__(256) k_lora_pack(LoraGradArgs g) {
   for (int i0 = 0; i0 < 32 * (RP / 4); i0 += 256) {
     const int i = i0 + threadIdx.x, row = i / (RP / 4), r = 4 * (i % (RP / 4));
     if (i >= 32 * (RP / 4)) break;
-    f32x4_t s = {0.f, 0.f, 0.f, 0.f}, p[4];
+    f32x4_t s = {0.f, 0.f, 0.f, 0.f}, p[kLoraMaxSplits];
     if (row < count && r < g.rank) {
       const int64_t at = (int64_t)rows[row] * g.rank + r;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)                             // at most four splits
+      for (int k = 0; k < kLoraMaxSplits; ++k)
         p[k] = *reinterpret_cast<const f32x4_t*>(src + (int64_t)min(k, splits - 1) * g.M * g.rank + at);
       loads_first();
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < kLoraMaxSplits; ++k)
         if (k < splits) s += p[k];
     }
 #pragma unroll
@@ -63,20 +63,21 @@ __device__ __forceinline__ int chunk_units(const LoraGradArgs& g) {
   return (g.R.first[g.L] + g.chunks - 1) / g.chunks;
 }
 
-// grid (128-column tiles of dy, then of x; chunks of units; rank chunks of 16
-// RB): one adapter of the chunk after the other.  The waves take its 32-row
+// One block per (128-column tile of dy or x, chunk of units, rank chunk of 16
+// RB): one adapter of the chunk after the other.  Block id i takes tile i % 8
+// + 8 k, its rank chunks side by side: they read the same rows at about the
+// same time through one XCD's L2.  The waves take its 32-row
 // steps in turn; their sums meet in LDS, in wave order.  An adapter that
 // reaches beyond the chunk leaves a partial sum: slot 2 j if it began before
 // chunk j, else 2 j + 1.
 template <int RP, int RB, bool db>
-__device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, float (*red)[132]) {
+__device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, int chunk, int r00, float (*red)[132]) {
   constexpr int RC = 16 * RB;
   const int64_t n = db ? g.N : g.K;
   const uint16_t* z = db ? g.dy : g.x;
-  const int r00 = blockIdx.z * RC;
   const uint16_t* f = (db ? g.ht : g.gt) + r00 * 32 + 8 * (threadIdx.x & 63);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
-  const int per = chunk_units(g), lo_u = blockIdx.y * per, hi_u = min(lo_u + per, g.R.first[g.L]);
+  const int per = chunk_units(g), lo_u = chunk * per, hi_u = min(lo_u + per, g.R.first[g.L]);
   const int64_t col = k0 + 8 * c;
   for (int ua = lo_u; ua < hi_u;) {
     const int e = g.R.units[2 * ua], e0 = g.R.first[e], e1 = g.R.first[e + 1], ub = min(e1, hi_u);
@@ -164,7 +165,7 @@ __device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, fl
       __syncthreads();
     }
     const bool whole = e0 >= lo_u && e1 <= hi_u;
-    float* part = g.sums + (int64_t)(2 * blockIdx.y + (e0 < lo_u ? 0 : 1)) * g.rank * (g.K + g.N);
+    float* part = g.sums + (int64_t)(2 * chunk + (e0 < lo_u ? 0 : 1)) * g.rank * (g.K + g.N);
     for (int i = threadIdx.x; i < 128 * RC / 8; i += 256) {
       int64_t at;
       float o[8];
@@ -197,10 +198,13 @@ __device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, fl
 
 template <int RP, int RB>
 __global__ void __launch_bounds__(256, 2) k_lora_outer(LoraGradArgs g) {
+  constexpr int RCS = RP / (16 * RB);
   __shared__ float red[16 * RB][132];
-  const int tiles_n = (int)((g.N + 127) / 128);
-  if ((int)blockIdx.x < tiles_n) outer_tile<RP, RB, true>(g, 128 * (int64_t)blockIdx.x, red);
-  else outer_tile<RP, RB, false>(g, 128 * (int64_t)(blockIdx.x - tiles_n), red);
+  const int tiles_n = (int)((g.N + 127) / 128), tiles = tiles_n + (int)(g.K / 128), per = (tiles + 7) / 8;
+  const int id = blockIdx.x >> 3, r00 = id % RCS * 16 * RB, at = id / RCS;
+  const int tile = at % per * 8 + (int)(blockIdx.x & 7), chunk = at / per;
+  if (tile < tiles_n) outer_tile<RP, RB, true>(g, 128 * (int64_t)tile, chunk, r00, red);
+  else if (tile < tiles) outer_tile<RP, RB, false>(g, 128 * (int64_t)(tile - tiles_n), chunk, r00, red);
 }
 
 // grid (eight values per thread of an adapter's da and db, adapters): sums of
@@ -236,14 +240,14 @@ hipError_t launch_lora_pack(const LoraGradArgs& g, hipStream_t st) {
 }
 
 hipError_t launch_lora_outer(const LoraGradArgs& g, hipStream_t st) {
-  dim3 grid((unsigned)((g.N + 127) / 128 + g.K / 128), (unsigned)g.chunks, 1);
-  switch (lora_rp(g.rank)) {
+  const int64_t per = ((g.N + 127) / 128 + g.K / 128 + 7) / 8;
+  const int rp = lora_rp(g.rank);
+  const dim3 grid((unsigned)(8 * per * g.chunks * (rp == 16 ? 1 : rp / 32)));
+  switch (rp) {
     case 16: hipLaunchKernelGGL((k_lora_outer<16, 1>), grid, dim3(256), 0, st, g); break;
     case 32: hipLaunchKernelGGL((k_lora_outer<32, 2>), grid, dim3(256), 0, st, g); break;
-    case 64: hipLaunchKernelGGL((k_lora_outer<64, 4>), grid, dim3(256), 0, st, g); break;
-    default:
-      grid.z = 2;
-      hipLaunchKernelGGL((k_lora_outer<128, 4>), grid, dim3(256), 0, st, g);
+    case 64: hipLaunchKernelGGL((k_lora_outer<64, 2>), grid, dim3(256), 0, st, g); break;
+    default: hipLaunchKernelGGL((k_lora_outer<128, 2>), grid, dim3(256), 0, st, g);
   }
   return hipGetLastError();
 }

@@ -11,6 +11,7 @@ namespace hm {
 constexpr int64_t kLoraMaxRows = 1 << 20;
 constexpr int kLoraDirect = 64;      // most rows of a call whose blocks find their unit from the ids themselves
 constexpr int kLoraPlanBlocks = 256; // most blocks of the grouping kernel
+constexpr int kLoraMaxSplits = 8;    // most blocks along a contraction
 constexpr int kLoraUnit = 64;        // rows per unit of the gradient
 constexpr int kLoraCols = 256;       // output columns that an expanding block takes at a time
 

@@ -54,6 +54,13 @@ __device__ __forceinline__ void st4_tail(uint16_t* row, int64_t c, int64_t n, u3
     if (c + e < n) row[c + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
 }
 
+constexpr int64_t kSmallPairs = 1024;      // pairs that are sorted and moved in one launch
+constexpr int64_t kSortDispatch = 131072;  // pairs that are sorted in one launch
+hipError_t launch_dispatch_small(const uint16_t* x, const int32_t* ids, int64_t t, int topk, int E, int64_t n,
+                                 uint16_t* xs, int32_t* counts, int32_t* offsets, int32_t* sorted_pairs,
+                                 int32_t* positions, hipStream_t st);
+hipError_t launch_dispatch_sort(const int32_t* ids, int64_t P, int E, int32_t* counts, int32_t* offsets,
+                                int32_t* sorted_pairs, int32_t* positions, hipStream_t st);
 // xs[positions[p]] = x[p / topk] for positions in [0, t topk)
 hipError_t launch_dispatch_rows(const uint16_t* x, const int32_t* positions, int64_t t, int topk, int64_t n,
                                 uint16_t* xs, hipStream_t st);

@@ -28,7 +28,8 @@ def _val(bits):
 
 # one token, one wave, many tokens, chunked sorts; rows shorter than a chunk, odd, a chunk past a block's first pass
 SHAPES = [(1, 1, 1, 1), (1, 8, 16, 7168), (3, 2, 5, 7), (5, 3, 9, 13), (64, 8, 256, 264), (33, 6, 512, 2049),
-          (70, 9, 40, 2056), (300, 17, 60, 72), (600, 8, 256, 40), (5000, 1, 3, 24), (2500, 4, 64, 33), (2, 512, 512, 130)]
+          (70, 9, 40, 2056), (300, 17, 60, 72), (600, 8, 256, 40), (5000, 1, 3, 24), (2500, 4, 64, 33), (2, 512, 512, 130),
+          (1024, 1, 7, 40), (1025, 1, 7, 40), (128, 8, 512, 16), (33000, 4, 100, 8)]
 
 
 def _ids(r, t, topk, E, dropped):

@@ -50,9 +50,9 @@ def test_dispatch_experts_and_workspace():
     assert _call("hm_moe_dispatch", *_with(DISPATCH, 4, 0)) == SHAPE
     assert _call("hm_moe_dispatch", *_with(DISPATCH, 4, 513)) == SHAPE
     assert _call("hm_moe_dispatch", *_with(DISPATCH, 4, 1)) == SHAPE      # topk above the experts
-    need = hm.hm_moe_dispatch_workspace_size(5000, 2, 8)
+    need = hm.hm_moe_dispatch_workspace_size(100000, 2, 8)
     assert need > 0 and hm.hm_moe_dispatch_workspace_size(4, 2, 8) == 0
-    big = _with(DISPATCH, 2, 5000)
+    big = _with(DISPATCH, 2, 100000)
     assert _call("hm_moe_dispatch", *big) == NULL
     assert _call("hm_moe_dispatch", *_with(_with(big, 11, GOOD), 12, need - 1)) == WORKSPACE
     assert _call("hm_moe_dispatch", *_with(_with(big, 11, ODD8), 12, need)) == ALIGN
