@@ -430,13 +430,14 @@ def _elsewhere(t, stream):
 
 
 def _arg(t, dtype, shape, name, dev):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shape} on {dev}")
-    return t
+    """The address of a checked tensor on the device of index dev."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {shape} on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _out(t, dtype, shape, name, dev):
-    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _arg(t, dtype, shape, name, dev)
+def _new(dtype, shape, dev):
+    return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
 
 
 def _ws(ws, size, args, dev):
@@ -447,10 +448,10 @@ def _ws(ws, size, args, dev):
         need = size(*args)
         if need == 0:
             return None, 0, None
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"ws: need a contiguous tensor on {dev}")
-    return _ptr(ws), ws.numel() * ws.element_size(), ws
+        ws = _new(torch.uint8, (need,), dev)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: need a contiguous tensor on cuda:{dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def hm_moe_dispatch_workspace_size(t, topk, num_experts):
@@ -471,19 +472,20 @@ def hm_moe_dispatch(x, topk_ids, num_experts, xs=None, counts=None, offsets=None
     if ctx is not None:
         with ctx:
             return hm_moe_dispatch(x, topk_ids, num_experts, xs, counts, offsets, sorted_pairs, positions, ws)
-    (t, n), topk, dev, i32 = x.shape, topk_ids.shape[1], x.device, torch.int32
-    _arg(x, torch.bfloat16, (t, n), "x", dev)
-    _arg(topk_ids, i32, (t, topk), "topk_ids", dev)
+    (t, n), topk, dev, bf, i32 = x.shape, topk_ids.shape[1], x.get_device(), torch.bfloat16, torch.int32
     E = int(num_experts)
-    xs = _out(xs, torch.bfloat16, (t * topk, n), "xs", dev)
-    counts = _out(counts, i32, (E,), "counts", dev)
-    offsets = _out(offsets, i32, (E + 1,), "offsets", dev)
-    sorted_pairs = _out(sorted_pairs, i32, (t * topk,), "sorted_pairs", dev)
-    positions = _out(positions, i32, (t, topk), "positions", dev)
+    xs = _new(bf, (t * topk, n), dev) if xs is None else xs
+    counts = _new(i32, (E,), dev) if counts is None else counts
+    offsets = _new(i32, (E + 1,), dev) if offsets is None else offsets
+    sorted_pairs = _new(i32, (t * topk,), dev) if sorted_pairs is None else sorted_pairs
+    positions = _new(i32, (t, topk), dev) if positions is None else positions
     wsp, wsb, ws = _ws(ws, hm_moe_dispatch_workspace_size, (t, topk, E), dev)
-    _ok("hm_moe_dispatch", lib.hm_moe_dispatch(_ptr(x), _ptr(topk_ids), t, topk, E, n, _ptr(xs), _ptr(counts),
-                                               _ptr(offsets), _ptr(sorted_pairs), _ptr(positions), wsp, wsb,
-                                               _stream()))
+    code = lib.hm_moe_dispatch(_arg(x, bf, (t, n), "x", dev), _arg(topk_ids, i32, (t, topk), "topk_ids", dev), t, topk,
+                               E, n, _arg(xs, bf, (t * topk, n), "xs", dev), _arg(counts, i32, (E,), "counts", dev),
+                               _arg(offsets, i32, (E + 1,), "offsets", dev),
+                               _arg(sorted_pairs, i32, (t * topk,), "sorted_pairs", dev),
+                               _arg(positions, i32, (t, topk), "positions", dev), wsp, wsb, _stream())
+    _ok("hm_moe_dispatch", code)
     return xs, counts, offsets, sorted_pairs, positions
 
 
@@ -494,12 +496,12 @@ def hm_moe_dispatch_grad(dxs, positions, dx=None, stream=None):
     if ctx is not None:
         with ctx:
             return hm_moe_dispatch_grad(dxs, positions, dx)
-    (t, topk), n, dev = positions.shape, dxs.shape[1], dxs.device
-    _arg(dxs, torch.bfloat16, (t * topk, n), "dxs", dev)
-    _arg(positions, torch.int32, (t, topk), "positions", dev)
-    dx = _out(dx, torch.bfloat16, (t, n), "dx", dev)
-    _ok("hm_moe_dispatch_grad", lib.hm_moe_dispatch_grad(_ptr(dxs), _ptr(positions), t, topk, n, _ptr(dx),
-                                                         _stream(stream)))
+    (t, topk), n, dev, bf = positions.shape, dxs.shape[1], dxs.get_device(), torch.bfloat16
+    dx = _new(bf, (t, n), dev) if dx is None else dx
+    code = lib.hm_moe_dispatch_grad(_arg(dxs, bf, (t * topk, n), "dxs", dev),
+                                    _arg(positions, torch.int32, (t, topk), "positions", dev), t, topk, n,
+                                    _arg(dx, bf, (t, n), "dx", dev), _stream())
+    _ok("hm_moe_dispatch_grad", code)
     return dx
 
 
@@ -510,13 +512,13 @@ def hm_moe_collect(ys, weights, positions, out=None, stream=None):
     if ctx is not None:
         with ctx:
             return hm_moe_collect(ys, weights, positions, out)
-    (t, topk), n, dev = positions.shape, ys.shape[1], ys.device
-    _arg(ys, torch.bfloat16, (t * topk, n), "ys", dev)
-    _arg(weights, torch.float32, (t, topk), "weights", dev)
-    _arg(positions, torch.int32, (t, topk), "positions", dev)
-    out = _out(out, torch.bfloat16, (t, n), "out", dev)
-    _ok("hm_moe_collect", lib.hm_moe_collect(_ptr(ys), _ptr(weights), _ptr(positions), t, topk, n, _ptr(out),
-                                             _stream(stream)))
+    (t, topk), n, dev, bf = positions.shape, ys.shape[1], ys.get_device(), torch.bfloat16
+    out = _new(bf, (t, n), dev) if out is None else out
+    code = lib.hm_moe_collect(_arg(ys, bf, (t * topk, n), "ys", dev),
+                              _arg(weights, torch.float32, (t, topk), "weights", dev),
+                              _arg(positions, torch.int32, (t, topk), "positions", dev), t, topk, n,
+                              _arg(out, bf, (t, n), "out", dev), _stream())
+    _ok("hm_moe_collect", code)
     return out
 
 
@@ -528,17 +530,16 @@ def hm_moe_collect_grad(dout, ys, weights, positions, dys=None, dweights=None, s
     if ctx is not None:
         with ctx:
             return hm_moe_collect_grad(dout, ys, weights, positions, dys, dweights)
-    (t, topk), n, dev = positions.shape, dout.shape[1], dout.device
-    _arg(dout, torch.bfloat16, (t, n), "dout", dev)
-    _arg(ys, torch.bfloat16, (t * topk, n), "ys", dev)
-    _arg(weights, torch.float32, (t, topk), "weights", dev)
-    _arg(positions, torch.int32, (t, topk), "positions", dev)
+    (t, topk), n, dev, bf, f32 = positions.shape, dout.shape[1], dout.get_device(), torch.bfloat16, torch.float32
     if dys is None:
-        dys = torch.zeros(t * topk, n, dtype=torch.bfloat16, device=dev)
-    _arg(dys, torch.bfloat16, (t * topk, n), "dys", dev)
-    dweights = _out(dweights, torch.float32, (t, topk), "dweights", dev)
-    _ok("hm_moe_collect_grad", lib.hm_moe_collect_grad(_ptr(dout), _ptr(ys), _ptr(weights), _ptr(positions), t,
-                                                       topk, n, _ptr(dys), _ptr(dweights), _stream(stream)))
+        dys = torch.zeros(t * topk, n, dtype=bf, device=dout.device)
+    dweights = _new(f32, (t, topk), dev) if dweights is None else dweights
+    code = lib.hm_moe_collect_grad(_arg(dout, bf, (t, n), "dout", dev), _arg(ys, bf, (t * topk, n), "ys", dev),
+                                   _arg(weights, f32, (t, topk), "weights", dev),
+                                   _arg(positions, torch.int32, (t, topk), "positions", dev), t, topk, n,
+                                   _arg(dys, bf, (t * topk, n), "dys", dev),
+                                   _arg(dweights, f32, (t, topk), "dweights", dev), _stream())
+    _ok("hm_moe_collect_grad", code)
     return dys, dweights
 
 
@@ -558,16 +559,6 @@ def hm_lora_grad_workspace_size(desc, m):
     return _lora_ws_size("hm_lora_grad_workspace_size", desc, m)
 
 
-def _lora_common(desc, x, adapter_ids, a, b, scales):
-    m, dev, bf = x.shape[0], x.device, torch.bfloat16
-    _arg(x, bf, (m, desc.k), "x", dev)
-    _arg(adapter_ids, torch.int32, (m,), "adapter_ids", dev)
-    _arg(a, bf, (desc.num_adapters, desc.rank, desc.k), "a", dev)
-    _arg(b, bf, (desc.num_adapters, desc.n, desc.rank), "b", dev)
-    _arg(scales, torch.float32, (desc.num_adapters,), "scales", dev)
-    return m, dev
-
-
 def hm_lora(desc, x, adapter_ids, a, b, scales, base=None, y=None, h=None, ws=None, stream=None):
     """Adapters beside a shared projection: x bf16 [m, k], adapter_ids int32
     [m], a bf16 [L, rank, k], b bf16 [L, n, rank], scales fp32 [L] -> y bf16
@@ -578,15 +569,16 @@ def hm_lora(desc, x, adapter_ids, a, b, scales, base=None, y=None, h=None, ws=No
     if ctx is not None:
         with ctx:
             return hm_lora(desc, x, adapter_ids, a, b, scales, base, y, h, ws)
-    m, dev = _lora_common(desc, x, adapter_ids, a, b, scales)
-    if base is not None:
-        _arg(base, torch.bfloat16, (m, desc.n), "base", dev)
-    if h is not None:
-        _arg(h, torch.float32, (m, desc.rank), "h", dev)
-    y = _out(y, torch.bfloat16, (m, desc.n), "y", dev)
+    m, dev, bf, f32 = x.shape[0], x.get_device(), torch.bfloat16, torch.float32
+    n, k, rank, L = desc.n, desc.k, desc.rank, desc.num_adapters
+    y = _new(bf, (m, n), dev) if y is None else y
     wsp, wsb, ws = _ws(ws, hm_lora_workspace_size, (desc, m), dev)
-    _ok("hm_lora", lib.hm_lora(ctypes.byref(desc), _ptr(x), _ptr(adapter_ids), _ptr(a), _ptr(b), _ptr(scales), m,
-                               _ptr(base), _ptr(y), _ptr(h), wsp, wsb, _stream(stream)))
+    code = lib.hm_lora(ctypes.byref(desc), _arg(x, bf, (m, k), "x", dev),
+                       _arg(adapter_ids, torch.int32, (m,), "adapter_ids", dev), _arg(a, bf, (L, rank, k), "a", dev),
+                       _arg(b, bf, (L, n, rank), "b", dev), _arg(scales, f32, (L,), "scales", dev), m,
+                       None if base is None else _arg(base, bf, (m, n), "base", dev), _arg(y, bf, (m, n), "y", dev),
+                       None if h is None else _arg(h, f32, (m, rank), "h", dev), wsp, wsb, _stream())
+    _ok("hm_lora", code)
     return y
 
 
@@ -600,23 +592,24 @@ def hm_lora_grad(desc, dy, x, h, adapter_ids, a, b, scales, dx_base=None, dx=Non
     if ctx is not None:
         with ctx:
             return hm_lora_grad(desc, dy, x, h, adapter_ids, a, b, scales, dx_base, dx, da, db, need_dx, ws)
-    m, dev = _lora_common(desc, x, adapter_ids, a, b, scales)
-    bf = torch.bfloat16
-    _arg(dy, bf, (m, desc.n), "dy", dev)
-    _arg(h, torch.float32, (m, desc.rank), "h", dev)
-    if dx_base is not None:
-        _arg(dx_base, bf, (m, desc.k), "dx_base", dev)
-    if not need_dx:
-        if dx is not None or dx_base is not None:
-            raise ValueError("need_dx=False takes neither dx nor dx_base")
-    else:
-        dx = _out(dx, bf, (m, desc.k), "dx", dev)
-    da = _out(da, bf, (desc.num_adapters, desc.rank, desc.k), "da", dev)
-    db = _out(db, bf, (desc.num_adapters, desc.n, desc.rank), "db", dev)
+    if not need_dx and (dx is not None or dx_base is not None):
+        raise ValueError("need_dx=False takes neither dx nor dx_base")
+    m, dev, bf, f32 = x.shape[0], x.get_device(), torch.bfloat16, torch.float32
+    n, k, rank, L = desc.n, desc.k, desc.rank, desc.num_adapters
+    if need_dx and dx is None:
+        dx = _new(bf, (m, k), dev)
+    da = _new(bf, (L, rank, k), dev) if da is None else da
+    db = _new(bf, (L, n, rank), dev) if db is None else db
     wsp, wsb, ws = _ws(ws, hm_lora_grad_workspace_size, (desc, m), dev)
-    _ok("hm_lora_grad", lib.hm_lora_grad(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(h), _ptr(adapter_ids), _ptr(a),
-                                         _ptr(b), _ptr(scales), m, _ptr(dx_base), _ptr(dx), _ptr(da), _ptr(db),
-                                         wsp, wsb, _stream(stream)))
+    code = lib.hm_lora_grad(ctypes.byref(desc), _arg(dy, bf, (m, n), "dy", dev), _arg(x, bf, (m, k), "x", dev),
+                            _arg(h, f32, (m, rank), "h", dev), _arg(adapter_ids, torch.int32, (m,), "adapter_ids", dev),
+                            _arg(a, bf, (L, rank, k), "a", dev), _arg(b, bf, (L, n, rank), "b", dev),
+                            _arg(scales, f32, (L,), "scales", dev), m,
+                            None if dx_base is None else _arg(dx_base, bf, (m, k), "dx_base", dev),
+                            None if dx is None else _arg(dx, bf, (m, k), "dx", dev),
+                            _arg(da, bf, (L, rank, k), "da", dev), _arg(db, bf, (L, n, rank), "db", dev), wsp, wsb,
+                            _stream())
+    _ok("hm_lora_grad", code)
     return dx, da, db
 
 

@@ -59,7 +59,7 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
   const bool few = w.unit_rows == 16;
   const int rp = lora_rp(d->rank);
   const int64_t blocks = few ? w.max_units : w.max_units * (w.unit_rows / 32), waves = grad ? 8 : (few ? (rp == 128 ? 4 : (rp == 64 ? 8 : 16)) : 4);
-  const int64_t want = few ? 4096 / (blocks * waves) : 640 / blocks, most = std::min<int64_t>(grad || (few && rp == 128) ? kLoraMaxSplits : 4, len / (64 * waves));
+  const int64_t want = few ? 4096 / (blocks * waves) : 640 / blocks, most = std::min<int64_t>(lora_max_splits(rp, w.unit_rows, grad), len / (64 * waves));
   w.splits = (int)std::max<int64_t>(1, std::min(want, most));
   // expanding blocks: several units against one part of B where there are many, several parts of the columns where
   // there are many units of few rows

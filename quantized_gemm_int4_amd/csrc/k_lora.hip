@@ -449,8 +449,8 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
       }
     };
     if (g.splits == 1) stage(Int<1>{});
-    else if ((T > 1 && !TRANS) || g.splits <= 4) stage(Int<4>{});   // the planner's limits
-    else stage(Int<kLoraMaxSplits>{});
+    else if (lora_max_splits(RP, U, TRANS) == 4 || g.splits <= 4) stage(Int<4>{});
+    else stage(Int<8>{});
     __syncthreads();
     while (n0 < c1) {
 #pragma unroll

@@ -17,6 +17,7 @@ namespace hm {
 // the rank and the unit's rows.
 template <int RP>
 __global__ void __launch_bounds__(256) k_lora_pack(LoraGradArgs g) {
+  constexpr int MS = lora_max_splits(RP, kLoraUnit, true);
   __shared__ float v[32][RP + 1];
   const int u = blockIdx.x, half = blockIdx.z, count = g.R.units[2 * u + 1] - 32 * half;
   const bool is_h = blockIdx.y != 0;
@@ -28,15 +29,15 @@ __global__ void __launch_bounds__(256) k_lora_pack(LoraGradArgs g) {
   for (int i0 = 0; i0 < 32 * (RP / 4); i0 += 256) {
     const int i = i0 + threadIdx.x, row = i / (RP / 4), r = 4 * (i % (RP / 4));
     if (i >= 32 * (RP / 4)) break;
-    f32x4_t s = {0.f, 0.f, 0.f, 0.f}, p[kLoraMaxSplits];
+    f32x4_t s = {0.f, 0.f, 0.f, 0.f}, p[MS];
     if (row < count && r < g.rank) {
       const int64_t at = (int64_t)rows[row] * g.rank + r;
 #pragma unroll
-      for (int k = 0; k < kLoraMaxSplits; ++k)
+      for (int k = 0; k < MS; ++k)
         p[k] = *reinterpret_cast<const f32x4_t*>(src + (int64_t)min(k, splits - 1) * g.M * g.rank + at);
       loads_first();
 #pragma unroll
-      for (int k = 0; k < kLoraMaxSplits; ++k)
+      for (int k = 0; k < MS; ++k)
         if (k < splits) s += p[k];
     }
 #pragma unroll

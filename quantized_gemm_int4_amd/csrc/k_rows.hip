@@ -127,6 +127,7 @@ k_collect_grad(const uint16_t* __restrict__ dout, const uint16_t* ys, const floa
     }
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
+      if (j0 + j >= topk) break;
       for (int off = 32; off >= 1; off >>= 1) s[j] += __shfl_xor(s[j], off, 64);
       if (lane == 0) red[wave][j] = s[j];
     }

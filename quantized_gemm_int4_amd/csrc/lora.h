@@ -11,7 +11,6 @@ namespace hm {
 constexpr int64_t kLoraMaxRows = 1 << 20;
 constexpr int kLoraDirect = 64;      // most rows of a call whose blocks find their unit from the ids themselves
 constexpr int kLoraPlanBlocks = 256; // most blocks of the grouping kernel
-constexpr int kLoraMaxSplits = 8;    // most blocks along a contraction
 constexpr int kLoraUnit = 64;        // rows per unit of the gradient
 constexpr int kLoraCols = 256;       // output columns that an expanding block takes at a time
 
@@ -57,6 +56,11 @@ struct LoraGradArgs {
   LoraRows R;
 };
 
+// Most blocks along a contraction: an expanding block adds their sums with
+// all of them in flight, in registers that it has left.
+constexpr int lora_max_splits(int rp, int unit_rows, bool trans) {
+  return trans ? (rp == 128 ? 4 : 8) : (unit_rows == 16 && rp == 128 ? 8 : 4);
+}
 inline int lora_rp(int rank) { return rank <= 16 ? 16 : (rank <= 32 ? 32 : (rank <= 64 ? 64 : 128)); }
 
 // Grouping of M rows by adapter id (ids outside [0, L) are left out).
