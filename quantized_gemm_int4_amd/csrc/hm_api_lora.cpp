@@ -66,7 +66,7 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
   int64_t slabs = 8 * ((cols + 8 * kLoraCols - 1) / (8 * kLoraCols));
   w.group = w.direct || w.unit_rows < 64 ? 1 : (w.max_units * slabs >= 4096 ? 4 : (w.max_units * slabs >= 2048 ? 2 : 1));
   w.cols = kLoraCols;
-  while (few && w.max_units * slabs > 1024 && w.cols < 4 * kLoraCols && cols > 8 * w.cols) {
+  while (few && w.max_units * slabs > 2048 && w.cols < 4 * kLoraCols && cols > 8 * w.cols) {
     w.cols *= 2;
     slabs = 8 * ((cols + 8 * w.cols - 1) / (8 * w.cols));
   }

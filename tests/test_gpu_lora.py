@@ -22,7 +22,9 @@ TINY = 2.0 ** -120            # products of bf16 values that underflow in fp32, 
 # m, n, k, rank, adapters
 SHAPES = [(1, 1, 128, 8, 1), (1, 130, 256, 16, 3), (2, 16, 128, 128, 2), (5, 37, 256, 24, 3), (17, 64, 1152, 32, 17),
           (33, 130, 384, 40, 4), (64, 513, 128, 64, 2), (100, 256, 640, 96, 5), (130, 1023, 256, 128, 3),
-          (300, 88, 256, 48, 512), (257, 640, 512, 16, 1), (4500, 40, 128, 8, 7)]
+          (300, 88, 256, 48, 512), (257, 640, 512, 16, 1), (4500, 40, 128, 8, 7),
+          (16, 2500, 256, 64, 9), (150, 72, 256, 16, 6), (150, 300, 256, 32, 6), (150, 72, 128, 64, 6),
+          (1500, 200, 256, 128, 3), (1100, 130, 128, 64, 2), (48, 2600, 128, 16, 30)]
 
 
 def _bits(r, *shape, std=1.0):
@@ -233,7 +235,8 @@ def test_adapters_beside_the_low_bit_projection(m):
     _check_grad(c, got, n, rank)
 
 
-@pytest.mark.parametrize("m,n,k,rank,L", [(1, 14336, 4096, 16, 64), (48, 7168, 2048, 64, 64), (700, 4096, 7168, 32, 9)])
+@pytest.mark.parametrize("m,n,k,rank,L", [(1, 14336, 4096, 16, 64), (48, 7168, 2048, 64, 64), (700, 4096, 7168, 32, 9),
+                                              (64, 14336, 512, 16, 64), (300001, 24, 128, 8, 5), (20000, 256, 128, 32, 3)])
 def test_lora_layer_shapes_sampled(m, n, k, rank, L):
     """Layer-sized calls against fp64 products on the GPU; the second half of
     the adapters is not used by any row."""
