@@ -30,7 +30,12 @@ hm_status check_lora(const hm_lora_desc* d, int64_t m) {
 // Blocks of one launch stay under 2^24 (2^32 threads).
 constexpr int64_t kMaxBlocks = (1ll << 24) - 1;
 
-// Largest A (values) that every block of a call reads by itself.
+// Calls that run both products in one launch: up to 16 rows, and an A (of
+// padded rank) that every block can read by itself.  One launch against two,
+// and as a Python loop issues them (the host needs 3 us a launch): m = 1, k =
+// 2048, n = 7168, rank 16 6.6 against 7.6 us, 8.4 against 10.7; m = 8, k = 4096,
+// n = 14336, rank 16 7.9 against 8.2, 8.3 against 10.9; beyond: rank 64 (262144
+// values) 15.9 against 9.8, m = 48 13.8 against 12.1.
 constexpr int64_t kSmallA = 131072;
 constexpr int64_t kSmallRows = 16;
 
@@ -43,9 +48,11 @@ struct LoraPlan {
   bool direct;
 };
 
-// Rows per unit: 64 where the adapters have that many rows each on average
+// Rows per unit: 64 where the adapters can have that many rows each on average
 // (every loaded value of A and B then serves four MFMAs), fewer where units
-// would be mostly empty.
+// would be mostly empty: m = 256, 32 adapters of rank 64, k = 7168, n = 4096
+// 22.3 us with 16 rows, 26.4 with 64; m = 128, 40 of rank 128, k = 4096, n =
+// 7168 39.4 against 44.3.
 int rows_per_unit(int64_t m, int64_t L) { return m <= 16 * L ? 16 : (m <= 32 * L ? 32 : 64); }
 
 hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) {
@@ -55,16 +62,20 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
   w.unit_rows = grad ? kLoraUnit : (w.direct ? 16 : rows_per_unit(m, L));
   w.max_units = w.direct ? m : m / w.unit_rows + std::min<int64_t>(L, m);
   // blocks along the contraction: about 4096 waves in all (16-row units) or
-  // 640 blocks (32-row blocks), each wave keeping a step of 64 or more
+  // 640 blocks (32-row blocks; m = 8192, rank 64: 1024 blocks cost 5 us more in
+  // sums that the expansion reads again), each wave keeping a step of 64 or more
   const bool few = w.unit_rows == 16;
   const int rp = lora_rp(d->rank);
-  const int64_t blocks = few ? w.max_units : w.max_units * (w.unit_rows / 32), waves = grad ? 8 : (few ? (rp == 128 ? 4 : (rp == 64 ? 8 : 16)) : 4);
-  const int64_t want = few ? 4096 / (blocks * waves) : 640 / blocks, most = std::min<int64_t>(lora_max_splits(rp, w.unit_rows, grad), len / (64 * waves));
+  const int64_t blocks = few ? w.max_units : w.max_units * (w.unit_rows / 32);
+  const int64_t waves = lora_waves(rp, w.unit_rows, grad);
+  const int64_t want = few ? 4096 / (blocks * waves) : 640 / blocks;
+  const int64_t most = std::min<int64_t>(lora_max_splits(rp, w.unit_rows, grad), len / (64 * waves));
   w.splits = (int)std::max<int64_t>(1, std::min(want, most));
-  // expanding blocks: several units against one part of B where there are many, several parts of the columns where
-  // there are many units of few rows
+  // expanding blocks: two units against one part of B where there are many (m = 8192: 150 us, 151 with four, 165 with
+  // eight), several parts of the columns where there are many units of few rows (m = 48, n = 14336: 12.1 us with 512
+  // columns a block, 13.5 with 1024)
   int64_t slabs = 8 * ((cols + 8 * kLoraCols - 1) / (8 * kLoraCols));
-  w.group = w.direct || w.unit_rows < 64 ? 1 : (w.max_units * slabs >= 4096 ? 4 : (w.max_units * slabs >= 2048 ? 2 : 1));
+  w.group = w.direct || w.unit_rows < 64 ? 1 : (w.max_units * slabs >= 2048 ? 2 : 1);
   w.cols = kLoraCols;
   while (few && w.max_units * slabs > 2048 && w.cols < 4 * kLoraCols && cols > 8 * w.cols) {
     w.cols *= 2;
@@ -93,6 +104,7 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
     const size_t packed = (size_t)w.max_units * 2 * (size_t)lora_rp(d->rank) * kLoraUnit * 2;
     w.gt = take(packed);
     w.ht = take(packed);
+    // about 768 blocks, three to a compute unit (m = 8192, rank 32: 67 us; 512 78, 1024 72)
     const int64_t tiles = ((d->n + 127) / 128 + d->k / 128) * std::max(1, lora_rp(d->rank) / 32);
     w.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(16, std::min((767 + tiles) / tiles, w.max_units / 4)));
     w.sums = take(w.chunks > 1 ? (size_t)(2 * w.chunks) * (size_t)d->rank * (size_t)(d->k + d->n) * 4 : 0);

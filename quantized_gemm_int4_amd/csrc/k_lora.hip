@@ -170,10 +170,6 @@ template <int RP> struct BGroup {
   }
 };
 
-// Waves of a contracting block.
-constexpr int shrink_waves(int rp, int t, bool trans) {
-  return trans ? 8 : (t > 1 || rp == 128 ? 4 : (rp == 64 ? 8 : 16));
-}
 
 // A wave's private LDS image of 64 values of 16 rows: row r's 16-byte chunk k
 // (0 .. 7) sits at place k ^ (r & 7) of its 128 bytes, so that both the
@@ -187,12 +183,13 @@ __device__ __forceinline__ int chunk_at(int r, int k) { return r * 128 + ((k ^ (
 // neighbouring lanes read neighbouring bytes, while an MFMA operand has a row
 // per lane: loaded in operand order, sixteen lanes touch sixteen cache lines
 // of 16 bytes each and the address unit, not HBM, sets the pace (m = 8192, k =
-// 4096, rank 64: 50 us).  So a wave loads eight whole lines per instruction
+// 4096, rank 64: 50 us; now 25 us, of which reading x at the copy rate takes
+// 13.  dy with n = 14336, rank 32: 41 us, 5.7 TB/s).  So a wave loads eight whole lines per instruction
 // into registers, one step ahead, and passes them through its own LDS image;
 // no block barrier.
-template <int RP, int T, bool DIRECT, bool TRANS>
-__global__ void __launch_bounds__(64 * shrink_waves(RP, T, TRANS)) k_lora_shrink(LoraArgs g) {
-  constexpr int RB = RP / 16, LD = RP + 4, U = 16 * T, NW = shrink_waves(RP, T, TRANS);
+template <int RP, int T, bool DIRECT, bool TRANS, int NW>
+__global__ void __launch_bounds__(64 * NW) k_lora_shrink(LoraArgs g) {
+  constexpr int RB = RP / 16, LD = RP + 4, U = 16 * T;
   constexpr int TILES = TRANS ? T : T + RB;                   // 16-row tiles staged per step
   // LDS: the waves' images, then the sums (one per wave while that is small, else one for several waves in turn)
   constexpr int IMG = TILES * 2048, FIT = 72 * 1024 / (U * LD * 4);
@@ -348,7 +345,7 @@ __device__ __forceinline__ void copy_rest(const LoraArgs& g, int64_t m0, int64_t
 // ends up with columns 4 c .. 4 c + 3 of rows 4 q + v: sixteen lanes read base
 // and write y 128 consecutive bytes at a time (with the rows along the lanes
 // instead, 16 bytes each, the address unit bound the kernel: m = 8192, n =
-// 14336, rank 64 132 us).  Blocks go round the XCDs one by one, so block id i takes columns i % 8 + 8 k: each XCD sees
+// 14336, rank 64 132 us; now 107 us, 4.4 TB/s of base and y).  Blocks go round the XCDs one by one, so block id i takes columns i % 8 + 8 k: each XCD sees
 // an eighth of B_e, which stays in its L2 from group to group.
 template <int RP, int T, bool DIRECT, bool TRANS>
 __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
@@ -359,7 +356,7 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
   const int64_t N = TRANS ? g.K : g.N;
   const int per = (int)((N + 8 * g.cols - 1) / (8 * g.cols));             // column slabs per XCD
   const uint32_t id = blockIdx.x >> 3;
-  const int gi = (int)(id / per), slab = (int)(blockIdx.x & 7) + 8 * (int)(id % per);
+  const int gi = (int)(id / per), slab = (int)(blockIdx.x & 7) * per + (int)(id % per);
   const int64_t c0 = (int64_t)slab * g.cols, c1 = min(c0 + g.cols, N);
   if (c0 >= N) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
@@ -647,12 +644,12 @@ template <int RP, bool TRANS>
 static void run_shrink(const LoraArgs& g, bool direct, hipStream_t st) {
   const int t = direct || g.R.unit_rows == 16 ? 1 : 2;
   const dim3 grid((unsigned)g.splits, (unsigned)(direct ? g.M : g.R.max_units * (g.R.unit_rows / (16 * t))));
-  const dim3 block(64u * (unsigned)shrink_waves(RP, t, TRANS));
+  constexpr int W1 = lora_waves(RP, 16, false), W2 = lora_waves(RP, 64, TRANS);
   if constexpr (!TRANS) {
-    if (direct) hipLaunchKernelGGL((k_lora_shrink<RP, 1, true, false>), grid, block, 0, st, g);
-    else if (t == 1) hipLaunchKernelGGL((k_lora_shrink<RP, 1, false, false>), grid, block, 0, st, g);
+    if (direct) hipLaunchKernelGGL((k_lora_shrink<RP, 1, true, false, W1>), grid, dim3(64 * W1), 0, st, g);
+    else if (t == 1) hipLaunchKernelGGL((k_lora_shrink<RP, 1, false, false, W1>), grid, dim3(64 * W1), 0, st, g);
   }
-  if (t == 2) hipLaunchKernelGGL((k_lora_shrink<RP, 2, false, TRANS>), grid, block, 0, st, g);
+  if (t == 2) hipLaunchKernelGGL((k_lora_shrink<RP, 2, false, TRANS, W2>), grid, dim3(64 * W2), 0, st, g);
 }
 
 template <int RP, bool TRANS>

@@ -5,7 +5,9 @@
 // the strided axis of x and dy: a lane loads eight rows of eight neighbouring
 // columns and transposes them in its registers, each column being one MFMA's
 // operand.  g and h are small; a packing pass brings them into operand order
-// once (as two bf16 terms), because every column tile reads them again.
+// once (as two bf16 terms), because every column tile reads them again (read
+// in their own order, 64 cache lines an access, they bound the kernel: m =
+// 8192, n = 14336, k = 4096, rank 32 189 us; now 68 us, 4.4 TB/s of dy and x).
 #include "lora.h"
 
 namespace hm {

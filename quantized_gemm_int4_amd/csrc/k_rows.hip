@@ -8,7 +8,11 @@
 //                  dw[p] = sum_c dout[p / topk][c] ys[positions[p]][c]
 // All three only move bf16 rows: every row of the token side is read (or
 // written) once and every row of the expert side once, so they are bound by
-// HBM, and calls of few tokens by their launches and round trips.
+// HBM, and calls of few tokens by their launches and round trips.  Measured at
+// n = 7168, topk = 8 (a 1 GiB device copy runs at 5.08 TB/s, read and written
+// bytes together): dispatch t = 8192 205 us, 5.1 TB/s; collect and the
+// dispatch's gradient t = 4096 103 us, 5.1 TB/s; collect's gradient t = 4096
+// 199 us, 5.0 TB/s; t = 64 dispatch 5.9 us, collect 4.0 us.
 #include "common.h"
 #include "launch.h"
 #include "rows.h"
@@ -155,8 +159,8 @@ __device__ __forceinline__ int write_offsets(int total, int E, int* wsum, int32_
   return end - total;
 }
 
-// The stable expert sort of hm_moe_sort with its inverse, in one launch for
-// up to kSortDispatch pairs: every block counts all ids (and those before its
+// The stable expert sort of hm_moe_sort with its inverse, in one launch (up to
+// kSortDispatch pairs): every block counts all ids (and those before its
 // own 1024), as k_lora_plan does.
 __global__ void __launch_bounds__(kSortThreads)
 k_dispatch_sort(const int32_t* __restrict__ ids, int64_t P, int E, int32_t* __restrict__ counts,

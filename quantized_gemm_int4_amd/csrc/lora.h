@@ -9,7 +9,11 @@
 namespace hm {
 
 constexpr int64_t kLoraMaxRows = 1 << 20;
-constexpr int kLoraDirect = 64;      // most rows of a call whose blocks find their unit from the ids themselves
+// Most rows of a call whose blocks find their unit from the ids themselves (one
+// ballot holds them all) instead of from a grouping launch: m = 48, 24 adapters
+// of rank 16, k = 4096, n = 14336 12.1 us against 16.8; m = 64, 40 of rank 64, k
+// = 2048, n = 7168 17.3 against 22.1.
+constexpr int kLoraDirect = 64;
 constexpr int kLoraPlanBlocks = 256; // most blocks of the grouping kernel
 constexpr int kLoraUnit = 64;        // rows per unit of the gradient
 constexpr int kLoraCols = 256;       // output columns that an expanding block takes at a time
@@ -60,6 +64,13 @@ struct LoraGradArgs {
 // all of them in flight, in registers that it has left.
 constexpr int lora_max_splits(int rp, int unit_rows, bool trans) {
   return trans ? (rp == 128 ? 4 : 8) : (unit_rows == 16 && rp == 128 ? 8 : 4);
+}
+// Waves of a contracting block: sixteen-row units take as many as their LDS
+// images allow, each with little to do; 32-row blocks of A four, so that two
+// or three blocks fit a compute unit (m = 8192, k = 4096, rank 64: 25 us, 34
+// with eight).
+constexpr int lora_waves(int rp, int unit_rows, bool trans) {
+  return trans ? 8 : (unit_rows > 16 || rp == 128 ? 4 : (rp == 64 ? 8 : 16));
 }
 inline int lora_rp(int rank) { return rank <= 16 ? 16 : (rank <= 32 ? 32 : (rank <= 64 ? 64 : 128)); }
 
