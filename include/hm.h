@@ -445,8 +445,9 @@ hm_status hm_moe_collect(const uint16_t* ys, const float* w, const int32_t* posi
  *   dout bf16 [t][n]; ys, dys bf16 [t*topk][n]; w, dw fp32 [t][topk].  dys may
  *   be ys itself (each row is read before it is written); otherwise no
  *   overlaps.
- * For all three: any n >= 1, t = 0 is a no-op, bf16 arrays 16-byte aligned,
- * fp32 and int32 arrays 4-byte; topk >= 1, t*topk < 2^31. */
+ * For these three: any n in 1 .. 2^24, t = 0 is a no-op, bf16 arrays 16-byte
+ * aligned, fp32 and int32 arrays 4-byte; topk >= 1, t*topk < 2^31.  For all
+ * four: t < 2^24 and t * ceil(n / 512) < 2^26 (HM_ERR_SHAPE otherwise). */
 hm_status hm_moe_collect_grad(const uint16_t* dout, const uint16_t* ys, const float* w,
                               const int32_t* positions, int64_t t, int32_t topk, int64_t n, uint16_t* dys,
                               float* dw, hipStream_t stream);
@@ -482,7 +483,8 @@ hm_status hm_lora_workspace_size(const hm_lora_desc* d, int64_t m, size_t* bytes
  *   y           bf16 [m][n]; must not overlap base in any other way.
  *   h           fp32 [m][rank], what hm_lora_grad needs; NULL if not wanted.
  *   ws          hm_lora_workspace_size bytes, overwritten.
- * m = 0 is a no-op; m up to 1048576 (HM_ERR_SHAPE above). */
+ * m = 0 is a no-op; m up to 1048576, and m * n up to about 10^11 (a launch's
+ * blocks; the size query and the call agree): HM_ERR_SHAPE above. */
 hm_status hm_lora(const hm_lora_desc* d, const uint16_t* x, const int32_t* adapter_ids, const uint16_t* a,
                   const uint16_t* b, const float* scales, int64_t m, const uint16_t* base, uint16_t* y,
                   float* h, void* ws, size_t ws_bytes, hipStream_t stream);
@@ -505,7 +507,7 @@ hm_status hm_lora_grad_workspace_size(const hm_lora_desc* d, int64_t m, size_t* 
  *   da          bf16 [num_adapters][rank][k];  db bf16 [num_adapters][n][rank];
  *               adapters that no row names get zeros.
  *   ws          hm_lora_grad_workspace_size bytes, overwritten.
- * m = 0 writes zeros to da and db; m up to 1048576. */
+ * m = 0 writes zeros to da and db; limits as hm_lora. */
 hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const uint16_t* x, const float* h,
                        const int32_t* adapter_ids, const uint16_t* a, const uint16_t* b, const float* scales,
                        int64_t m, const uint16_t* dx_base, uint16_t* dx, uint16_t* da, uint16_t* db, void* ws,
