@@ -436,6 +436,12 @@ def _arg(t, dtype, shape, name, dev):
     return t.data_ptr()
 
 
+def _dims(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: need a 2-dimensional tensor")
+    return t.shape
+
+
 def _new(dtype, shape, dev):
     return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
 
@@ -472,7 +478,8 @@ def hm_moe_dispatch(x, topk_ids, num_experts, xs=None, counts=None, offsets=None
     if ctx is not None:
         with ctx:
             return hm_moe_dispatch(x, topk_ids, num_experts, xs, counts, offsets, sorted_pairs, positions, ws)
-    (t, n), topk, dev, bf, i32 = x.shape, topk_ids.shape[1], x.get_device(), torch.bfloat16, torch.int32
+    (t, n), (_, topk), dev = _dims(x, "x"), _dims(topk_ids, "topk_ids"), x.get_device()
+    bf, i32 = torch.bfloat16, torch.int32
     E = int(num_experts)
     xs = _new(bf, (t * topk, n), dev) if xs is None else xs
     counts = _new(i32, (E,), dev) if counts is None else counts
@@ -496,7 +503,7 @@ def hm_moe_dispatch_grad(dxs, positions, dx=None, stream=None):
     if ctx is not None:
         with ctx:
             return hm_moe_dispatch_grad(dxs, positions, dx)
-    (t, topk), n, dev, bf = positions.shape, dxs.shape[1], dxs.get_device(), torch.bfloat16
+    (t, topk), (_, n), dev, bf = _dims(positions, "positions"), _dims(dxs, "dxs"), dxs.get_device(), torch.bfloat16
     dx = _new(bf, (t, n), dev) if dx is None else dx
     code = lib.hm_moe_dispatch_grad(_arg(dxs, bf, (t * topk, n), "dxs", dev),
                                     _arg(positions, torch.int32, (t, topk), "positions", dev), t, topk, n,
@@ -512,7 +519,7 @@ def hm_moe_collect(ys, weights, positions, out=None, stream=None):
     if ctx is not None:
         with ctx:
             return hm_moe_collect(ys, weights, positions, out)
-    (t, topk), n, dev, bf = positions.shape, ys.shape[1], ys.get_device(), torch.bfloat16
+    (t, topk), (_, n), dev, bf = _dims(positions, "positions"), _dims(ys, "ys"), ys.get_device(), torch.bfloat16
     out = _new(bf, (t, n), dev) if out is None else out
     code = lib.hm_moe_collect(_arg(ys, bf, (t * topk, n), "ys", dev),
                               _arg(weights, torch.float32, (t, topk), "weights", dev),
@@ -530,7 +537,8 @@ def hm_moe_collect_grad(dout, ys, weights, positions, dys=None, dweights=None, s
     if ctx is not None:
         with ctx:
             return hm_moe_collect_grad(dout, ys, weights, positions, dys, dweights)
-    (t, topk), n, dev, bf, f32 = positions.shape, dout.shape[1], dout.get_device(), torch.bfloat16, torch.float32
+    (t, topk), (_, n), dev = _dims(positions, "positions"), _dims(dout, "dout"), dout.get_device()
+    bf, f32 = torch.bfloat16, torch.float32
     if dys is None:
         dys = torch.zeros(t * topk, n, dtype=bf, device=dout.device)
     dweights = _new(f32, (t, topk), dev) if dweights is None else dweights
@@ -569,7 +577,7 @@ def hm_lora(desc, x, adapter_ids, a, b, scales, base=None, y=None, h=None, ws=No
     if ctx is not None:
         with ctx:
             return hm_lora(desc, x, adapter_ids, a, b, scales, base, y, h, ws)
-    m, dev, bf, f32 = x.shape[0], x.get_device(), torch.bfloat16, torch.float32
+    (m, _), dev, bf, f32 = _dims(x, "x"), x.get_device(), torch.bfloat16, torch.float32
     n, k, rank, L = desc.n, desc.k, desc.rank, desc.num_adapters
     y = _new(bf, (m, n), dev) if y is None else y
     wsp, wsb, ws = _ws(ws, hm_lora_workspace_size, (desc, m), dev)
@@ -594,7 +602,7 @@ def hm_lora_grad(desc, dy, x, h, adapter_ids, a, b, scales, dx_base=None, dx=Non
             return hm_lora_grad(desc, dy, x, h, adapter_ids, a, b, scales, dx_base, dx, da, db, need_dx, ws)
     if not need_dx and (dx is not None or dx_base is not None):
         raise ValueError("need_dx=False takes neither dx nor dx_base")
-    m, dev, bf, f32 = x.shape[0], x.get_device(), torch.bfloat16, torch.float32
+    (m, _), dev, bf, f32 = _dims(x, "x"), x.get_device(), torch.bfloat16, torch.float32
     n, k, rank, L = desc.n, desc.k, desc.rank, desc.num_adapters
     if need_dx and dx is None:
         dx = _new(bf, (m, k), dev)

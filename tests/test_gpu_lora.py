@@ -214,6 +214,32 @@ def test_lora_in_a_graph_and_one_workspace_for_many_calls(m):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("m", [2, 50, 400])
+def test_lora_calls_on_two_streams_at_once(m):
+    """Two streams run forward and gradient of different rows side by side,
+    each with buffers of its own; the bits are those of the same calls alone."""
+    import quantized_gemm_int4_amd as hm
+    n, k, rank, L = 300, 512, 32, 4
+    d = hm.lora_desc(n, k, rank, L)
+    cases = [_dev(_case(m, n, k, rank, L, seed=20 + i)) for i in range(2)]
+
+    def step(t, stream=None):
+        h = torch.zeros(m, rank, device="cuda") if stream is None else t["hbuf"]
+        y = hm.hm_lora(d, t["x"], t["ids"], t["a"], t["b"], t["s"], base=t["base"], h=h, stream=stream)
+        return (y,) + hm.hm_lora_grad(d, t["dy"], t["x"], h, t["ids"], t["a"], t["b"], t["s"], stream=stream)
+
+    want = [step(t) for t in cases]
+    for t in cases:
+        t["hbuf"] = torch.zeros(m, rank, device="cuda")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[step(t, s) for t, s in zip(cases, streams)] for _ in range(5)][-1]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for a, b in zip(w, g):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
 @pytest.mark.parametrize("m", [1, 20, 300])
 def test_adapters_beside_the_low_bit_projection(m):
     """As a layer runs: the shared INT4 projection, the adapters added in

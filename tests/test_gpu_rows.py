@@ -139,7 +139,8 @@ def test_rows_no_tokens_and_refusals():
                 lambda: hm.hm_moe_dispatch(x, ids.long(), 4), lambda: hm.hm_moe_dispatch(x, ids[:3], 4),
                 lambda: hm.hm_moe_dispatch(x, ids, 4, xs=ys[:7]), lambda: hm.hm_moe_collect(ys[:7], w, ids),
                 lambda: hm.hm_moe_collect(ys, w.double(), ids), lambda: hm.hm_moe_collect_grad(x[:3], ys, w, ids),
-                lambda: hm.hm_moe_collect_grad(x, ys, w, ids, dys=x), lambda: hm.hm_moe_dispatch_grad(x, ids)):
+                lambda: hm.hm_moe_collect_grad(x, ys, w, ids, dys=x), lambda: hm.hm_moe_dispatch_grad(x, ids),
+                lambda: hm.hm_moe_dispatch(x, ids.flatten(), 4), lambda: hm.hm_moe_dispatch_grad(ys, ids.flatten())):
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(hm.HmError):
