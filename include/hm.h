@@ -394,7 +394,8 @@ hm_status hm_moe_combine(const uint16_t* y, const float* w, int64_t t, int32_t t
 
 /* ------------------------------------------------ MoE rows in expert order */
 
-/* Workspace bytes hm_moe_dispatch needs (that of hm_moe_sort; may be 0). */
+/* Workspace bytes hm_moe_dispatch needs: 0 up to 32768 pairs, else those of
+ * hm_moe_sort. */
 hm_status hm_moe_dispatch_workspace_size(int64_t t, int32_t topk, int32_t num_experts, size_t* bytes);
 
 /* Tokens sorted by expert: the stable order of hm_moe_sort and the token rows

@@ -42,7 +42,7 @@ struct LoraArgs {
   float* h;                  // [M][rank]: written by the forward if not null
   float* part;               // fp32 [splits][M][rank] contracted values
   int splits;
-  int group, cols;           // units and columns per expanding block; one of them is more than a unit, kLoraCols
+  int group, cols;           // units and columns per expanding block (one unit, or kLoraCols columns)
   LoraRows R;
 };
 

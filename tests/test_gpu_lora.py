@@ -292,3 +292,35 @@ def test_lora_layer_shapes_sampled(m, n, k, rank, L):
                                      (db[e], D.t() @ H, ab(D.t(), H), m)):
             err = bnd * (2.0 ** -16 + (terms + 64) * 2.0 ** -23)
             assert ((got.to(f) - ref).abs() <= U * (ref.abs() + err) + err).all()
+
+
+def test_lora_rows_beyond_4gib():
+    """base, y and dy past 2^32 bytes: the last rows of y, and db of some
+    columns (a sum over every row), against fp64."""
+    import quantized_gemm_int4_amd as hm
+    m, n, k, rank, L = 160000, 14336, 128, 8, 2                 # 4.6 GB of y
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)     # noqa: E731
+    x, a, b, y, s = rn(m, k), rn(L, rank, k), rn(L, n, rank), rn(m, n), torch.ones(L, device="cuda")
+    ids = torch.arange(m, device="cuda", dtype=torch.int32) % 3 - 1                       # a third without an adapter
+    d, h, f = hm.lora_desc(n, k, rank, L), torch.empty(m, rank, device="cuda"), torch.float64
+    last = slice(m - 300, m)
+    base = y[last].clone()
+    hm.hm_lora(d, x, ids, a, b, s, base=y, y=y, h=h)
+    e = ids[last].long().clamp(min=0)
+    on = (ids[last] >= 0).to(f)[:, None]
+    hr = on * torch.stack([a[i].to(f) @ v.to(f) for i, v in zip(e, x[last])])
+    hb = on * torch.stack([a[i].to(f).abs() @ v.to(f).abs() for i, v in zip(e, x[last])])
+    ref = base.to(f) + torch.stack([b[i].to(f) @ v for i, v in zip(e, hr)])
+    bnd = base.to(f).abs() + torch.stack([b[i].to(f).abs() @ v for i, v in zip(e, hb)])
+    err = bnd * (2.0 ** -16 + (k + 2 * rank + 64) * 2.0 ** -23)
+    assert ((y[last].to(f) - ref).abs() <= U * (ref.abs() + err) + err).all()
+    _, _, db = hm.hm_lora_grad(d, y, x, h, ids, a, b, s, need_dx=False)
+    cols = torch.tensor([0, 1, 129, n - 1], device="cuda")
+    for i in range(L):
+        r = (ids == i).nonzero()[:, 0]
+        dy = y[r][:, cols].to(f)
+        ref, bnd = dy.t() @ h[r].to(f), dy.t().abs() @ h[r].to(f).abs()
+        # the terms of one sum are added in four waves' and sixteen chunks' pieces of 32 rows a step
+        err = bnd * (2.0 ** -16 + (m + 64) * 2.0 ** -23)
+        assert ((db[i][cols].to(f) - ref).abs() <= U * (ref.abs() + err) + err).all()
