@@ -81,7 +81,9 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
     w.cols *= 2;
     slabs = 8 * ((cols + 8 * w.cols - 1) / (8 * w.cols));
   }
-  if (slabs * ((w.max_units + w.group - 1) / w.group + (m + 63) / 64) > kMaxBlocks) return HM_ERR_SHAPE;
+  int64_t launch = slabs * ((w.max_units + w.group - 1) / w.group + (m + 63) / 64);
+  if (grad) launch += 4 * w.max_units + L * lora_zero_parts(d->rank, d->k, d->n) + 16;
+  if (launch > kMaxBlocks) return HM_ERR_SHAPE;
   if (!grad && m <= kSmallRows && d->rank <= 64 && (int64_t)lora_rp(d->rank) * d->k <= kSmallA) {
     const int64_t waves = d->rank > 32 ? 8 : 16, most = (d->n + 64 * waves - 1) / (64 * waves);
     w.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, 256 / m));
@@ -104,7 +106,8 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
     const size_t packed = (size_t)w.max_units * 2 * (size_t)lora_rp(d->rank) * kLoraUnit * 2;
     w.gt = take(packed);
     w.ht = take(packed);
-    // about 768 blocks, three to a compute unit (m = 8192, rank 32: 67 us; 512 78, 1024 72)
+    // about 768 blocks, three to a compute unit (m = 8192, rank 32: 67 us; 512 78, 1024 72), a chunk of four units or
+    // more (m = 777, rank 16: 32.4 us a call; of sixteen 37.3)
     const int64_t tiles = ((d->n + 127) / 128 + d->k / 128) * std::max(1, lora_rp(d->rank) / 32);
     w.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(16, std::min((767 + tiles) / tiles, w.max_units / 4)));
     w.sums = take(w.chunks > 1 ? (size_t)(2 * w.chunks) * (size_t)d->rank * (size_t)(d->k + d->n) * 4 : 0);
@@ -183,7 +186,7 @@ HM_API hm_status hm_lora(const hm_lora_desc* d, const uint16_t* x, const int32_t
   if (h && w.splits == 1) g.part = h;
   hipError_t e = w.direct ? hipSuccess : group_rows(d, adapter_ids, m, w, (uint8_t*)ws, &g.R, stream);
   if (e == hipSuccess) e = launch_lora_shrink(g, w.direct, false, stream);
-  if (e == hipSuccess) e = launch_lora_expand(g, w.direct, false, stream);
+  if (e == hipSuccess) e = launch_lora_expand(g, w.direct, stream);
   return e == hipSuccess ? HM_OK : HM_ERR_HIP;
 }
 
@@ -209,7 +212,7 @@ HM_API hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const u
   o.L = d->num_adapters;
   o.da = da;
   o.db = db;
-  if (m == 0) return launch_lora_sums(o, stream) == hipSuccess ? HM_OK : HM_ERR_HIP;
+  if (m == 0) return launch_lora_dx(LoraArgs{}, o, stream) == hipSuccess ? HM_OK : HM_ERR_HIP;
   if (!dy || !x || !h || !adapter_ids || !a || !b || !scales) return HM_ERR_NULL;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(h, 16) || !aligned(a, 16) || !aligned(b, 16) ||
       !aligned(dx_base, 16) || !aligned(dx, 16) || !aligned(adapter_ids, 4) || !aligned(scales, 4))
@@ -223,7 +226,6 @@ HM_API hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const u
   LoraArgs g = args_of(d, dy, adapter_ids, a, b, scales, m, dx_base, dx, w, at);
   hipError_t e = group_rows(d, adapter_ids, m, w, at, &g.R, stream);
   if (e == hipSuccess) e = launch_lora_shrink(g, false, true, stream);
-  if (e == hipSuccess && dx) e = launch_lora_expand(g, false, true, stream);
   o.part = g.part;
   o.splits = w.splits;
   o.gt = (uint16_t*)(at + w.gt);
@@ -231,8 +233,8 @@ HM_API hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const u
   o.sums = (float*)(at + w.sums);
   o.chunks = w.chunks;
   o.R = g.R;
-  if (e == hipSuccess) e = launch_lora_pack(o, stream);
+  if (e == hipSuccess) e = launch_lora_dx(g, o, stream);
   if (e == hipSuccess) e = launch_lora_outer(o, stream);
-  if (e == hipSuccess) e = launch_lora_sums(o, stream);
+  if (e == hipSuccess && w.chunks > 1) e = launch_lora_sums(o, stream);
   return e == hipSuccess ? HM_OK : HM_ERR_HIP;
 }

@@ -4,63 +4,13 @@
 // (g and dx are k_lora.hip's).  The contraction runs over the rows, which are
 // the strided axis of x and dy: a lane loads eight rows of eight neighbouring
 // columns and transposes them in its registers, each column being one MFMA's
-// operand.  g and h are small; a packing pass brings them into operand order
+// operand.  g and h are small; a packing pass (k_lora_dx's) brings them into operand order
 // once (as two bf16 terms), because every column tile reads them again (read
 // in their own order, 64 cache lines an access, they bound the kernel: m =
 // 8192, n = 14336, k = 4096, rank 32 189 us; now 68 us, 4.4 TB/s of dy and x).
 #include "lora.h"
 
 namespace hm {
-
-// grid (units, 2, 2): g (the splits' sums; y = 0) or h (y = 1) of 32 of a unit's rows
-// in the order of the outer product's operands, so that a wave loads each
-// with one contiguous access: [32-row step][hi, lo][16-rank block][lane][8],
-// lane (c, q) holding rank 16 k + c of rows 32 s + 8 q .. + 7; zeros beyond
-// the rank and the unit's rows.
-template <int RP>
-__global__ void __launch_bounds__(256) k_lora_pack(LoraGradArgs g) {
-  constexpr int MS = lora_max_splits(RP, kLoraUnit, true);
-  __shared__ float v[32][RP + 1];
-  const int u = blockIdx.x, half = blockIdx.z, count = g.R.units[2 * u + 1] - 32 * half;
-  const bool is_h = blockIdx.y != 0;
-  if (count <= 0) return;                                     // unused units and steps are not read
-  const int32_t* rows = g.R.rows + (int64_t)u * kLoraUnit + 32 * half;
-  const float* src = is_h ? g.h : g.part;
-  const int splits = is_h ? 1 : g.splits;
-#pragma unroll
-  for (int i0 = 0; i0 < 32 * (RP / 4); i0 += 256) {
-    const int i = i0 + threadIdx.x, row = i / (RP / 4), r = 4 * (i % (RP / 4));
-    if (i >= 32 * (RP / 4)) break;
-    f32x4_t s = {0.f, 0.f, 0.f, 0.f}, p[MS];
-    if (row < count && r < g.rank) {
-      const int64_t at = (int64_t)rows[row] * g.rank + r;
-#pragma unroll
-      for (int k = 0; k < MS; ++k)
-        p[k] = *reinterpret_cast<const f32x4_t*>(src + (int64_t)min(k, splits - 1) * g.M * g.rank + at);
-      loads_first();
-#pragma unroll
-      for (int k = 0; k < MS; ++k)
-        if (k < splits) s += p[k];
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[row][r + k] = s[k];
-  }
-  __syncthreads();
-  uint16_t* out = (is_h ? g.ht : g.gt) + ((int64_t)u * 2 + half) * 2 * RP * 32;
-  for (int i = threadIdx.x; i < RP * 4; i += 256) {
-    const int lane = i & 63, k = i >> 6, r = 16 * k + (lane & 15), m = 8 * (lane >> 4);
-    u32x4_t hi, lo;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      uint32_t h2, l2;
-      split2(v[m + 2 * p][r], v[m + 2 * p + 1][r], &h2, &l2);
-      hi[p] = h2;
-      lo[p] = l2;
-    }
-    st16(out + 8 * i, hi);
-    st16(out + RP * 32 + 8 * i, lo);
-  }
-}
 
 __device__ __forceinline__ int chunk_units(const LoraGradArgs& g) {
   return (g.R.first[g.L] + g.chunks - 1) / g.chunks;
@@ -211,35 +161,23 @@ __global__ void __launch_bounds__(256, 2) k_lora_outer(LoraGradArgs g) {
 }
 
 // grid (eight values per thread of an adapter's da and db, adapters): sums of
-// the partial sums in chunk order, zeros for adapters without rows.
+// the partial sums in chunk order for adapters that reach over chunks.
 __global__ void __launch_bounds__(256) k_lora_sums(LoraGradArgs g) {
   const int e = blockIdx.y;
   const int64_t i = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x), na = (int64_t)g.rank * g.K, nb = (int64_t)g.rank * g.N;
   if (i >= na + nb) return;
+  const int u0 = g.R.first[e], u1 = g.R.first[e + 1];
+  if (u0 == u1) return;                                       // zeros, written beside dx
+  const int per = chunk_units(g), j0 = u0 / per, j1 = (u1 - 1) / per;
+  if (j0 == j1) return;                                       // written whole
   f32x4_t a = {0.f, 0.f, 0.f, 0.f}, b = {0.f, 0.f, 0.f, 0.f};
-  const int u0 = g.M ? g.R.first[e] : 0, u1 = g.M ? g.R.first[e + 1] : 0;
-  if (u1 > u0) {
-    const int per = chunk_units(g), j0 = u0 / per, j1 = (u1 - 1) / per;
-    if (j0 == j1) return;                                     // written whole
-    for (int j = j0; j <= j1; ++j) {
-      const float* p = g.sums + (int64_t)(2 * j + (j == j0 ? 1 : 0)) * (na + nb) + i;
-      a += *reinterpret_cast<const f32x4_t*>(p);
-      b += *reinterpret_cast<const f32x4_t*>(p + 4);
-    }
+  for (int j = j0; j <= j1; ++j) {
+    const float* p = g.sums + (int64_t)(2 * j + (j == j0 ? 1 : 0)) * (na + nb) + i;
+    a += *reinterpret_cast<const f32x4_t*>(p);
+    b += *reinterpret_cast<const f32x4_t*>(p + 4);
   }
   st16(i < na ? g.da + e * na + i : g.db + e * nb + i - na,
        (u32x4_t){pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])});
-}
-
-hipError_t launch_lora_pack(const LoraGradArgs& g, hipStream_t st) {
-  const dim3 grid((unsigned)g.R.max_units, 2, 2);
-  switch (lora_rp(g.rank)) {
-    case 16: hipLaunchKernelGGL(k_lora_pack<16>, grid, dim3(256), 0, st, g); break;
-    case 32: hipLaunchKernelGGL(k_lora_pack<32>, grid, dim3(256), 0, st, g); break;
-    case 64: hipLaunchKernelGGL(k_lora_pack<64>, grid, dim3(256), 0, st, g); break;
-    default: hipLaunchKernelGGL(k_lora_pack<128>, grid, dim3(256), 0, st, g);
-  }
-  return hipGetLastError();
 }
 
 hipError_t launch_lora_outer(const LoraGradArgs& g, hipStream_t st) {

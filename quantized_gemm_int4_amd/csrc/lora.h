@@ -53,7 +53,7 @@ struct LoraGradArgs {
   int splits;
   int64_t M, N, K;
   int rank, L;
-  uint16_t *gt, *ht;         // packed g and h, 2 RP kLoraUnit values a unit (k_lora_pack)
+  uint16_t *gt, *ht;         // packed g and h, 2 RP kLoraUnit values a unit (pack_block)
   float* sums;               // partial sums [2 chunks][rank (K + N)]
   int chunks;
   uint16_t *da, *db;
@@ -74,17 +74,24 @@ constexpr int lora_waves(int rp, int unit_rows, bool trans) {
 }
 inline int lora_rp(int rank) { return rank <= 16 ? 16 : (rank <= 32 ? 32 : (rank <= 64 ? 64 : 128)); }
 
+// Blocks that write an adapter's zero gradients: 16384 values each, at most 64.
+inline int lora_zero_parts(int rank, int64_t K, int64_t N) {
+  const int64_t parts = (rank * (K + N) + 16383) / 16384;
+  return (int)(parts < 64 ? parts : 64);
+}
+
 // Grouping of M rows by adapter id (ids outside [0, L) are left out).
 hipError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, int unit_rows, int64_t max_units, int32_t* units,
                             int32_t* rows, int32_t* first, hipStream_t st);
 // part = scale * (A z) or, trans, scale * (B^T z).  direct: units found from
 // the ids by every block (M <= kLoraDirect, 16 rows a unit).
 hipError_t launch_lora_shrink(const LoraArgs& g, bool direct, bool trans, hipStream_t st);
-// y = base + B h or, trans, base + A^T g.
-hipError_t launch_lora_expand(const LoraArgs& g, bool direct, bool trans, hipStream_t st);
+// y = base + B h.
+hipError_t launch_lora_expand(const LoraArgs& g, bool direct, hipStream_t st);
 // both forward products in one launch (M <= kLoraDirect, rank <= 64)
 hipError_t launch_lora_small(const LoraArgs& g, int parts, hipStream_t st);
-hipError_t launch_lora_pack(const LoraGradArgs& g, hipStream_t st);
+// packed g and h, zeros for adapters without rows, and (g.y not null) y = base + A^T g
+hipError_t launch_lora_dx(const LoraArgs& g, const LoraGradArgs& o, hipStream_t st);
 hipError_t launch_lora_outer(const LoraGradArgs& g, hipStream_t st);
 hipError_t launch_lora_sums(const LoraGradArgs& g, hipStream_t st);
 

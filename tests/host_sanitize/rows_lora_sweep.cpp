@@ -95,14 +95,17 @@ hipError_t launch_lora_shrink(const LoraArgs& g, bool direct, bool trans, hipStr
   ++g_launches;
   return hipSuccess;
 }
-hipError_t launch_lora_expand(const LoraArgs& g, bool direct, bool trans, hipStream_t) {
+static int64_t check_expand(const LoraArgs& g, bool direct, bool trans) {
   check_lora(g, direct, trans);
   const int64_t cols = trans ? g.K : g.N, unit = direct ? 16 : g.R.unit_rows;
   need(g.y != nullptr && g.group >= 1 && g.cols >= kLoraCols && g.cols % kLoraCols == 0, "blocks of the expansion");
   need(unit == 64 ? g.cols == kLoraCols : g.group == 1, "units of few rows come one to a block, others against one part");
   const int64_t per = (cols + 8 * g.cols - 1) / (8 * g.cols);
   const int64_t groups = direct ? g.M : (g.R.max_units + g.group - 1) / g.group + (g.M + 63) / 64;
-  need(8 * per * groups < (1ll << 24), "grid of the expansion");
+  return 8 * per * groups;
+}
+hipError_t launch_lora_expand(const LoraArgs& g, bool direct, hipStream_t) {
+  need(check_expand(g, direct, false) < (1ll << 24), "grid of the expansion");
   ++g_launches;
   return hipSuccess;
 }
@@ -118,8 +121,14 @@ static void check_grad(const LoraGradArgs& g) {
   need(g.chunks == 1 || in_ws(g.sums, 2ull * g.chunks * g.rank * (g.K + g.N) * 4), "partial sums in the workspace");
   need(in_ws(g.part, (uint64_t)g.splits * g.M * g.rank * 4), "g in the workspace");
 }
-hipError_t launch_lora_pack(const LoraGradArgs& g, hipStream_t) {
-  check_grad(g);
+hipError_t launch_lora_dx(const LoraArgs& g, const LoraGradArgs& o, hipStream_t) {
+  need(o.da && o.db && o.L >= 1 && o.L <= 512, "outputs of the zeros");
+  int64_t blocks = o.L * lora_zero_parts(o.rank, o.K, o.N) + 8;
+  if (o.M) {
+    check_grad(o);
+    blocks += 4 * o.R.max_units + 8 + (g.y ? check_expand(g, false, true) : 0);
+  }
+  need(blocks < (1ll << 24), "grid of the dx launch");
   ++g_launches;
   return hipSuccess;
 }
@@ -131,7 +140,8 @@ hipError_t launch_lora_outer(const LoraGradArgs& g, hipStream_t) {
   return hipSuccess;
 }
 hipError_t launch_lora_sums(const LoraGradArgs& g, hipStream_t) {
-  need(g.da && g.db && g.L >= 1 && g.L <= 512, "sums");
+  check_grad(g);
+  need(g.da && g.db && g.L >= 1 && g.L <= 512 && g.chunks > 1, "sums");
   ++g_launches;
   return hipSuccess;
 }
