@@ -5,10 +5,10 @@
 // that is, one contraction of long rows to the rank ("shrink") and one
 // product back ("expand"), the gradient's with the transposed matrices
 // (TRANS).  Rows are grouped by adapter into units that share the loads of
-// their adapter's matrices.  Both products run on the bf16 MFMA with the rows
-// as columns of the result; the rank is far too small for either to be bound
-// by it: the shrink reads its rows once, the expand reads base and writes y
-// once, and calls of few rows read the adapters.  An MFMA operand wants eight
+// their adapter's matrices.  Both products run on the bf16 MFMA; the rank is
+// far too small for either to be bound by it: the shrink reads its rows once,
+// the expand reads base and writes y once, and calls of few rows read the
+// adapters.  An MFMA operand wants eight
 // consecutive values of the contracted axis per lane; where that axis is the
 // strided one in memory (TRANS) a lane loads eight rows of a few neighbouring
 // columns and transposes them in its registers, each column being one MFMA's.
@@ -183,10 +183,10 @@ __device__ __forceinline__ int chunk_at(int r, int k) { return r * 128 + ((k ^ (
 // neighbouring lanes read neighbouring bytes, while an MFMA operand has a row
 // per lane: loaded in operand order, sixteen lanes touch sixteen cache lines
 // of 16 bytes each and the address unit, not HBM, sets the pace (m = 8192, k =
-// 4096, rank 64: 50 us; now 25 us, of which reading x at the copy rate takes
-// 13.  dy with n = 14336, rank 32: 41 us, 5.7 TB/s).  So a wave loads eight whole lines per instruction
+// 4096, rank 64: 50 us).  So a wave loads eight whole lines per instruction
 // into registers, one step ahead, and passes them through its own LDS image;
-// no block barrier.
+// no block barrier.  Now 25 us, of which reading x at the copy rate takes 13;
+// dy with n = 14336, rank 32: 41 us, 5.7 TB/s.
 template <int RP, int T, bool DIRECT, bool TRANS, int NW>
 __global__ void __launch_bounds__(64 * NW) k_lora_shrink(LoraArgs g) {
   constexpr int RB = RP / 16, LD = RP + 4, U = 16 * T;
@@ -345,8 +345,10 @@ __device__ __forceinline__ void copy_rest(const LoraArgs& g, int64_t m0, int64_t
 // ends up with columns 4 c .. 4 c + 3 of rows 4 q + v: sixteen lanes read base
 // and write y 128 consecutive bytes at a time (with the rows along the lanes
 // instead, 16 bytes each, the address unit bound the kernel: m = 8192, n =
-// 14336, rank 64 132 us; now 107 us, 4.4 TB/s of base and y).  Blocks go round the XCDs one by one, so block id i takes columns i % 8 + 8 k: each XCD sees
-// an eighth of B_e, which stays in its L2 from group to group.
+// 14336, rank 64 132 us; now 107 us, 4.4 TB/s of base and y).  Blocks go round
+// the XCDs one by one, so block id i takes its columns from the eighth i % 8:
+// each XCD sees an eighth of B_e, which stays in its L2 from group to group,
+// and writes neighbouring parts of a row.
 template <int RP, int T> struct ExpandLds {
   static constexpr int U = 16 * T, HB = T < 4 ? 1 : 2;        // units of fewer than 64 rows come one to a block
   __align__(16) uint16_t hs[HB][U][2 * RP + 8];               // a row's h: RP values hi, RP values lo
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
   expand_block<RP, T, DIRECT, false>(g, blockIdx.x, lds);
 }
 
-// g (the splits' sums; which = 0) or h (which = 1) of 32 of a unit's rows
+// g (the splits' sums) or, is_h, h of 32 of a unit's rows
 // in the order of the outer product's operands, so that a wave loads each
 // with one contiguous access: [32-row step][hi, lo][16-rank block][lane][8],
 // lane (c, q) holding rank 16 k + c of rows 32 s + 8 q .. + 7; zeros beyond

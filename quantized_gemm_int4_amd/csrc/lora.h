@@ -88,7 +88,7 @@ hipError_t launch_lora_plan(const int32_t* ids, int64_t M, int L, int unit_rows,
 hipError_t launch_lora_shrink(const LoraArgs& g, bool direct, bool trans, hipStream_t st);
 // y = base + B h.
 hipError_t launch_lora_expand(const LoraArgs& g, bool direct, hipStream_t st);
-// both forward products in one launch (M <= kLoraDirect, rank <= 64)
+// both forward products in one launch (M <= 16, rank <= 64)
 hipError_t launch_lora_small(const LoraArgs& g, int parts, hipStream_t st);
 // packed g and h, zeros for adapters without rows, and (g.y not null) y = base + A^T g
 hipError_t launch_lora_dx(const LoraArgs& g, const LoraGradArgs& o, hipStream_t st);
