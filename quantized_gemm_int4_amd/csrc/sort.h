@@ -1,5 +1,5 @@
-// Stable counting sort of ids inside one block: the parts that the expert
-// sort (k_moe.hip) and the grouping of rows by adapter (k_lora.hip) share.
+// Parts of the stable counting sorts of ids by expert or adapter (k_moe.hip,
+// k_rows.hip, k_lora.hip): a block's scan, and a block's placing of a range.
 #pragma once
 #include "common.h"
 
