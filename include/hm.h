@@ -474,7 +474,7 @@ hm_status hm_lora_workspace_size(const hm_lora_desc* d, int64_t m, size_t* bytes
  *   h[m][:] = scales[e] * A_e x[m],  y[m][:] = bf16( base[m][:] + B_e h[m] ),
  * e = adapter_ids[m]; a row whose id is outside [0, num_adapters) has no
  * adapter: h = 0 and y = base.  Both products accumulate in fp32 and h enters
- * the second one with 16 significant bits or more (two bf16 terms).
+ * the second one with all its 24 bits (as three bf16 terms).
  *   x           bf16 [m][k];  adapter_ids int32 [m], in any order.
  *   a           bf16 [num_adapters][rank][k];  b bf16 [num_adapters][n][rank].
  *   scales      fp32 [num_adapters].
@@ -498,7 +498,7 @@ hm_status hm_lora_grad_workspace_size(const hm_lora_desc* d, int64_t m, size_t* 
  *   da[e] = bf16( sum over the rows m of e of g[m] x[m]^T ),
  *   db[e] = bf16( sum over the rows m of e of dy[m] h[m]^T ),
  * sums in fp32 in an order that the shapes and ids fix (equal calls give
- * equal bits); g and h enter the products as two bf16 terms.  (The gradient
+ * equal bits); g and h enter the products with all their 24 bits.  (The gradient
  * to base is dy itself.)
  *   dy          bf16 [m][n];  x bf16 [m][k];  h fp32 [m][rank] from hm_lora.
  *   dx_base     bf16 [m][k], the gradient through the shared projection, or

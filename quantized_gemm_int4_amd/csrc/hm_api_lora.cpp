@@ -103,7 +103,7 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
   }
   w.part = take((size_t)w.splits * (size_t)m * (size_t)d->rank * 4);
   if (grad) {
-    const size_t packed = (size_t)w.max_units * 2 * (size_t)lora_rp(d->rank) * kLoraUnit * 2;
+    const size_t packed = (size_t)w.max_units * kTerms * (size_t)lora_rp(d->rank) * kLoraUnit * 2;
     w.gt = take(packed);
     w.ht = take(packed);
     // about 768 blocks, three to a compute unit (m = 8192, rank 32: 67 us; 512 78, 1024 72), a chunk of four units or

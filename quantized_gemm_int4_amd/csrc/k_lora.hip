@@ -349,16 +349,18 @@ __device__ __forceinline__ void copy_rest(const LoraArgs& g, int64_t m0, int64_t
 // the XCDs one by one, so block id i takes its columns from the eighth i % 8:
 // each XCD sees an eighth of B_e, which stays in its L2 from group to group,
 // and writes neighbouring parts of a row.
+// A row of h in LDS: RP values of each term; RP = 16 has a fourth of zeros, so
+// that two MFMAs of 32 take the four.
+constexpr int h_values(int rp) { return rp == 16 ? 64 : kTerms * rp; }
 template <int RP, int T> struct ExpandLds {
-  static constexpr int U = 16 * T, HB = T < 4 ? 1 : 2;        // units of fewer than 64 rows come one to a block
-  __align__(16) uint16_t hs[HB][U][2 * RP + 8];               // a row's h: RP values hi, RP values lo
+  static constexpr int U = 16 * T;
+  __align__(16) uint16_t hs[U][h_values(RP) + 8];             // one image: find_unit's barrier comes before the next unit's
   __align__(16) int rows[2][U < 32 ? 32 : U];                 // 64 in all: copy_rest's list
 };
 template <int RP, int T, bool DIRECT, bool TRANS>
 __device__ __forceinline__ void expand_block(const LoraArgs& g, uint32_t block, ExpandLds<RP, T>& lds) {
-  constexpr int S = RP == 16 ? 1 : RP / 16, HALF = RP == 16 ? 1 : RP / 32, U = 16 * T, LDH = 2 * RP + 8;
-  constexpr int HB = ExpandLds<RP, T>::HB;
-  auto& hs = lds.hs;
+  constexpr int S = h_values(RP) / 32, HALF = RP == 16 ? 1 : RP / 32, U = 16 * T;
+  auto& hu = lds.hs;
   auto& rows = lds.rows;
   const int64_t N = TRANS ? g.K : g.N;
   const int per = (int)((N + 8 * g.cols - 1) / (8 * g.cols));             // column slabs per XCD
@@ -373,7 +375,7 @@ __device__ __forceinline__ void expand_block(const LoraArgs& g, uint32_t block, 
     copy_rest(g, (int64_t)(gi - groups) * 64, N, c0, c1, keep, rows[0]);
     return;
   }
-  // rank column of MFMA step s (of 32 over [hi | lo]) that quarter q supplies first; RP = 16: one step, 0-1 hi, 2-3 lo
+  // rank column of MFMA step s (of 32 over the terms) that quarter q supplies first; RP = 16: two terms a step
   auto rank0 = [q](int s) { return RP == 16 ? 8 * (q & 1) : 32 * s + 8 * q; };
   u32x4_t bv[TRANS ? 1 : 4][HALF];
   u32x2_t yv[T][4];
@@ -382,7 +384,6 @@ __device__ __forceinline__ void expand_block(const LoraArgs& g, uint32_t block, 
   const int u0 = DIRECT ? gi : gi * g.group, un = DIRECT ? gi + 1 : (int)min((int64_t)u0 + g.group, g.R.max_units);
   for (int u = u0; u < un; ++u) {
     int e, *rw = rows[u & 1];
-    uint16_t(*hu)[LDH] = hs[u & (HB - 1)];
     const int count = find_unit<U, DIRECT>(g, u, 0, &e, rw);
     if (count <= 0) {
       if (DIRECT && count < 0 && wave == 0) copy_row(g, u, N, c0, c1, keep);
@@ -422,7 +423,7 @@ __device__ __forceinline__ void expand_block(const LoraArgs& g, uint32_t block, 
     };
     if (n0 < c1) load_group();
     loads_first();
-    // h of the unit's rows: the splits' sums in split order, as two bf16 terms
+    // h of the unit's rows: the splits' sums in split order, as bf16 terms
     auto stage = [&](auto max_splits) __attribute__((always_inline)) {
       constexpr int MS = decltype(max_splits)::value;
       for (int i = threadIdx.x; i < count * (RP / 4); i += 256) {
@@ -440,16 +441,12 @@ __device__ __forceinline__ void expand_block(const LoraArgs& g, uint32_t block, 
             if (s < g.splits) v += p[s];
           if (keep && g.part != g.h) *reinterpret_cast<f32x4_t*>(g.h + at) = v;
         }
-        u32x2_t hi, lo;
+        uint32_t t[2][kTerms];
+        split3(v[0], v[1], t[0]);
+        split3(v[2], v[3], t[1]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t h2, l2;
-          split2(v[2 * k], v[2 * k + 1], &h2, &l2);
-          hi[k] = h2;
-          lo[k] = l2;
-        }
-        *reinterpret_cast<u32x2_t*>(&hu[row][r0]) = hi;
-        *reinterpret_cast<u32x2_t*>(&hu[row][RP + r0]) = lo;
+        for (int k = 0; k < kTerms; ++k) *reinterpret_cast<u32x2_t*>(&hu[row][RP * k + r0]) = (u32x2_t){t[0][k], t[1][k]};
+        if (RP == 16) *reinterpret_cast<u32x2_t*>(&hu[row][48 + r0]) = (u32x2_t){0u, 0u};
       }
     };
     if (g.splits == 1) stage(Int<1>{});
@@ -461,19 +458,21 @@ __device__ __forceinline__ void expand_block(const LoraArgs& g, uint32_t block, 
     for (int t = 0; t < T; ++t) {
       if (16 * t >= count) break;
       const uint16_t* hr = hu[min(16 * t + c, count - 1)] + 8 * q;
-      u32x4_t hf[S];
-#pragma unroll
-      for (int s = 0; s < S; ++s) hf[s] = ld16(hr + 32 * s);
       f32x4_t acc[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        acc[b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+      for (int b = 0; b < 4; ++b) acc[b] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
+      for (int s0 = 0; s0 < HALF; ++s0) {
+        u32x4_t hf[S / HALF];
+#pragma unroll
+        for (int i = 0; i < S / HALF; ++i) hf[i] = ld16(hr + 32 * (s0 + HALF * i));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
           u32x4_t a;
-          if constexpr (TRANS) a = cv[s % HALF].operand(b);
-          else a = bv[b][s % HALF];
-          acc[b] = mfma_bf16(hf[s], a, acc[b]);
+          if constexpr (TRANS) a = cv[s0].operand(b);
+          else a = bv[b][s0];
+#pragma unroll
+          for (int i = 0; i < S / HALF; ++i) acc[b] = mfma_bf16(hf[i], a, acc[b]);
         }
       }
       const int4 m4 = *reinterpret_cast<const int4*>(rw + 16 * t + 4 * q);
@@ -504,7 +503,7 @@ __global__ void __launch_bounds__(256) k_lora_expand(LoraArgs g) {
 
 // g (the splits' sums) or, is_h, h of 32 of a unit's rows
 // in the order of the outer product's operands, so that a wave loads each
-// with one contiguous access: [32-row step][hi, lo][16-rank block][lane][8],
+// with one contiguous access: [32-row step][term][16-rank block][lane][8],
 // lane (c, q) holding rank 16 k + c of rows 32 s + 8 q .. + 7; zeros beyond
 // the rank and the unit's rows.
 template <int RP>
@@ -534,19 +533,14 @@ __device__ __forceinline__ void pack_block(const LoraGradArgs& g, int u, bool is
     for (int k = 0; k < 4; ++k) v[row][r + k] = s[k];
   }
   __syncthreads();
-  uint16_t* out = (is_h ? g.ht : g.gt) + ((int64_t)u * 2 + half) * 2 * RP * 32;
+  uint16_t* out = (is_h ? g.ht : g.gt) + ((int64_t)u * 2 + half) * kTerms * RP * 32;
   for (int i = threadIdx.x; i < RP * 4; i += 256) {
     const int lane = i & 63, k = i >> 6, r = 16 * k + (lane & 15), m = 8 * (lane >> 4);
-    u32x4_t hi, lo;
+    uint32_t t[4][kTerms];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      uint32_t h2, l2;
-      split2(v[m + 2 * p][r], v[m + 2 * p + 1][r], &h2, &l2);
-      hi[p] = h2;
-      lo[p] = l2;
-    }
-    st16(out + 8 * i, hi);
-    st16(out + RP * 32 + 8 * i, lo);
+    for (int p = 0; p < 4; ++p) split3(v[m + 2 * p][r], v[m + 2 * p + 1][r], t[p]);
+#pragma unroll
+    for (int j = 0; j < kTerms; ++j) st16(out + RP * 32 * j + 8 * i, (u32x4_t){t[0][j], t[1][j], t[2][j], t[3][j]});
   }
 }
 
@@ -585,8 +579,8 @@ __global__ void __launch_bounds__(256, 2) k_lora_dx(LoraArgs g, LoraGradArgs o, 
 constexpr int small_waves(int rp) { return rp == 64 ? 8 : 16; }
 template <int RP>
 __global__ void __launch_bounds__(64 * small_waves(RP)) k_lora_small(LoraArgs g) {
-  constexpr int RB = RP / 16, NW = small_waves(RP), LD = RP + 4, S = RP == 16 ? 1 : RP / 16, HALF = RP == 16 ? 1 : RP / 32;
-  constexpr int NB = RB == 1 ? 4 : 2, IMG = (1 + RB) * 2048, LDH = 2 * RP + 8;
+  constexpr int RB = RP / 16, NW = small_waves(RP), LD = RP + 4, S = h_values(RP) / 32, HALF = RP == 16 ? 1 : RP / 32;
+  constexpr int NB = RB == 1 ? 4 : 2, IMG = (1 + RB) * 2048, LDH = h_values(RP) + 8;
   constexpr int BYTES = NW * IMG > NW * 16 * LD * 4 ? NW * IMG : NW * 16 * LD * 4;
   __shared__ __align__(16) uint8_t lds[BYTES];
   __shared__ __align__(16) uint16_t hs[16][LDH];
@@ -677,7 +671,11 @@ __global__ void __launch_bounds__(64 * small_waves(RP)) k_lora_small(LoraArgs g)
       g.h[(int64_t)rows[row] * g.rank + r] = a;
       g.h[(int64_t)rows[row] * g.rank + r + 1] = b;
     }
-    split2(a, b, reinterpret_cast<uint32_t*>(&hs[row][r]), reinterpret_cast<uint32_t*>(&hs[row][RP + r]));
+    uint32_t t[kTerms];
+    split3(a, b, t);
+#pragma unroll
+    for (int k = 0; k < kTerms; ++k) *reinterpret_cast<uint32_t*>(&hs[row][RP * k + r]) = t[k];
+    if (RP == 16) *reinterpret_cast<uint32_t*>(&hs[row][48 + r]) = 0u;
   }
   __syncthreads();
   u32x4_t hf[S];

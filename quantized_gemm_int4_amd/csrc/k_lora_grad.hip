@@ -5,7 +5,7 @@
 // the strided axis of x and dy: a lane loads eight rows of eight neighbouring
 // columns and transposes them in its registers, each column being one MFMA's
 // operand.  g and h are small; a packing pass (k_lora_dx's) brings them into operand order
-// once (as two bf16 terms), because every column tile reads them again (read
+// once (as three bf16 terms), because every column tile reads them again (read
 // in their own order, 64 cache lines an access, they bound the kernel: m =
 // 8192, n = 14336, k = 4096, rank 32 189 us; now 68 us, 4.4 TB/s of dy and x).
 #include "lora.h"
@@ -74,13 +74,12 @@ __device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, in
     }
     for (; s < s_end; s += 4) {
       const Cols8<8> zv = next;
-      u32x4_t fh[RB], fl[RB];
-      const uint16_t* fu = f + (int64_t)s * 2 * RP * 32;
+      u32x4_t fv[kTerms][RB];
+      const uint16_t* fu = f + (int64_t)s * kTerms * RP * 32;
 #pragma unroll
-      for (int k = 0; k < RB; ++k) {
-        fh[k] = ld16(fu + 512 * k);
-        fl[k] = ld16(fu + RP * 32 + 512 * k);
-      }
+      for (int i = 0; i < kTerms; ++i)
+#pragma unroll
+        for (int k = 0; k < RB; ++k) fv[i][k] = ld16(fu + RP * 32 * i + 512 * k);
       const int count = g.R.units[2 * (s >> 1) + 1] - 32 * (s & 1);
       if (s + 4 < s_end) {
         fetch_z(R);
@@ -92,15 +91,10 @@ __device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, in
       for (int j = 0; j < 8; ++j) {
         const u32x4_t zo = zv.operand(j);
 #pragma unroll
-        for (int k = 0; k < RB; ++k) {
-          if (db) {
-            acc[j][k] = mfma_bf16(fh[k], zo, acc[j][k]);
-            acc[j][k] = mfma_bf16(fl[k], zo, acc[j][k]);
-          } else {
-            acc[j][k] = mfma_bf16(zo, fh[k], acc[j][k]);
-            acc[j][k] = mfma_bf16(zo, fl[k], acc[j][k]);
-          }
-        }
+        for (int k = 0; k < RB; ++k)
+#pragma unroll
+          for (int i = 0; i < kTerms; ++i)
+            acc[j][k] = db ? mfma_bf16(fv[i][k], zo, acc[j][k]) : mfma_bf16(zo, fv[i][k], acc[j][k]);
       }
     }
     // db: the lane holds column 8 c + j, rank 16 k + 4 q + v; da: rank 16 k + c, column 8 (4 q + v) + j

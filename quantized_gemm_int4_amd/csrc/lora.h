@@ -16,6 +16,7 @@ constexpr int64_t kLoraMaxRows = 1 << 20;
 constexpr int kLoraDirect = 64;
 constexpr int kLoraPlanBlocks = 256; // most blocks of the grouping kernel
 constexpr int kLoraUnit = 64;        // rows per unit of the gradient
+constexpr int kTerms = 3;            // bf16 terms that carry an fp32 value of h or g into an MFMA (split3)
 constexpr int kLoraCols = 256;       // output columns that an expanding block takes at a time
 
 // Rows grouped by adapter.  A unit is up to unit_rows rows of one adapter,
@@ -53,7 +54,7 @@ struct LoraGradArgs {
   int splits;
   int64_t M, N, K;
   int rank, L;
-  uint16_t *gt, *ht;         // packed g and h, 2 RP kLoraUnit values a unit (pack_block)
+  uint16_t *gt, *ht;         // packed g and h, kTerms RP kLoraUnit values a unit (pack_block)
   float* sums;               // partial sums [2 chunks][rank (K + N)]
   int chunks;
   uint16_t *da, *db;
@@ -98,12 +99,17 @@ hipError_t launch_lora_sums(const LoraGradArgs& g, hipStream_t st);
 #ifdef __HIPCC__
 template <int N> struct Int { static constexpr int value = N; };
 
-// fp32 pair -> two bf16 terms hi + lo: hi = bf16(v), lo = bf16(v - hi).  The
-// sum carries v to 2^-16 of its size, far below the bf16 rounding of the
-// results (2^-8), where hi alone would add an error as large as that rounding.
-__device__ __forceinline__ void split2(float a, float b, uint32_t* hi, uint32_t* lo) {
-  *hi = pack_bf16(a, b);
-  *lo = pack_bf16(a - lo_bf16(*hi), b - hi_bf16(*hi));
+// fp32 pair -> kTerms pairs of bf16 terms, v = t[0] + t[1] + t[2]: each the
+// leading eight bits, cut off, of what the ones before it leave, so that the
+// three carry all 24 bits (of values of 2^-102 and more) and have v's sign.
+__device__ __forceinline__ void split3(float a, float b, uint32_t t[kTerms]) {
+  float v[2] = {a, b};
+#pragma unroll
+  for (int i = 0; i < kTerms; ++i) {
+    t[i] = __builtin_amdgcn_perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u);
+    v[0] -= lo_bf16(t[i]);
+    v[1] -= hi_bf16(t[i]);
+  }
 }
 
 // Keeps the loads written before this point before it (the compiler would
