@@ -474,7 +474,10 @@ hm_status hm_lora_workspace_size(const hm_lora_desc* d, int64_t m, size_t* bytes
  *   h[m][:] = scales[e] * A_e x[m],  y[m][:] = bf16( base[m][:] + B_e h[m] ),
  * e = adapter_ids[m]; a row whose id is outside [0, num_adapters) has no
  * adapter: h = 0 and y = base.  Both products accumulate in fp32 and h enters
- * the second one with all its 24 bits (as three bf16 terms).
+ * the second one with all its 24 bits (as three bf16 terms).  Infinities and
+ * NaN among the inputs give what the formulas give in fp32, where h (here) and
+ * g (in hm_lora_grad) are 0 or 2^-90 and more in size; they stay within the
+ * rows and matrices of their adapter.
  *   x           bf16 [m][k];  adapter_ids int32 [m], in any order.
  *   a           bf16 [num_adapters][rank][k];  b bf16 [num_adapters][n][rank].
  *   scales      fp32 [num_adapters].

@@ -349,8 +349,8 @@ __device__ __forceinline__ void copy_rest(const LoraArgs& g, int64_t m0, int64_t
 // the XCDs one by one, so block id i takes its columns from the eighth i % 8:
 // each XCD sees an eighth of B_e, which stays in its L2 from group to group,
 // and writes neighbouring parts of a row.
-// A row of h in LDS: RP values of each term; RP = 16 has a fourth of zeros, so
-// that two MFMAs of 32 take the four.
+// A row of h in LDS: RP values of each term; RP = 16 has the fourth too, so
+// that two MFMAs of 32 take the row.
 constexpr int h_values(int rp) { return rp == 16 ? 64 : kTerms * rp; }
 template <int RP, int T> struct ExpandLds {
   static constexpr int U = 16 * T;
@@ -441,12 +441,12 @@ __device__ __forceinline__ void expand_block(const LoraArgs& g, uint32_t block, 
             if (s < g.splits) v += p[s];
           if (keep && g.part != g.h) *reinterpret_cast<f32x4_t*>(g.h + at) = v;
         }
-        uint32_t t[2][kTerms];
-        split3(v[0], v[1], t[0]);
-        split3(v[2], v[3], t[1]);
+        uint32_t t[2][4];
+        split4(v[0], v[1], t[0]);
+        split4(v[2], v[3], t[1]);
 #pragma unroll
-        for (int k = 0; k < kTerms; ++k) *reinterpret_cast<u32x2_t*>(&hu[row][RP * k + r0]) = (u32x2_t){t[0][k], t[1][k]};
-        if (RP == 16) *reinterpret_cast<u32x2_t*>(&hu[row][48 + r0]) = (u32x2_t){0u, 0u};
+        for (int k = 0; k < h_values(RP) / RP; ++k)
+          *reinterpret_cast<u32x2_t*>(&hu[row][RP * k + r0]) = (u32x2_t){t[0][k], t[1][k]};
       }
     };
     if (g.splits == 1) stage(Int<1>{});
@@ -536,9 +536,9 @@ __device__ __forceinline__ void pack_block(const LoraGradArgs& g, int u, bool is
   uint16_t* out = (is_h ? g.ht : g.gt) + ((int64_t)u * 2 + half) * kTerms * RP * 32;
   for (int i = threadIdx.x; i < RP * 4; i += 256) {
     const int lane = i & 63, k = i >> 6, r = 16 * k + (lane & 15), m = 8 * (lane >> 4);
-    uint32_t t[4][kTerms];
+    uint32_t t[4][4];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) split3(v[m + 2 * p][r], v[m + 2 * p + 1][r], t[p]);
+    for (int p = 0; p < 4; ++p) split4(v[m + 2 * p][r], v[m + 2 * p + 1][r], t[p]);
 #pragma unroll
     for (int j = 0; j < kTerms; ++j) st16(out + RP * 32 * j + 8 * i, (u32x4_t){t[0][j], t[1][j], t[2][j], t[3][j]});
   }
@@ -671,11 +671,10 @@ __global__ void __launch_bounds__(64 * small_waves(RP)) k_lora_small(LoraArgs g)
       g.h[(int64_t)rows[row] * g.rank + r] = a;
       g.h[(int64_t)rows[row] * g.rank + r + 1] = b;
     }
-    uint32_t t[kTerms];
-    split3(a, b, t);
+    uint32_t t[4];
+    split4(a, b, t);
 #pragma unroll
-    for (int k = 0; k < kTerms; ++k) *reinterpret_cast<uint32_t*>(&hs[row][RP * k + r]) = t[k];
-    if (RP == 16) *reinterpret_cast<uint32_t*>(&hs[row][48 + r]) = 0u;
+    for (int k = 0; k < h_values(RP) / RP; ++k) *reinterpret_cast<uint32_t*>(&hs[row][RP * k + r]) = t[k];
   }
   __syncthreads();
   u32x4_t hf[S];

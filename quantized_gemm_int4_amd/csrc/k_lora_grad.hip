@@ -56,12 +56,13 @@ __device__ __forceinline__ void outer_tile(const LoraGradArgs& g, int64_t k0, in
       const int first = __builtin_amdgcn_readfirstlane(R.r[0]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        // rows behind the unit's last repeat the step's first: their g and h are 0
-        const int64_t m = 8 * q + i < R.count ? R.r[i] : first;
+        // rows behind the unit's last read the step's first and count as 0, as their g and h are
+        const bool in = 8 * q + i < R.count;
+        const int64_t m = in ? R.r[i] : first;
         u32x4_t v = {0u, 0u, 0u, 0u};
         if (R.count > 0 && col < n) v = ld8_tail(z + m * n, col, n);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) next.w[i][k] = v[k];
+        for (int k = 0; k < 4; ++k) next.w[i][k] = in ? v[k] : 0u;
       }
     };
     const int s_end = 2 * ub;

@@ -16,7 +16,7 @@ constexpr int64_t kLoraMaxRows = 1 << 20;
 constexpr int kLoraDirect = 64;
 constexpr int kLoraPlanBlocks = 256; // most blocks of the grouping kernel
 constexpr int kLoraUnit = 64;        // rows per unit of the gradient
-constexpr int kTerms = 3;            // bf16 terms that carry an fp32 value of h or g into an MFMA (split3)
+constexpr int kTerms = 3;            // bf16 terms that carry an fp32 value of h or g into an MFMA (split4)
 constexpr int kLoraCols = 256;       // output columns that an expanding block takes at a time
 
 // Rows grouped by adapter.  A unit is up to unit_rows rows of one adapter,
@@ -99,16 +99,24 @@ hipError_t launch_lora_sums(const LoraGradArgs& g, hipStream_t st);
 #ifdef __HIPCC__
 template <int N> struct Int { static constexpr int value = N; };
 
-// fp32 pair -> kTerms pairs of bf16 terms, v = t[0] + t[1] + t[2]: each the
-// leading eight bits, cut off, of what the ones before it leave, so that the
-// three carry all 24 bits (of values of 2^-102 and more) and have v's sign.
-__device__ __forceinline__ void split3(float a, float b, uint32_t t[kTerms]) {
+// fp32 pair -> four pairs of bf16 terms.  The first kTerms carry v: each is the
+// leading eight bits, cut off, of what the ones before it leave, 24 in all (of
+// values of 2^-102 and more).  A term is multiplied by values that may be
+// infinite, so all four have v's sign and none is 0 unless v is: where nothing
+// is left, and as the fourth, stands 2^-32 v, too small to change a sum.  An
+// infinite or NaN v has itself in all four.
+__device__ __forceinline__ void split4(float a, float b, uint32_t t[4]) {
   float v[2] = {a, b};
+  const float e[2] = {a * 0x1p-32f, b * 0x1p-32f};
 #pragma unroll
-  for (int i = 0; i < kTerms; ++i) {
-    t[i] = __builtin_amdgcn_perm(__float_as_uint(v[1]), __float_as_uint(v[0]), 0x07060302u);
-    v[0] -= lo_bf16(t[i]);
-    v[1] -= hi_bf16(t[i]);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t p[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      p[j] = __float_as_uint(i < kTerms && __builtin_fabsf(v[j]) > 0.f ? v[j] : e[j]);
+      v[j] -= __uint_as_float(__float_as_uint(v[j]) & 0xffff0000u);
+    }
+    t[i] = __builtin_amdgcn_perm(p[1], p[0], 0x07060302u);
   }
 }
 
