@@ -323,7 +323,8 @@ hipError_t launch_collect(const uint16_t* ys, const float* w, const int32_t* pos
 
 hipError_t launch_collect_grad(const uint16_t* dout, const uint16_t* ys, const float* w, const int32_t* positions,
                                int64_t t, int topk, int64_t n, uint16_t* dys, float* dw, hipStream_t st) {
-  const int threads = n <= 2048 ? 256 : 512;
+  // a launch stays under 2^32 threads: from 2^23 tokens on blocks of 256, whatever n
+  const int threads = n <= 2048 || t >= (1 << 23) ? 256 : 512;
   hipLaunchKernelGGL(k_collect_grad, dim3((unsigned)t), dim3(threads), 0, st, dout, ys, w, positions, t, topk, n, dys,
                      dw);
   return hipGetLastError();
