@@ -39,7 +39,7 @@
  *   - Alignment: w_dev and workspaces 256 bytes, every other pointer 16 bytes
  *     (HM_ERR_ALIGN otherwise).
  *   - Inputs are finite; NaN or Inf in X, scales or weights gives unspecified
- *     (but memory-safe) results.
+ *     (but memory-safe) results where an entry point does not say more.
  */
 #ifndef HM_H
 #define HM_H
@@ -59,7 +59,7 @@ typedef enum hm_status {
   HM_ERR_NULL = 1,        /* a required pointer is NULL */
   HM_ERR_SHAPE = 2,       /* bad size, group or count */
   HM_ERR_ALIGN = 3,       /* pointer not aligned as required */
-  HM_ERR_UNSUPPORTED = 4, /* unknown weight format or format/activation pair */
+  HM_ERR_UNSUPPORTED = 4, /* unknown weight format or format/activation pair; arrays that overlap (hm_lora, hm_lora_grad) */
   HM_ERR_WORKSPACE = 5,   /* buffer smaller than its size query */
   HM_ERR_HIP = 6,         /* a HIP launch failed */
   HM_ERR_ABI = 7,         /* descriptor abi field != HM_ABI_VERSION */
@@ -484,9 +484,11 @@ hm_status hm_lora_workspace_size(const hm_lora_desc* d, int64_t m, size_t* bytes
  *   base        bf16 [m][n], the shared projection's output (hm_gemm), or NULL
  *               for zeros.  May be y itself: the adapters are then added in
  *               place, and rows without an adapter are not touched.
- *   y           bf16 [m][n]; must not overlap base in any other way.
+ *   y           bf16 [m][n]; must not overlap x, a, b, or base in any other
+ *               way (HM_ERR_UNSUPPORTED).
  *   h           fp32 [m][rank], what hm_lora_grad needs; NULL if not wanted.
  *   ws          hm_lora_workspace_size bytes, overwritten.
+ * h and ws must overlap no other array.
  * m = 0 is a no-op; m up to 1048576, and m * n up to about 10^11 (a launch's
  * blocks; the size query and the call agree): HM_ERR_SHAPE above. */
 hm_status hm_lora(const hm_lora_desc* d, const uint16_t* x, const int32_t* adapter_ids, const uint16_t* a,
@@ -511,6 +513,8 @@ hm_status hm_lora_grad_workspace_size(const hm_lora_desc* d, int64_t m, size_t* 
  *   da          bf16 [num_adapters][rank][k];  db bf16 [num_adapters][n][rank];
  *               adapters that no row names get zeros.
  *   ws          hm_lora_grad_workspace_size bytes, overwritten.
+ * dx, da and db must not overlap dy, x, h, a, b, or dx_base in any other way
+ * (HM_ERR_UNSUPPORTED), nor each other; ws must overlap no other array.
  * m = 0 writes zeros to da and db; limits as hm_lora. */
 hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const uint16_t* x, const float* h,
                        const int32_t* adapter_ids, const uint16_t* a, const uint16_t* b, const float* scales,

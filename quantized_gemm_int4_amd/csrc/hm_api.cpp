@@ -472,7 +472,7 @@ HM_API const char* hm_status_string(int32_t s) {
     case HM_ERR_NULL: return "null pointer";
     case HM_ERR_SHAPE: return "bad shape, group or count";
     case HM_ERR_ALIGN: return "misaligned pointer";
-    case HM_ERR_UNSUPPORTED: return "unsupported format or format/activation pair";
+    case HM_ERR_UNSUPPORTED: return "unsupported format, format/activation pair or overlap of arrays";
     case HM_ERR_WORKSPACE: return "workspace too small";
     case HM_ERR_HIP: return "HIP launch failed";
     case HM_ERR_ABI: return "descriptor ABI version mismatch";

@@ -16,6 +16,23 @@ using namespace hm;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
+// Whether an output's bytes and those of one of the arrays it must leave alone
+// meet.  No array is longer than the card's memory (288 GB), so lengths end
+// at 2^39 and ends do not wrap.
+struct Span {
+  const void* p;             // null: no array
+  uint64_t bytes;
+};
+bool meets(const Span& out, const Span& in) {
+  if (!out.p || !in.p) return false;
+  constexpr uint64_t kMost = 1ull << 39;
+  const uint64_t a = (uintptr_t)out.p, b = (uintptr_t)in.p;
+  return a < b + std::min(in.bytes, kMost) && b < a + std::min(out.bytes, kMost);
+}
+template <size_t N> bool meets_any(const Span& out, const Span (&in)[N]) {
+  return std::any_of(in, in + N, [&](const Span& s) { return meets(out, s); });
+}
+
 hm_status check_lora(const hm_lora_desc* d, int64_t m) {
   if (!d) return HM_ERR_NULL;
   if (d->abi != HM_ABI_VERSION) return HM_ERR_ABI;
@@ -180,6 +197,9 @@ HM_API hm_status hm_lora(const hm_lora_desc* d, const uint16_t* x, const int32_t
     if (ws_bytes < w.total) return HM_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return HM_ERR_ALIGN;
   }
+  const uint64_t um = m, k = d->k, n = d->n, mats = 2ull * d->num_adapters * d->rank;
+  if (meets_any({y, 2 * um * n}, {{x, 2 * um * k}, {a, mats * k}, {b, mats * n}, {y == base ? nullptr : base, 2 * um * n}}))
+    return HM_ERR_UNSUPPORTED;
   LoraArgs g = args_of(d, x, adapter_ids, a, b, scales, m, base, y, w, (uint8_t*)ws);
   g.h = h;
   if (w.parts) return launch_lora_small(g, w.parts, stream) == hipSuccess ? HM_OK : HM_ERR_HIP;
@@ -222,6 +242,12 @@ HM_API hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const u
   if (!ws) return HM_ERR_NULL;
   if (ws_bytes < w.total) return HM_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return HM_ERR_ALIGN;
+  const uint64_t um = m, k = d->k, n = d->n, mats = 2ull * d->num_adapters * d->rank;
+  const Span in[] = {{dy, 2 * um * n}, {x, 2 * um * k}, {h, 4 * um * d->rank}, {a, mats * k}, {b, mats * n}};
+  const Span base = {dx_base, 2 * um * k}, odx = {dx, 2 * um * k}, oda = {da, mats * k}, odb = {db, mats * n};
+  if (meets_any(odx, in) || meets_any(oda, in) || meets_any(odb, in) || meets(oda, base) || meets(odb, base) ||
+      (dx != dx_base && meets(odx, base)))
+    return HM_ERR_UNSUPPORTED;
   uint8_t* at = (uint8_t*)ws;
   LoraArgs g = args_of(d, dy, adapter_ids, a, b, scales, m, dx_base, dx, w, at);
   hipError_t e = group_rows(d, adapter_ids, m, w, at, &g.R, stream);
