@@ -412,8 +412,9 @@ hm_status hm_moe_dispatch_workspace_size(int64_t t, int32_t topk, int32_t num_ex
  * "tokens", topk = 1, these offsets and the identity 0, 1, 2, ... as
  * sorted_pairs; its output is then in expert order too.
  * Any n >= 1; x and xs 16-byte aligned, the integer arrays 4-byte; limits on
- * t, topk and num_experts as hm_moe_sort.  t = 0 is a no-op.  xs must not
- * overlap x.  ws: hm_moe_dispatch_workspace_size bytes. */
+ * t, topk and num_experts as hm_moe_sort.  t = 0 is a no-op: counts and
+ * offsets are not written either.  No output may overlap x, topk_ids, ws or
+ * another output.  ws: hm_moe_dispatch_workspace_size bytes. */
 hm_status hm_moe_dispatch(const uint16_t* x, const int32_t* topk_ids, int64_t t, int32_t topk,
                           int32_t num_experts, int64_t n, uint16_t* xs, int32_t* counts, int32_t* offsets,
                           int32_t* sorted_pairs, int32_t* positions, void* ws, size_t ws_bytes,

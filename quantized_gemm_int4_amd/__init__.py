@@ -473,7 +473,8 @@ def hm_moe_dispatch(x, topk_ids, num_experts, xs=None, counts=None, offsets=None
     (xs bf16 [t*topk, n], counts [E], offsets [E+1], sorted_pairs [t*topk],
     positions [t, topk]).  Rows of xs and entries of sorted_pairs from
     offsets[E] on (as many as ids lie outside [0, E)) are left as they were:
-    uninitialised when allocated here."""
+    uninitialised when allocated here.  No tokens: counts and offsets are 0
+    (the C entry point, a no-op then, leaves them)."""
     ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:
@@ -493,6 +494,9 @@ def hm_moe_dispatch(x, topk_ids, num_experts, xs=None, counts=None, offsets=None
                                _arg(sorted_pairs, i32, (t * topk,), "sorted_pairs", dev),
                                _arg(positions, i32, (t, topk), "positions", dev), wsp, wsb, _stream())
     _ok("hm_moe_dispatch", code)
+    if t == 0:
+        counts.zero_()
+        offsets.zero_()
     return xs, counts, offsets, sorted_pairs, positions
 
 
