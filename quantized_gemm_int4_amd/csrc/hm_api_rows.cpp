@@ -31,8 +31,7 @@ hm_status check_dispatch(int64_t t, int32_t topk, int32_t num_experts) {
 
 size_t dispatch_ws(int64_t t, int32_t topk, int32_t num_experts) {
   if (t * topk <= kSortDispatch) return 0;
-  const int nb = moe_sort_blocks(t * topk, nullptr);
-  return nb > 1 ? (size_t)nb * (size_t)num_experts * sizeof(int32_t) : 0;
+  return (size_t)moe_sort_blocks(t * topk, nullptr) * (size_t)num_experts * sizeof(int32_t);
 }
 
 hm_status done(hipError_t e) { return e == hipSuccess ? HM_OK : HM_ERR_HIP; }

@@ -33,10 +33,9 @@ __device__ void expert_offsets(const int* tot, int* base, int E, int* wsum, bool
 
 // Deterministic, stable counting sort of pair ids by expert in one block
 // (few pairs).
-template <bool POS>
 __global__ void __launch_bounds__(kSortThreads)
 k_moe_sort(const int32_t* __restrict__ ids, int64_t P, int E, int32_t* __restrict__ counts,
-           int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pairs, int32_t* __restrict__ positions) {
+           int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pairs) {
   __shared__ int hist[kSortWaves][512];
   __shared__ int tot[512], base[512];
   __shared__ int wsum[8];
@@ -49,7 +48,7 @@ k_moe_sort(const int32_t* __restrict__ ids, int64_t P, int E, int32_t* __restric
   }
   __syncthreads();
   expert_offsets(tot, base, E, wsum, true, counts, offsets);
-  sort_range<POS>(ids, 0, P, E, base, hist, sorted_pairs, positions);
+  sort_range<false>(ids, 0, P, E, base, hist, sorted_pairs, nullptr);
 }
 
 // GPU-wide sort, pass 1: block b counts the pairs of its chunk
@@ -169,16 +168,11 @@ k_moe_schedule(const int32_t* __restrict__ offsets, int E, int64_t P, int s_rows
 }
 
 
+// the GPU-wide sort, in nb chunks of C pairs
 template <bool POS>
-static hipError_t run_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* counts, int32_t* offsets,
-                               int32_t* sorted_pairs, int32_t* positions, int32_t* cnt, hipStream_t st) {
-  int64_t C = 0;
-  const int nb = moe_sort_blocks(P, &C);
-  if (nb == 1) {
-    hipLaunchKernelGGL(k_moe_sort<POS>, dim3(1), dim3(kSortThreads), 0, st, ids, P, E, counts, offsets,
-                       sorted_pairs, positions);
-    return hipGetLastError();
-  }
+static hipError_t chunked_sort(const int32_t* ids, int64_t P, int E, int64_t C, int nb, int32_t* counts,
+                               int32_t* offsets, int32_t* sorted_pairs, int32_t* positions, int32_t* cnt,
+                               hipStream_t st) {
   hipLaunchKernelGGL(k_moe_sort_count, dim3(nb), dim3(kSortThreads), 0, st, ids, P, E, C, cnt);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -189,12 +183,18 @@ static hipError_t run_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* co
 
 hipError_t launch_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* counts, int32_t* offsets,
                            int32_t* sorted_pairs, int32_t* cnt, hipStream_t st) {
-  return run_moe_sort<false>(ids, P, E, counts, offsets, sorted_pairs, nullptr, cnt, st);
+  int64_t C = 0;
+  const int nb = moe_sort_blocks(P, &C);
+  if (nb > 1) return chunked_sort<false>(ids, P, E, C, nb, counts, offsets, sorted_pairs, nullptr, cnt, st);
+  hipLaunchKernelGGL(k_moe_sort, dim3(1), dim3(kSortThreads), 0, st, ids, P, E, counts, offsets, sorted_pairs);
+  return hipGetLastError();
 }
 
 hipError_t launch_moe_sort_pos(const int32_t* ids, int64_t P, int E, int32_t* counts, int32_t* offsets,
                                int32_t* sorted_pairs, int32_t* positions, int32_t* cnt, hipStream_t st) {
-  return run_moe_sort<true>(ids, P, E, counts, offsets, sorted_pairs, positions, cnt, st);
+  int64_t C = 0;
+  const int nb = moe_sort_blocks(P, &C);
+  return chunked_sort<true>(ids, P, E, C, nb, counts, offsets, sorted_pairs, positions, cnt, st);
 }
 
 hipError_t launch_moe_schedule(const int32_t* offsets, int E, int64_t P, int s_rows, int s_max, int bm,

@@ -65,7 +65,7 @@ constexpr int kSortMaxBlocks = 512;
 int moe_sort_blocks(int64_t P, int64_t* chunk);
 hipError_t launch_moe_sort(const int32_t* ids, int64_t P, int E, int32_t* counts, int32_t* offsets,
                            int32_t* sorted_pairs, int32_t* cnt, hipStream_t st);
-// the same with each pair's position (-1: dropped)
+// the same with each pair's position (-1: dropped), in chunks: more pairs than kSortDispatch
 hipError_t launch_moe_sort_pos(const int32_t* ids, int64_t P, int E, int32_t* counts, int32_t* offsets,
                                int32_t* sorted_pairs, int32_t* positions, int32_t* cnt, hipStream_t st);
 hipError_t launch_moe_schedule(const int32_t* offsets, int E, int64_t P, int s_rows, int s_max, int bm,

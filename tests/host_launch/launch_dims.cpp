@@ -145,6 +145,13 @@ int main() {
   long total = 0;
   for (const auto& k : g_launches) total += k.second;
   need(g_launches.size() > 40 && total > 100000, "launches of every kernel");
+  // every kernel of these operators is reached by some size; hm_moe_sort and the grouped GEMM have the others of k_moe
+  for (const auto& k : names()) {
+    const std::string& s = k.second;
+    if (s.find("k_moe_sortILb0") != s.npos || s.find("k_moe_sort_placeILb0") != s.npos || s.find("k_moe_schedule") != s.npos) continue;
+    if (!g_launches.count(s)) printf("never launched: %s\n", s.c_str());
+    need(g_launches.count(s) != 0, "a kernel that no call reaches");
+  }
   printf("launch shapes ok: %ld launches of %zu kernels\n", total, g_launches.size());
   return 0;
 }
