@@ -410,7 +410,10 @@ hm_status hm_moe_dispatch_workspace_size(int64_t t, int32_t topk, int32_t num_ex
  *                 a dropped pair (id outside [0, num_experts)).
  * hm_moe_gemm runs on the rows of xs with a_rows_are_pairs = 1, t*topk
  * "tokens", topk = 1, these offsets and the identity 0, 1, 2, ... as
- * sorted_pairs; its output is then in expert order too.
+ * sorted_pairs; its output is then in expert order too.  Its own gather
+ * (a_rows_are_pairs = 0, sorted_pairs of hm_moe_sort) reads the tokens without
+ * this copy: prefer it where the rows are not needed in expert order for
+ * something else, such as an exchange between ranks or a gradient.
  * Any n >= 1; x and xs 16-byte aligned, the integer arrays 4-byte; limits on
  * t, topk and num_experts as hm_moe_sort.  t = 0 is a no-op: counts and
  * offsets are not written either.  No output may overlap x, topk_ids, ws or
@@ -443,7 +446,9 @@ hm_status hm_moe_collect(const uint16_t* ys, const float* w, const int32_t* posi
  *   dw[t'][j] = sum_c dout[t'][c] * ys[positions[t'][j]][c]   (fp32),
  * dw = 0 for a dropped pair; rows of dys that no position names are left as
  * they were.  No two positions in [0, t*topk) may be equal (hm_moe_dispatch
- * gives none), else which pair's row stays is unspecified.
+ * gives none), else which pair's row stays is unspecified, and so are their dw
+ * where dys is ys.  With positions[t'][j] = t'*topk + j this is the gradient of
+ * hm_moe_combine.
  *   dout bf16 [t][n]; ys, dys bf16 [t*topk][n]; w, dw fp32 [t][topk].  dys may
  *   be ys itself (each row is read before it is written); otherwise no
  *   overlaps.

@@ -536,7 +536,8 @@ def hm_moe_collect(ys, weights, positions, out=None, stream=None):
 def hm_moe_collect_grad(dout, ys, weights, positions, dys=None, dweights=None, stream=None):
     """Gradient of hm_moe_collect: dout bf16 [t, n] -> (dys bf16 [t*topk, n],
     dweights fp32 [t, topk]).  Rows of dys that no position names are left as
-    they were (zeros when allocated here).  dys may be ys."""
+    they were (zeros when allocated here).  dys may be ys.  With positions 0, 1,
+    2, ... it is the gradient of hm_moe_combine."""
     ctx = _elsewhere(dout, stream)
     if ctx is not None:
         with ctx:

@@ -50,9 +50,9 @@ constexpr int64_t kMaxBlocks = (1ll << 24) - 1;
 // Calls that run both products in one launch: up to 16 rows, and an A (of
 // padded rank) that every block can read by itself.  One launch against two,
 // and as a Python loop issues them (the host needs 3 us a launch): m = 1, k =
-// 2048, n = 7168, rank 16 6.6 against 7.6 us, 8.4 against 10.7; m = 8, k = 4096,
-// n = 14336, rank 16 7.9 against 8.2, 8.3 against 10.9; beyond: rank 64 (262144
-// values) 15.9 against 9.8, m = 48 13.8 against 12.1.
+// 2048, n = 7168, rank 16 6.9 against 7.8 us, 8.5 against 10.7; m = 8, k = 4096,
+// n = 14336, rank 16 8.3 against 8.4, 8.4 against 10.9; beyond: rank 64 (262144
+// values) 16.5 against 10.3, m = 48 14.3 against 12.5.
 constexpr int64_t kSmallA = 131072;
 constexpr int64_t kSmallRows = 16;
 
@@ -68,8 +68,12 @@ struct LoraPlan {
 // Rows per unit: 64 where the adapters can have that many rows each on average
 // (every loaded value of A and B then serves four MFMAs), fewer where units
 // would be mostly empty: m = 256, 32 adapters of rank 64, k = 7168, n = 4096
-// 22.3 us with 16 rows, 26.4 with 64; m = 128, 40 of rank 128, k = 4096, n =
-// 7168 39.4 against 44.3.
+// 22.6 us with 16 rows, 26.8 with 64; m = 128, 40 of rank 128, k = 4096, n =
+// 7168 39.7 against 45.0.  The rule sees the adapters that are loaded, not those
+// in use, which can go either way: with 6 of 512 in use, m = 8192, k = 4096, n =
+// 14336, rank 64 takes 231 us where 64-row units would take 169 (6 loaded: 148);
+// with 7 of 64, m = 1021, k = 7168, n = 4099 36.5 against 28.1; with 4 of 512,
+// m = 256, k = 7168, n = 4096 27.4 against 36.3.
 int rows_per_unit(int64_t m, int64_t L) { return m <= 16 * L ? 16 : (m <= 32 * L ? 32 : 64); }
 
 hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) {
@@ -79,8 +83,8 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
   w.unit_rows = grad ? kLoraUnit : (w.direct ? 16 : rows_per_unit(m, L));
   w.max_units = w.direct ? m : m / w.unit_rows + std::min<int64_t>(L, m);
   // blocks along the contraction: about 4096 waves in all (16-row units) or
-  // 640 blocks (32-row blocks; m = 8192, rank 64: 1024 blocks cost 5 us more in
-  // sums that the expansion reads again), each wave keeping a step of 64 or more
+  // 640 blocks (32-row blocks; m = 8192, rank 64: 1024 blocks cost 3 us more, a gradient of rank 32 12 us, in
+  // sums that are read again), each wave keeping a step of 64 or more
   const bool few = w.unit_rows == 16;
   const int rp = lora_rp(d->rank);
   const int64_t blocks = few ? w.max_units : w.max_units * (w.unit_rows / 32);
@@ -88,9 +92,10 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
   const int64_t want = few ? 4096 / (blocks * waves) : 640 / blocks;
   const int64_t most = std::min<int64_t>(lora_max_splits(rp, w.unit_rows, grad), len / (64 * waves));
   w.splits = (int)std::max<int64_t>(1, std::min(want, most));
-  // expanding blocks: two units against one part of B where there are many (m = 8192: 150 us, 151 with four, 165 with
-  // eight), several parts of the columns where there are many units of few rows (m = 48, n = 14336: 12.1 us with 512
-  // columns a block, 13.5 with 1024)
+  // expanding blocks: two units against one part of B where there are many (m = 8192, n = 14336, rank 64: 148 us, 154
+  // with one, 152 with four; rank 16: 116, 113, 119), several parts of the columns where there are many units of few
+  // rows (rank 16: m = 48, n = 14336 12.6 us, 13.0 with one part; m = 128 24.1 against 28.0; m = 32, n = 28672 17.2
+  // against 18.3; rank 64, m = 64 31.8 against 31.3; where one adapter has all 64 rows 12.3 against 10.5)
   int64_t slabs = 8 * ((cols + 8 * kLoraCols - 1) / (8 * kLoraCols));
   w.group = w.direct || w.unit_rows < 64 ? 1 : (w.max_units * slabs >= 2048 ? 2 : 1);
   w.cols = kLoraCols;
@@ -123,8 +128,8 @@ hm_status plan_lora(const hm_lora_desc* d, int64_t m, bool grad, LoraPlan* out) 
     const size_t packed = (size_t)w.max_units * kTerms * (size_t)lora_rp(d->rank) * kLoraUnit * 2;
     w.gt = take(packed);
     w.ht = take(packed);
-    // about 768 blocks, three to a compute unit (m = 8192, rank 32: 67 us; 512 78, 1024 72), a chunk of four units or
-    // more (m = 777, rank 16: 32.4 us a call; of sixteen 37.3)
+    // about 768 blocks, three to a compute unit (m = 8192, k = 4096, n = 14336, rank 32: 159 us a call; 512 168, 1024
+    // 165; rank 64: 231, 252, 239), a chunk of four units or more (m = 777, rank 16: 33.3 us a call; of sixteen 38.1)
     const int64_t tiles = ((d->n + 127) / 128 + d->k / 128) * std::max(1, lora_rp(d->rank) / 32);
     w.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(16, std::min((767 + tiles) / tiles, w.max_units / 4)));
     w.sums = take(w.chunks > 1 ? (size_t)(2 * w.chunks) * (size_t)d->rank * (size_t)(d->k + d->n) * 4 : 0);

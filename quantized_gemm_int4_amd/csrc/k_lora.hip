@@ -185,7 +185,7 @@ __device__ __forceinline__ int chunk_at(int r, int k) { return r * 128 + ((k ^ (
 // of 16 bytes each and the address unit, not HBM, sets the pace (m = 8192, k =
 // 4096, rank 64: 50 us).  So a wave loads eight whole lines per instruction
 // into registers, one step ahead, and passes them through its own LDS image;
-// no block barrier.  Now 25 us, of which reading x at the copy rate takes 13;
+// no block barrier.  Now 26 us, of which reading x at the copy rate takes 13;
 // dy with n = 14336, rank 32: 41 us, 5.7 TB/s.
 template <int RP, int T, bool DIRECT, bool TRANS, int NW>
 __global__ void __launch_bounds__(64 * NW) k_lora_shrink(LoraArgs g) {
@@ -345,7 +345,7 @@ __device__ __forceinline__ void copy_rest(const LoraArgs& g, int64_t m0, int64_t
 // ends up with columns 4 c .. 4 c + 3 of rows 4 q + v: sixteen lanes read base
 // and write y 128 consecutive bytes at a time (with the rows along the lanes
 // instead, 16 bytes each, the address unit bound the kernel: m = 8192, n =
-// 14336, rank 64 132 us; now 107 us, 4.4 TB/s of base and y).  Blocks go round
+// 14336, rank 64 132 us; now 112 us, 4.2 TB/s of base and y).  Blocks go round
 // the XCDs one by one, so block id i takes its columns from the eighth i % 8:
 // each XCD sees an eighth of B_e, which stays in its L2 from group to group,
 // and writes neighbouring parts of a row.

@@ -9,10 +9,10 @@
 // All three only move bf16 rows: every row of the token side is read (or
 // written) once and every row of the expert side once, so they are bound by
 // HBM, and calls of few tokens by their launches and round trips.  Measured at
-// n = 7168, topk = 8 (a 1 GiB device copy runs at 5.08 TB/s, read and written
-// bytes together): dispatch t = 8192 205 us, 5.1 TB/s; collect and the
-// dispatch's gradient t = 4096 103 us, 5.1 TB/s; collect's gradient t = 4096
-// 199 us, 5.0 TB/s; t = 64 dispatch 5.9 us, collect 4.0 us.
+// n = 7168, topk = 8 (a 1 GiB device copy runs at 5.1 TB/s, read and written
+// bytes together): dispatch t = 8192 205 us, 5.2 TB/s; collect and the
+// dispatch's gradient t = 4096 103 us, 5.1 TB/s, t = 8192 205 us; collect's
+// gradient t = 4096 199 us, 5.0 TB/s; t = 64 dispatch 5.9 us, collect 4.0 us.
 #include "common.h"
 #include "launch.h"
 #include "rows.h"
@@ -323,7 +323,9 @@ hipError_t launch_collect(const uint16_t* ys, const float* w, const int32_t* pos
 
 hipError_t launch_collect_grad(const uint16_t* dout, const uint16_t* ys, const float* w, const int32_t* positions,
                                int64_t t, int topk, int64_t n, uint16_t* dys, float* dw, hipStream_t st) {
-  // a launch stays under 2^32 threads: from 2^23 tokens on blocks of 256, whatever n
+  // A block's threads take 8 columns each, so 512 of them would idle below n = 4096, or wait for little work: topk = 8,
+  // n = 2048, t = 4096 49 us with 256 threads, 61 with 512 (n = 1024: 29, 44); n = 7168, t = 64 11.2 with 256, 9.2 with
+  // 512, t = 4096 208 and 206.  A launch stays under 2^32 threads: from 2^23 tokens on 256, whatever n.
   const int threads = n <= 2048 || t >= (1 << 23) ? 256 : 512;
   hipLaunchKernelGGL(k_collect_grad, dim3((unsigned)t), dim3(threads), 0, st, dout, ys, w, positions, t, topk, n, dys,
                      dw);

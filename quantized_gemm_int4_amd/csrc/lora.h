@@ -11,8 +11,8 @@ namespace hm {
 constexpr int64_t kLoraMaxRows = 1 << 20;
 // Most rows of a call whose blocks find their unit from the ids themselves (one
 // ballot holds them all) instead of from a grouping launch: m = 48, 24 adapters
-// of rank 16, k = 4096, n = 14336 12.1 us against 16.8; m = 64, 40 of rank 64, k
-// = 2048, n = 7168 17.3 against 22.1.
+// of rank 16, k = 4096, n = 14336 12.5 us against 16.4; m = 64, 40 of rank 64, k
+// = 2048, n = 7168 17.7 against 22.3.
 constexpr int kLoraDirect = 64;
 constexpr int kLoraPlanBlocks = 256; // most blocks of the grouping kernel
 constexpr int kLoraUnit = 64;        // rows per unit of the gradient

@@ -59,8 +59,10 @@ __device__ __forceinline__ void st4_tail(uint16_t* row, int64_t c, int64_t n, u3
 // 8.6 with a sort of its own.
 constexpr int64_t kSmallPairs = 1024;
 // Pairs that are sorted in one launch, each block counting all ids, where a
-// chunked sort counts and places in two: 4000 pairs 10.7 us with the rows (n =
-// 2048) against 13.4; 65536 pairs 207.1 us (n = 7168) against 205.4.
+// chunked sort counts and places in two: with rows of n = 2048, topk = 8, 2048
+// pairs 9.1 us against 11.7, 8192 14.0 against 16.6, 32768 33.6 against 34.3,
+// and 65536 65.4 against 63.0; of n = 7168, 8192 pairs 27.9 against 30.5, 65536
+// 208 against 204.
 constexpr int64_t kSortDispatch = 32768;
 hipError_t launch_dispatch_small(const uint16_t* x, const int32_t* ids, int64_t t, int topk, int E, int64_t n,
                                  uint16_t* xs, int32_t* counts, int32_t* offsets, int32_t* sorted_pairs,
