@@ -805,8 +805,10 @@ def ingest_counters(fetch_dir, write_dir):
     import glob
 
     def load(d, counter):
-        f = glob.glob(os.path.join(d, "**", "*counter_collection.csv"), recursive=True)[0]
-        rows = [r for r in csv.DictReader(open(f)) if r["Counter_Name"] == counter]
+        f = glob.glob(os.path.join(d, "**", "*counter_collection.csv"), recursive=True)
+        if len(f) != 1:
+            raise ValueError(f"{d}: need one counter file of one run, found {len(f)}")
+        rows = [r for r in csv.DictReader(open(f[0])) if r["Counter_Name"] == counter]
         rows.sort(key=lambda r: int(r["Dispatch_Id"]))
         return rows
 
