@@ -490,8 +490,8 @@ hm_status hm_lora_workspace_size(const hm_lora_desc* d, int64_t m, size_t* bytes
  *   base        bf16 [m][n], the shared projection's output (hm_gemm), or NULL
  *               for zeros.  May be y itself: the adapters are then added in
  *               place, and rows without an adapter are not touched.
- *   y           bf16 [m][n]; must not overlap x, a, b, or base in any other
- *               way (HM_ERR_UNSUPPORTED).
+ *   y           bf16 [m][n]; must not overlap an input in any other way
+ *               (HM_ERR_UNSUPPORTED for x, a, b and base).
  *   h           fp32 [m][rank], what hm_lora_grad needs; NULL if not wanted.
  *   ws          hm_lora_workspace_size bytes, overwritten.
  * h and ws must overlap no other array.
@@ -519,8 +519,9 @@ hm_status hm_lora_grad_workspace_size(const hm_lora_desc* d, int64_t m, size_t* 
  *   da          bf16 [num_adapters][rank][k];  db bf16 [num_adapters][n][rank];
  *               adapters that no row names get zeros.
  *   ws          hm_lora_grad_workspace_size bytes, overwritten.
- * dx, da and db must not overlap dy, x, h, a, b, or dx_base in any other way
- * (HM_ERR_UNSUPPORTED), nor each other; ws must overlap no other array.
+ * dx, da and db must not overlap an input in any other way (HM_ERR_UNSUPPORTED
+ * for dy, x, h, a, b and dx_base), nor each other; ws must overlap no other
+ * array.
  * m = 0 writes zeros to da and db; limits as hm_lora. */
 hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const uint16_t* x, const float* h,
                        const int32_t* adapter_ids, const uint16_t* a, const uint16_t* b, const float* scales,
