@@ -59,7 +59,7 @@ typedef enum hm_status {
   HM_ERR_NULL = 1,        /* a required pointer is NULL */
   HM_ERR_SHAPE = 2,       /* bad size, group or count */
   HM_ERR_ALIGN = 3,       /* pointer not aligned as required */
-  HM_ERR_UNSUPPORTED = 4, /* unknown weight format or format/activation pair; arrays that overlap (hm_lora, hm_lora_grad) */
+  HM_ERR_UNSUPPORTED = 4, /* unknown weight format or format/activation pair; arrays that overlap (hm_lora, hm_lora_grad, the int8 calls) */
   HM_ERR_WORKSPACE = 5,   /* buffer smaller than its size query */
   HM_ERR_HIP = 6,         /* a HIP launch failed */
   HM_ERR_ABI = 7,         /* descriptor abi field != HM_ABI_VERSION */
@@ -527,6 +527,91 @@ hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const uint16_t
                        const int32_t* adapter_ids, const uint16_t* a, const uint16_t* b, const float* scales,
                        int64_t m, const uint16_t* dx_base, uint16_t* dx, uint16_t* da, uint16_t* db, void* ws,
                        size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------- 8-bit integer layers */
+
+/* Linear layers whose activations and weights are both 8-bit integers, with
+ * one fp32 scale per token (row of X) and one per output channel (row of W):
+ *   x_hat[m,k] = x_scales[m] x8[m,k],   w_hat[n,k] = w_scales[n] w8[n,k]
+ * (W8A8 among the GEMM types that the pages list, cocoloop.cn news item, format
+ * list; per-token scales: ywsung.com note, section on weight format /
+ * activation / backend).  Both are plain row-major int8 arrays, x8 [m][k] and
+ * w8 [n][k], as hm_quant_int8_rows writes them (rows of W are its rows too), so
+ * weights that change every training step need no repacking.  A training step
+ * keeps the codes and scales of its rows, a byte a value, instead of the bf16
+ * activations: the gradients below need nothing else of the forward pass.
+ *
+ * Sizes of all of them: 0 <= m <= 8388480; 1 <= n <= 2^22; k a multiple of 128,
+ * 128 .. 130944 (every sum of k products then fits an int32: sums are exact);
+ * ceil(m/128) ceil(n/128) < 2^24 - 8, and the same of (m, k) and (n, k) for the
+ * gradient.  HM_ERR_SHAPE otherwise.  Codes may be any int8, scales any finite
+ * fp32; a NaN or infinite scale makes its row (token) or column (channel) of
+ * the results NaN or infinite and leaves the others alone, but where it is
+ * summed over (hm_gemm_int8_grad) unspecified.  bf16 and int8 arrays and h are
+ * 16-byte aligned, scales 4-byte, ws 256-byte (HM_ERR_ALIGN).  No output nor ws
+ * may overlap an input or another output (HM_ERR_UNSUPPORTED). */
+
+/* Codes and scales of rows, x bf16 [m][k] -> x8 int8 [m][k], row_scale fp32 [m]:
+ *   row_scale[m] = amax_k |x[m,k]| / 127  (fp32 division),
+ *   x8[m,k] = the whole number nearest to 127 x[m,k] / amax, ties to even,
+ * the quotient exact (codes lie in -127..127).  A row of zeros gives scale 0 and
+ * zero codes; a row that holds an infinity or a NaN gives scale NaN and zero
+ * codes, so that products of it are NaN.  m = 0 is a no-op; any k >= 1, m k <=
+ * 2^39 (HM_ERR_SHAPE). */
+hm_status hm_quant_int8_rows(const uint16_t* x, int64_t m, int64_t k, int8_t* x8, float* row_scale,
+                             hipStream_t stream);
+
+/* Workspace bytes hm_gemm_int8 needs (may be 0). */
+hm_status hm_gemm_int8_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+
+/* y[m][n] = bf16( (sum_k x8[m,k] w8[n,k]) x_scales[m] w_scales[n] ): the sum as an
+ * exact int32, converted to fp32 and multiplied in fp32 in this order.
+ * m = 0 is a no-op. */
+hm_status hm_gemm_int8(const int8_t* x8, const float* x_scales, const int8_t* w8, const float* w_scales,
+                       int64_t m, int64_t n, int64_t k, uint16_t* y, void* ws, size_t ws_bytes,
+                       hipStream_t stream);
+
+/* Workspace bytes of the two gated calls (may be 0); n as there. */
+hm_status hm_gemm_int8_gated_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+hm_status hm_gemm_int8_gated_grad_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+
+/* The first half of a gated feed-forward block: both projections, SiLU and the
+ * product in one call.  w8 [n][k] holds n = 2d rows, gate rows 0..d-1, up rows
+ * d..2d-1 (any d >= 1; an odd n gives HM_ERR_SHAPE); with g and u the fp32
+ * products of hm_gemm_int8 before their rounding,
+ *   h[m][i] = bf16( silu(g[m,i]) u[m,i] ),  silu(g) = g / (1 + exp(-g)).
+ *   h bf16 [m][n/2].  m = 0 is a no-op.  (hm_gemm_int8 followed by hm_silu_mul
+ * rounds g and u to bf16 in between.) */
+hm_status hm_gemm_int8_gated(const int8_t* x8, const float* x_scales, const int8_t* w8, const float* w_scales,
+                             int64_t m, int64_t n, int64_t k, uint16_t* h, void* ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+/* The gradient of hm_gemm_int8_gated to its gate and up products, which are
+ * computed again from the 8-bit rows (they are never stored): with s = 1 / (1 + exp(-g)),
+ *   dgu[m][i]     = bf16( dh[m,i] u s (1 + g (1 - s)) ),
+ *   dgu[m][d + i] = bf16( dh[m,i] g s ).
+ *   dh bf16 [m][n/2]; dgu bf16 [m][n]: the dy of hm_gemm_int8_grad (and of
+ * hm_lora_grad) for the gate_up projection.  m = 0 is a no-op. */
+hm_status hm_gemm_int8_gated_grad(const uint16_t* dh, const int8_t* x8, const float* x_scales, const int8_t* w8,
+                                  const float* w_scales, int64_t m, int64_t n, int64_t k, uint16_t* dgu, void* ws,
+                                  size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes hm_gemm_int8_grad needs (for either gradient or both). */
+hm_status hm_gemm_int8_grad_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+
+/* The gradient of y = x_hat w_hat^T to its factors (quantization passes
+ * gradients straight through, so they are those to the bf16 rows and weights
+ * that the codes were made from):
+ *   dx[m][k] = bf16( sum_n dy[m,n] w~[n,k] ),  w~ = bf16(w_scales[n] w8[n,k]),
+ *   dw[n][k] = bf16( sum_m dy[m,n] x~[m,k] ),  x~ = bf16(x_scales[m] x8[m,k]),
+ * summed in fp32 in an order that the sizes fix (equal calls give equal bits).
+ *   dy bf16 [m][n];  dx bf16 [m][k] and dw bf16 [n][k]: either may be NULL if not
+ *   wanted (both: HM_ERR_NULL); the scales and codes that only the other needs
+ *   may be NULL then.  m = 0 writes zeros to dw.
+ *   dx can be the dx_base of hm_lora_grad where the layer has adapters. */
+hm_status hm_gemm_int8_grad(const uint16_t* dy, const int8_t* x8, const float* x_scales, const int8_t* w8,
+                            const float* w_scales, int64_t m, int64_t n, int64_t k, uint16_t* dx, uint16_t* dw,
+                            void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------ measurement */
 

@@ -125,6 +125,15 @@ def _load():
         "hm_lora": [LD, P, P, P, P, P, I64, P, P, P, P, SZ, P],
         "hm_lora_grad_workspace_size": [LD, I64, ctypes.POINTER(SZ)],
         "hm_lora_grad": [LD, P, P, P, P, P, P, P, I64, P, P, P, P, P, SZ, P],
+        "hm_quant_int8_rows": [P, I64, I64, P, P, P],
+        "hm_gemm_int8_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],
+        "hm_gemm_int8": [P, P, P, P, I64, I64, I64, P, P, SZ, P],
+        "hm_gemm_int8_gated_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],
+        "hm_gemm_int8_gated": [P, P, P, P, I64, I64, I64, P, P, SZ, P],
+        "hm_gemm_int8_gated_grad_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],
+        "hm_gemm_int8_gated_grad": [P, P, P, P, P, I64, I64, I64, P, P, SZ, P],
+        "hm_gemm_int8_grad_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],
+        "hm_gemm_int8_grad": [P, P, P, P, P, I64, I64, I64, P, P, P, SZ, P],
         "hm_moe_gemm_static": [D, P, I32, P, P, I32, I64, I32, P, P, P, T, P],
     }
     for name, args in sig.items():
@@ -624,6 +633,122 @@ def hm_lora_grad(desc, dy, x, h, adapter_ids, a, b, scales, dx_base=None, dx=Non
                             _stream())
     _ok("hm_lora_grad", code)
     return dx, da, db
+
+
+# -------------------------------------------------------- 8-bit integer layers
+
+def hm_quant_int8_rows(x, x8=None, row_scale=None, stream=None):
+    """x bf16 [m, k] -> (int8 codes [m, k], fp32 row scales [m]): activations of
+    the calls below, and their weights (bf16 rows of W)."""
+    ctx = _elsewhere(x, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_quant_int8_rows(x, x8, row_scale)
+    (m, k), dev = _dims(x, "x"), x.get_device()
+    x8 = _new(torch.int8, (m, k), dev) if x8 is None else x8
+    row_scale = _new(torch.float32, (m,), dev) if row_scale is None else row_scale
+    code = lib.hm_quant_int8_rows(_arg(x, torch.bfloat16, (m, k), "x", dev), m, k, _arg(x8, torch.int8, (m, k), "x8", dev),
+                                  _arg(row_scale, torch.float32, (m,), "row_scale", dev), _stream())
+    _ok("hm_quant_int8_rows", code)
+    return x8, row_scale
+
+
+def _int8_ws_size(fn, m, n, k):
+    out = ctypes.c_size_t()
+    _ok(fn, getattr(lib, fn)(int(m), int(n), int(k), ctypes.byref(out)))
+    return out.value
+
+
+def hm_gemm_int8_workspace_size(m, n, k):
+    return _int8_ws_size("hm_gemm_int8_workspace_size", m, n, k)
+
+
+def hm_gemm_int8_gated_workspace_size(m, n, k):
+    return _int8_ws_size("hm_gemm_int8_gated_workspace_size", m, n, k)
+
+
+def hm_gemm_int8_gated_grad_workspace_size(m, n, k):
+    return _int8_ws_size("hm_gemm_int8_gated_grad_workspace_size", m, n, k)
+
+
+def hm_gemm_int8_grad_workspace_size(m, n, k):
+    return _int8_ws_size("hm_gemm_int8_grad_workspace_size", m, n, k)
+
+
+def _int8_args(x8, x_scales, w8, w_scales, dev):
+    (m, k), n = x8.shape, w8.shape[0]
+    return (_arg(x8, torch.int8, (m, k), "x8", dev), _arg(x_scales, torch.float32, (m,), "x_scales", dev),
+            _arg(w8, torch.int8, (n, k), "w8", dev), _arg(w_scales, torch.float32, (n,), "w_scales", dev))
+
+
+def hm_gemm_int8(x8, x_scales, w8, w_scales, y=None, ws=None, stream=None):
+    """x8 int8 [m, k] with fp32 x_scales [m], w8 int8 [n, k] with fp32 w_scales
+    [n] -> y bf16 [m, n], the product of the values the codes stand for."""
+    ctx = _elsewhere(x8, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_gemm_int8(x8, x_scales, w8, w_scales, y, ws)
+    (m, k), (n, _), dev = _dims(x8, "x8"), _dims(w8, "w8"), x8.get_device()
+    y = _new(torch.bfloat16, (m, n), dev) if y is None else y
+    wsp, wsb, ws = _ws(ws, hm_gemm_int8_workspace_size, (m, n, k), dev)
+    code = lib.hm_gemm_int8(*_int8_args(x8, x_scales, w8, w_scales, dev), m, n, k,
+                            _arg(y, torch.bfloat16, (m, n), "y", dev), wsp, wsb, _stream())
+    _ok("hm_gemm_int8", code)
+    return y
+
+
+def hm_gemm_int8_gated(x8, x_scales, w8, w_scales, h=None, ws=None, stream=None):
+    """hm_gemm_int8 of a gate_up weight (w8 int8 [2d, k], gate rows, then up
+    rows) with the gated activation: h bf16 [m, d] = silu(gate) * up."""
+    ctx = _elsewhere(x8, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_gemm_int8_gated(x8, x_scales, w8, w_scales, h, ws)
+    (m, k), (n, _), dev = _dims(x8, "x8"), _dims(w8, "w8"), x8.get_device()
+    h = _new(torch.bfloat16, (m, n // 2), dev) if h is None else h
+    wsp, wsb, ws = _ws(ws, hm_gemm_int8_gated_workspace_size, (m, n, k), dev)
+    code = lib.hm_gemm_int8_gated(*_int8_args(x8, x_scales, w8, w_scales, dev), m, n, k,
+                                  _arg(h, torch.bfloat16, (m, n // 2), "h", dev), wsp, wsb, _stream())
+    _ok("hm_gemm_int8_gated", code)
+    return h
+
+
+def hm_gemm_int8_gated_grad(dh, x8, x_scales, w8, w_scales, dgu=None, ws=None, stream=None):
+    """Gradient of hm_gemm_int8_gated to its gate and up products, which are
+    computed again from the 8-bit rows: dh bf16 [m, d] -> dgu bf16 [m, 2d]."""
+    ctx = _elsewhere(x8, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_gemm_int8_gated_grad(dh, x8, x_scales, w8, w_scales, dgu, ws)
+    (m, k), (n, _), dev = _dims(x8, "x8"), _dims(w8, "w8"), x8.get_device()
+    dgu = _new(torch.bfloat16, (m, n), dev) if dgu is None else dgu
+    wsp, wsb, ws = _ws(ws, hm_gemm_int8_gated_grad_workspace_size, (m, n, k), dev)
+    code = lib.hm_gemm_int8_gated_grad(_arg(dh, torch.bfloat16, (m, n // 2), "dh", dev),
+                                       *_int8_args(x8, x_scales, w8, w_scales, dev), m, n, k,
+                                       _arg(dgu, torch.bfloat16, (m, n), "dgu", dev), wsp, wsb, _stream())
+    _ok("hm_gemm_int8_gated_grad", code)
+    return dgu
+
+
+def hm_gemm_int8_grad(dy, x8, x_scales, w8, w_scales, dx=None, dw=None, need_dx=True, need_dw=True, ws=None, stream=None):
+    """Gradient of hm_gemm_int8 to its rows and weights: dy bf16 [m, n] -> (dx
+    bf16 [m, k] or None, dw bf16 [n, k] or None); need_dx=False, need_dw=False leave
+    one out."""
+    ctx = _elsewhere(x8, stream)
+    if ctx is not None:
+        with ctx:
+            return hm_gemm_int8_grad(dy, x8, x_scales, w8, w_scales, dx, dw, need_dx, need_dw, ws)
+    if (not need_dx and dx is not None) or (not need_dw and dw is not None):
+        raise ValueError("need_dx=False takes no dx, need_dw=False no dw")
+    (m, k), (n, _), dev, bf = _dims(x8, "x8"), _dims(w8, "w8"), x8.get_device(), torch.bfloat16
+    dx = _new(bf, (m, k), dev) if need_dx and dx is None else dx
+    dw = _new(bf, (n, k), dev) if need_dw and dw is None else dw
+    wsp, wsb, ws = _ws(ws, hm_gemm_int8_grad_workspace_size, (m, n, k), dev)
+    code = lib.hm_gemm_int8_grad(_arg(dy, bf, (m, n), "dy", dev), *_int8_args(x8, x_scales, w8, w_scales, dev), m, n, k,
+                                 None if dx is None else _arg(dx, bf, (m, k), "dx", dev),
+                                 None if dw is None else _arg(dw, bf, (n, k), "dw", dev), wsp, wsb, _stream())
+    _ok("hm_gemm_int8_grad", code)
+    return dx, dw
 
 
 # ----------------------------------------------------------------- measurement

@@ -1,0 +1,281 @@
+// C ABI entry points of the 8-bit integer layers: argument checks, workspace
+// layout and launches.  Every check runs before any launch; nothing is
+// allocated.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "../../include/hm.h"
+#include "common.h"
+#include "i8.h"
+
+#define HM_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using namespace hm;
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// An array of a call.  No array is longer than the card's memory (288 GB), so
+// lengths end at 2^39 and ends do not wrap.
+struct Span {
+  const void* p;             // null, or no bytes: no array
+  uint64_t bytes;
+};
+bool meets(const Span& a, const Span& b) {
+  if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+  constexpr uint64_t kMost = 1ull << 39;
+  const uint64_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x < y + std::min(b.bytes, kMost) && y < x + std::min(a.bytes, kMost);
+}
+// Whether an output or the workspace meets an input or another of them.
+bool overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (meets(*o, i)) return true;
+    for (const Span* p = o + 1; p != outs.end(); ++p)
+      if (meets(*o, *p)) return true;
+  }
+  return false;
+}
+
+constexpr int64_t kMaxRows = 8388480;         // 65535 x 128, as hm_gemm
+constexpr int64_t kMaxCols = 1ll << 22;       // 256 rows of bf16 gradients stay under 2^31 bytes
+constexpr int64_t kMaxK = 130944;             // below 2^31 / 128^2: no sum of products of two int8 leaves the int32 range
+constexpr int64_t kMaxBlocks = (1ll << 24) - 1;   // of a launch: 2^32 threads
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool tiles_fit(int64_t rows, int64_t cols) { return div_up(rows, kI8Tile) * div_up(cols, kI8Tile) + 7 <= kMaxBlocks; }
+
+// n: rows of the weights (gated: 2 d)
+hm_status check_sizes(int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || m > kMaxRows || n < 1 || n > kMaxCols || k < 128 || (k % 128) != 0 || k > kMaxK) return HM_ERR_SHAPE;
+  return tiles_fit(m, n) ? HM_OK : HM_ERR_SHAPE;
+}
+
+hm_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
+  if (!need) return HM_OK;
+  if (!ws) return HM_ERR_NULL;
+  if (ws_bytes < need) return HM_ERR_WORKSPACE;
+  return aligned(ws, 256) ? HM_OK : HM_ERR_ALIGN;
+}
+
+hm_status done(hipError_t e) { return e == hipSuccess ? HM_OK : HM_ERR_HIP; }
+
+TileArgs product(const int8_t* x8, const float* xs, const int8_t* w8, const float* ws, int64_t m, int64_t n, int64_t k,
+                 uint16_t* out) {
+  TileArgs a{};
+  a.p = (const uint8_t*)w8;
+  a.p_ld = k;
+  a.p_bytes = n * k;
+  a.q = (const uint8_t*)x8;
+  a.q_ld = k;
+  a.q_bytes = m * k;
+  a.rows = m;
+  a.cols = n;
+  a.kbytes = k;
+  a.ps = ws;
+  a.qs = xs;
+  a.out = out;
+  return a;
+}
+
+// Byte offsets in the workspace of the gradient.
+struct GradPlan {
+  size_t dyp, w, x, total;
+  int64_t np;                // columns of the padded copy of dy, 0: dy itself
+};
+GradPlan plan_grad(int64_t m, int64_t n, int64_t k) {
+  GradPlan g{};
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t o = at;
+    at = align256(at + bytes);
+    return o;
+  };
+  if (m == 0) return g;
+  g.np = (n % 8) ? (n + 7) / 8 * 8 : 0;
+  g.dyp = take((size_t)m * (size_t)g.np * 2);
+  g.w = take((size_t)n * (size_t)k * 2);
+  g.x = take((size_t)m * (size_t)k * 2);
+  g.total = at;
+  return g;
+}
+
+}  // namespace
+
+HM_API hm_status hm_quant_int8_rows(const uint16_t* x, int64_t m, int64_t k, int8_t* x8, float* row_scale,
+                                    hipStream_t stream) {
+  if (m < 0 || k < 1) return HM_ERR_SHAPE;
+  if (m == 0) return HM_OK;
+  if (!x || !x8 || !row_scale) return HM_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(x8, 16) || !aligned(row_scale, 4)) return HM_ERR_ALIGN;
+  if (k > (1ll << 39) / m) return HM_ERR_SHAPE;
+  const uint64_t e = (uint64_t)m * (uint64_t)k;
+  if (overlap({{x8, e}, {row_scale, 4ull * m}}, {{x, 2 * e}})) return HM_ERR_UNSUPPORTED;
+  return done(launch_i8_quant_rows(x, m, k, x8, row_scale, stream));
+}
+
+// ------------------------------------------------------------------ products
+
+HM_API hm_status hm_gemm_int8_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+  if (hm_status s = check_sizes(m, n, k)) return s;
+  if (!bytes) return HM_ERR_NULL;
+  *bytes = 0;
+  return HM_OK;
+}
+
+HM_API hm_status hm_gemm_int8(const int8_t* x8, const float* x_scales, const int8_t* w8, const float* w_scales,
+                              int64_t m, int64_t n, int64_t k, uint16_t* y, void* ws, size_t ws_bytes,
+                              hipStream_t stream) {
+  if (hm_status s = check_sizes(m, n, k)) return s;
+  if (m == 0) return HM_OK;
+  if (!x8 || !x_scales || !w8 || !w_scales || !y) return HM_ERR_NULL;
+  if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(y, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
+    return HM_ERR_ALIGN;
+  const size_t need = 0;
+  if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
+  const uint64_t um = m, un = n, uk = k;
+  if (overlap({{y, 2 * um * un}, {ws, need}}, {{x8, um * uk}, {x_scales, 4 * um}, {w8, un * uk}, {w_scales, 4 * un}}))
+    return HM_ERR_UNSUPPORTED;
+  return done(launch_i8_tile(product(x8, x_scales, w8, w_scales, m, n, k, y), I8_FORWARD, stream));
+}
+
+// ---------------------------------------------------------------- gated block
+
+namespace {
+
+hm_status check_gated(int64_t m, int64_t n, int64_t k) {
+  if (hm_status s = check_sizes(m, n, k)) return s;
+  return (n % 2) ? HM_ERR_SHAPE : HM_OK;
+}
+
+}  // namespace
+
+HM_API hm_status hm_gemm_int8_gated_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+  if (hm_status s = check_gated(m, n, k)) return s;
+  if (!bytes) return HM_ERR_NULL;
+  *bytes = 0;
+  return HM_OK;
+}
+
+HM_API hm_status hm_gemm_int8_gated(const int8_t* x8, const float* x_scales, const int8_t* w8, const float* w_scales,
+                                    int64_t m, int64_t n, int64_t k, uint16_t* h, void* ws, size_t ws_bytes,
+                                    hipStream_t stream) {
+  if (hm_status s = check_gated(m, n, k)) return s;
+  if (m == 0) return HM_OK;
+  if (!x8 || !x_scales || !w8 || !w_scales || !h) return HM_ERR_NULL;
+  if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(h, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
+    return HM_ERR_ALIGN;
+  const size_t need = 0;
+  if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
+  const uint64_t um = m, un = n, uk = k;
+  if (overlap({{h, um * un}, {ws, need}}, {{x8, um * uk}, {x_scales, 4 * um}, {w8, un * uk}, {w_scales, 4 * un}}))
+    return HM_ERR_UNSUPPORTED;
+  TileArgs a = product(x8, x_scales, w8, w_scales, m, n, k, h);
+  a.cols = n / 2;
+  a.p_bytes = n / 2 * k;
+  return done(launch_i8_tile(a, I8_GATED, stream));
+}
+
+HM_API hm_status hm_gemm_int8_gated_grad_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+  if (hm_status s = check_gated(m, n, k)) return s;
+  if (!bytes) return HM_ERR_NULL;
+  *bytes = 0;
+  return HM_OK;
+}
+
+HM_API hm_status hm_gemm_int8_gated_grad(const uint16_t* dh, const int8_t* x8, const float* x_scales, const int8_t* w8,
+                                         const float* w_scales, int64_t m, int64_t n, int64_t k, uint16_t* dgu, void* ws,
+                                         size_t ws_bytes, hipStream_t stream) {
+  if (hm_status s = check_gated(m, n, k)) return s;
+  if (m == 0) return HM_OK;
+  if (!dh || !x8 || !x_scales || !w8 || !w_scales || !dgu) return HM_ERR_NULL;
+  if (!aligned(dh, 16) || !aligned(x8, 16) || !aligned(w8, 16) || !aligned(dgu, 16) || !aligned(x_scales, 4) ||
+      !aligned(w_scales, 4))
+    return HM_ERR_ALIGN;
+  const size_t need = 0;
+  if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
+  const uint64_t um = m, un = n, uk = k;
+  if (overlap({{dgu, 2 * um * un}, {ws, need}},
+              {{dh, um * un}, {x8, um * uk}, {x_scales, 4 * um}, {w8, un * uk}, {w_scales, 4 * un}}))
+    return HM_ERR_UNSUPPORTED;
+  TileArgs a = product(x8, x_scales, w8, w_scales, m, n, k, dgu);
+  a.cols = n / 2;
+  a.p_bytes = n / 2 * k;
+  a.dh = dh;
+  return done(launch_i8_tile(a, I8_GATED_GRAD, stream));
+}
+
+// ------------------------------------------------------------------- gradient
+
+namespace {
+
+hm_status check_grad(int64_t m, int64_t n, int64_t k) {
+  if (hm_status s = check_sizes(m, n, k)) return s;
+  return tiles_fit(m, k) && tiles_fit(n, k) ? HM_OK : HM_ERR_SHAPE;
+}
+
+}  // namespace
+
+HM_API hm_status hm_gemm_int8_grad_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
+  if (hm_status s = check_grad(m, n, k)) return s;
+  if (!bytes) return HM_ERR_NULL;
+  *bytes = plan_grad(m, n, k).total;
+  return HM_OK;
+}
+
+HM_API hm_status hm_gemm_int8_grad(const uint16_t* dy, const int8_t* x8, const float* x_scales, const int8_t* w8,
+                                   const float* w_scales, int64_t m, int64_t n, int64_t k, uint16_t* dx, uint16_t* dw,
+                                   void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (hm_status s = check_grad(m, n, k)) return s;
+  if (!dx && !dw) return HM_ERR_NULL;
+  if (m == 0 && !dw) return HM_OK;
+  if (!aligned(dx, 16) || !aligned(dw, 16)) return HM_ERR_ALIGN;
+  TileArgs a{};
+  if (m) {
+    if (!dy || (dw && (!x8 || !x_scales)) || (dx && (!w8 || !w_scales))) return HM_ERR_NULL;
+    if (!aligned(dy, 16) || !aligned(x8, 16) || !aligned(w8, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
+      return HM_ERR_ALIGN;
+  }
+  const GradPlan g = plan_grad(m, n, k);
+  if (hm_status s = check_ws(ws, ws_bytes, g.total)) return s;
+  const uint64_t um = m, un = n, uk = k;
+  if (overlap({{dx, 2 * um * uk}, {dw, 2 * un * uk}, {ws, g.total}},
+              {{dy, 2 * um * un}, {x8, um * uk}, {x_scales, 4 * um}, {w8, un * uk}, {w_scales, 4 * un}}))
+    return HM_ERR_UNSUPPORTED;
+  uint8_t* at = (uint8_t*)ws;
+  hipError_t e = hipSuccess;
+  const uint16_t* dyp = dy;
+  const int64_t ldy = g.np ? g.np : n;
+  if (g.np) {
+    dyp = (const uint16_t*)(at + g.dyp);
+    e = launch_i8_pad_rows(dy, m, n, g.np, (uint16_t*)(at + g.dyp), stream);
+  }
+  a.q = (const uint8_t*)dyp;
+  a.q_ld = 2 * ldy;
+  a.q_bytes = 2 * m * ldy;
+  a.cols = k;
+  a.p_ld = 2 * k;
+  if (dx && m) {
+    if (e == hipSuccess) e = launch_i8_dequant_rows(w8, w_scales, n, k, (uint16_t*)(at + g.w), stream);
+    a.p = at + g.w;
+    a.p_bytes = 2 * n * k;
+    a.rows = m;
+    a.kbytes = 2 * ldy;
+    a.out = dx;
+    if (e == hipSuccess) e = launch_i8_tile(a, I8_DX, stream);
+  }
+  if (dw) {
+    if (e == hipSuccess && m) e = launch_i8_dequant_rows(x8, x_scales, m, k, (uint16_t*)(at + g.x), stream);
+    a.p = at + g.x;
+    a.p_bytes = 2 * m * k;
+    a.rows = n;
+    a.kbytes = 2 * m;
+    a.out = dw;
+    if (e == hipSuccess) e = launch_i8_tile(a, I8_DW, stream);
+  }
+  return done(e);
+}

@@ -1,0 +1,46 @@
+// Linear layers in 8-bit integers (one fp32 scale per token and per output
+// channel), their gated block and gradients: internal launchers.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace hm {
+
+// What a tile kernel does with its sums (row q of the output, column p):
+enum I8Epi : int {
+  EPI_SCALE = 0,       // bf16(acc * qs[q] * ps[p]), integer sums
+  EPI_GATED = 1,       // P rows are gate / up pairs: bf16(silu(g) * u)
+  EPI_GATED_GRAD = 2,  // the same pairs and dh: bf16(dg), bf16(du)
+  EPI_ROUND = 3        // bf16(acc), fp32 sums of bf16 products
+};
+
+// One product O[q][p] = sum_c Q[q][c] P[p][c].  An operand is held either with
+// the contraction along its rows (c contiguous) or with the contraction as its
+// rows (p or q contiguous, bf16 only); which one is the kernel's template.
+struct TileArgs {
+  const uint8_t* p;       // operand of the output's columns; gated: gate rows 0..d-1, up rows d..2d-1
+  int64_t p_ld, p_bytes;  // bytes between its rows, bytes of the array (gated: of one half)
+  const uint8_t* q;       // operand of the output's rows
+  int64_t q_ld, q_bytes;
+  int64_t rows, cols;     // of the output (gated: cols = d, of h or of each of dg and du)
+  int64_t kbytes;         // contraction length in bytes of one element row (steps of 128)
+  const float* ps;        // scales (integer products)
+  const float* qs;
+  const uint16_t* dh;     // EPI_GATED_GRAD: [rows][cols]
+  uint16_t* out;          // bf16 [rows][cols] (EPI_GATED_GRAD: [rows][2 cols])
+};
+
+enum I8Kind : int { I8_FORWARD = 0, I8_GATED = 1, I8_GATED_GRAD = 2, I8_DX = 3, I8_DW = 4 };
+
+// 128 x 128 output tiles: blocks of four waves
+constexpr int kI8Tile = 128;
+hipError_t launch_i8_tile(const TileArgs& a, int kind, hipStream_t st);
+
+// bf16 rows -> int8 codes and fp32 scales
+hipError_t launch_i8_quant_rows(const uint16_t* x, int64_t m, int64_t k, int8_t* x8, float* s, hipStream_t st);
+// int8 rows -> bf16(scale * code), [rows][k], k a multiple of 16
+hipError_t launch_i8_dequant_rows(const int8_t* q, const float* s, int64_t rows, int64_t k, uint16_t* out, hipStream_t st);
+// bf16 rows of n values -> rows of np >= n (a multiple of 8), zeros behind
+hipError_t launch_i8_pad_rows(const uint16_t* x, int64_t rows, int64_t n, int64_t np, uint16_t* out, hipStream_t st);
+
+}  // namespace hm
