@@ -82,10 +82,59 @@ TileArgs product(const int8_t* x8, const float* xs, const int8_t* w8, const floa
   return a;
 }
 
+// How a product runs: which tiles, and how the last ones are cut.
+struct Plan {
+  bool big;
+  TilePlan tiles;
+  size_t part;               // workspace bytes of the cut tiles' sums
+};
+
+// Nanoseconds of up to 256 tiles at once, one a compute unit, by the contraction's steps
+// of 128 bytes (fitted to 60 sizes from m = 128, n = 2048, k = 7168 to m = 4096, n = 14336, k = 4096, most
+// within 10 %): copies from L2 bound the small tiles, copies and the matrix cores the large ones.
+constexpr int kCus = 256;
+int64_t small_round(int64_t tiles, int64_t steps) { return steps * (700 + 70 * tiles / kCus) + 2000; }
+int64_t big_round(int64_t tiles, int64_t steps) { return steps * (1070 + 380 * tiles / kCus) + 5500; }
+
+Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t kbytes) {
+  const int64_t steps = div_up(kbytes, 128);
+  Plan p{};
+  p.tiles.tiles_p = (int)div_up(cols, pairs ? kI8Tile / 2 : kI8Tile);
+  p.tiles.tiles_q = (int)div_up(rows, kI8Tile);
+  const int64_t tiles = (int64_t)p.tiles.tiles_p * p.tiles.tiles_q, rest = tiles % kCus;
+  int64_t best = rest ? small_round(rest, steps) : 0, cut = 1;
+  for (int64_t c = 2; c <= 32 && rest && rest * c <= 2 * kCus && steps >= 4 * c; ++c) {
+    // a second launch, and the sums written and read again
+    const int64_t t = div_up(rest * c, kCus) * small_round(std::min<int64_t>(rest * c, kCus), div_up(steps, c)) + 3000 +
+                      30 * rest * c;
+    if (t < best) {
+      best = t;
+      cut = c;
+    }
+  }
+  p.tiles.per = (int)std::max<int64_t>(1, div_up(steps, cut));
+  p.tiles.cut = (int)std::max<int64_t>(1, div_up(steps, p.tiles.per));
+  p.tiles.full = (int)(p.tiles.cut > 1 ? tiles - rest : tiles);
+  p.part = p.tiles.cut > 1 ? (size_t)rest * p.tiles.cut * kI8Tile * kI8Tile * 4 : 0;
+  best += tiles / kCus * small_round(kCus, steps);
+  const int64_t bigs = div_up(cols, pairs ? kI8Big / 2 : kI8Big) * div_up(rows, kI8Big);
+  p.big = bigs / kCus * big_round(kCus, steps) + (bigs % kCus ? big_round(bigs % kCus, steps) : 0) + 1500 < best;
+  if (p.big) p.part = 0;
+  return p;
+}
+
+hipError_t multiply(const TileArgs& a, const Plan& p, int kind, void* part, hipStream_t st) {
+  if (p.big) return launch_i8_big(a, kind, st);
+  TilePlan t = p.tiles;
+  t.part = part;
+  return launch_i8_tile(a, t, kind, st);
+}
+
 // Byte offsets in the workspace of the gradient.
 struct GradPlan {
-  size_t dyp, w, x, total;
+  size_t dyp, w, x, part, total;
   int64_t np;                // columns of the padded copy of dy, 0: dy itself
+  Plan dx, dw;
 };
 GradPlan plan_grad(int64_t m, int64_t n, int64_t k) {
   GradPlan g{};
@@ -95,11 +144,14 @@ GradPlan plan_grad(int64_t m, int64_t n, int64_t k) {
     at = align256(at + bytes);
     return o;
   };
-  if (m == 0) return g;
   g.np = (n % 8) ? (n + 7) / 8 * 8 : 0;
+  g.dw = plan_product(n, k, false, 2 * m);
+  if (m == 0) return g;
+  g.dx = plan_product(m, k, false, 2 * (g.np ? g.np : n));
   g.dyp = take((size_t)m * (size_t)g.np * 2);
   g.w = take((size_t)n * (size_t)k * 2);
   g.x = take((size_t)m * (size_t)k * 2);
+  g.part = take(std::max(g.dx.part, g.dw.part));
   g.total = at;
   return g;
 }
@@ -123,7 +175,7 @@ HM_API hm_status hm_quant_int8_rows(const uint16_t* x, int64_t m, int64_t k, int
 HM_API hm_status hm_gemm_int8_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_sizes(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = 0;
+  *bytes = m ? plan_product(m, n, false, k).part : 0;
   return HM_OK;
 }
 
@@ -135,12 +187,13 @@ HM_API hm_status hm_gemm_int8(const int8_t* x8, const float* x_scales, const int
   if (!x8 || !x_scales || !w8 || !w_scales || !y) return HM_ERR_NULL;
   if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(y, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const size_t need = 0;
+  const Plan p = plan_product(m, n, false, k);
+  const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
   if (overlap({{y, 2 * um * un}, {ws, need}}, {{x8, um * uk}, {x_scales, 4 * um}, {w8, un * uk}, {w_scales, 4 * un}}))
     return HM_ERR_UNSUPPORTED;
-  return done(launch_i8_tile(product(x8, x_scales, w8, w_scales, m, n, k, y), I8_FORWARD, stream));
+  return done(multiply(product(x8, x_scales, w8, w_scales, m, n, k, y), p, I8_FORWARD, ws, stream));
 }
 
 // ---------------------------------------------------------------- gated block
@@ -157,7 +210,7 @@ hm_status check_gated(int64_t m, int64_t n, int64_t k) {
 HM_API hm_status hm_gemm_int8_gated_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_gated(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = 0;
+  *bytes = m ? plan_product(m, n / 2, true, k).part : 0;
   return HM_OK;
 }
 
@@ -169,7 +222,8 @@ HM_API hm_status hm_gemm_int8_gated(const int8_t* x8, const float* x_scales, con
   if (!x8 || !x_scales || !w8 || !w_scales || !h) return HM_ERR_NULL;
   if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(h, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const size_t need = 0;
+  const Plan p = plan_product(m, n / 2, true, k);
+  const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
   if (overlap({{h, um * un}, {ws, need}}, {{x8, um * uk}, {x_scales, 4 * um}, {w8, un * uk}, {w_scales, 4 * un}}))
@@ -177,13 +231,13 @@ HM_API hm_status hm_gemm_int8_gated(const int8_t* x8, const float* x_scales, con
   TileArgs a = product(x8, x_scales, w8, w_scales, m, n, k, h);
   a.cols = n / 2;
   a.p_bytes = n / 2 * k;
-  return done(launch_i8_tile(a, I8_GATED, stream));
+  return done(multiply(a, p, I8_GATED, ws, stream));
 }
 
 HM_API hm_status hm_gemm_int8_gated_grad_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_gated(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = 0;
+  *bytes = m ? plan_product(m, n / 2, true, k).part : 0;
   return HM_OK;
 }
 
@@ -196,7 +250,8 @@ HM_API hm_status hm_gemm_int8_gated_grad(const uint16_t* dh, const int8_t* x8, c
   if (!aligned(dh, 16) || !aligned(x8, 16) || !aligned(w8, 16) || !aligned(dgu, 16) || !aligned(x_scales, 4) ||
       !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const size_t need = 0;
+  const Plan p = plan_product(m, n / 2, true, k);
+  const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
   if (overlap({{dgu, 2 * um * un}, {ws, need}},
@@ -206,7 +261,7 @@ HM_API hm_status hm_gemm_int8_gated_grad(const uint16_t* dh, const int8_t* x8, c
   a.cols = n / 2;
   a.p_bytes = n / 2 * k;
   a.dh = dh;
-  return done(launch_i8_tile(a, I8_GATED_GRAD, stream));
+  return done(multiply(a, p, I8_GATED_GRAD, ws, stream));
 }
 
 // ------------------------------------------------------------------- gradient
@@ -250,7 +305,7 @@ HM_API hm_status hm_gemm_int8_grad(const uint16_t* dy, const int8_t* x8, const f
   hipError_t e = hipSuccess;
   const uint16_t* dyp = dy;
   const int64_t ldy = g.np ? g.np : n;
-  if (g.np) {
+  if (g.np && m) {
     dyp = (const uint16_t*)(at + g.dyp);
     e = launch_i8_pad_rows(dy, m, n, g.np, (uint16_t*)(at + g.dyp), stream);
   }
@@ -266,7 +321,7 @@ HM_API hm_status hm_gemm_int8_grad(const uint16_t* dy, const int8_t* x8, const f
     a.rows = m;
     a.kbytes = 2 * ldy;
     a.out = dx;
-    if (e == hipSuccess) e = launch_i8_tile(a, I8_DX, stream);
+    if (e == hipSuccess) e = multiply(a, g.dx, I8_DX, at + g.part, stream);
   }
   if (dw) {
     if (e == hipSuccess && m) e = launch_i8_dequant_rows(x8, x_scales, m, k, (uint16_t*)(at + g.x), stream);
@@ -275,7 +330,7 @@ HM_API hm_status hm_gemm_int8_grad(const uint16_t* dy, const int8_t* x8, const f
     a.rows = n;
     a.kbytes = 2 * m;
     a.out = dw;
-    if (e == hipSuccess) e = launch_i8_tile(a, I8_DW, stream);
+    if (e == hipSuccess) e = multiply(a, g.dw, I8_DW, at + g.part, stream);
   }
   return done(e);
 }

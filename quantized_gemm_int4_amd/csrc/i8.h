@@ -32,9 +32,19 @@ struct TileArgs {
 
 enum I8Kind : int { I8_FORWARD = 0, I8_GATED = 1, I8_GATED_GRAD = 2, I8_DX = 3, I8_DW = 4 };
 
-// 128 x 128 output tiles: blocks of four waves
+// 128 x 128 output tiles.  Tiles from number `full` on are cut along the
+// contraction into `cut` parts of `per` steps of 128 bytes, whose sums go to
+// part [(tile - full) * cut][128][128], 4 bytes each.
 constexpr int kI8Tile = 128;
-hipError_t launch_i8_tile(const TileArgs& a, int kind, hipStream_t st);
+struct TilePlan {
+  int tiles_p, tiles_q;
+  int full, cut, per;
+  void* part;
+};
+hipError_t launch_i8_tile(const TileArgs& a, const TilePlan& pl, int kind, hipStream_t st);
+// 256 x 256 output tiles: blocks of four waves, one a compute unit
+constexpr int kI8Big = 256;
+hipError_t launch_i8_big(const TileArgs& a, int kind, hipStream_t st);
 
 // bf16 rows -> int8 codes and fp32 scales
 hipError_t launch_i8_quant_rows(const uint16_t* x, int64_t m, int64_t k, int8_t* x8, float* s, hipStream_t st);

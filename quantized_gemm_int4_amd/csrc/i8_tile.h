@@ -14,6 +14,8 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "common.h"
 #include "i8.h"
 
@@ -32,26 +34,33 @@ constexpr int kHalfBytes = 16384;
 template <class T> struct Mma;
 template <> struct Mma<int8_t> {
   using Acc = i32x16_t;
+  using Sum = int32_t;
   static __device__ __forceinline__ Acc run(u32x4_t a, u32x4_t b, Acc c) {
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
   }
 };
 template <> struct Mma<uint16_t> {   // bf16 patterns
   using Acc = f32x16_t;
+  using Sum = float;
   static __device__ __forceinline__ Acc run(u32x4_t a, u32x4_t b, Acc c) { return mfma32_bf16(a, b, c); }
 };
 
-// Tile of this block: the eight XCDs (block b runs on b % 8) get consecutive
-// ranges of an order that goes through four tile rows together, so that the
-// blocks of an L2 share operands.  False: no tile.
-__device__ __forceinline__ bool tile_of(int tiles_p, int tiles_q, int& tp, int& tq) {
-  const uint32_t total = (uint32_t)tiles_p * (uint32_t)tiles_q, x = blockIdx.x & 7;    // under 2^24
-  const uint32_t t = x * total / 8 + (blockIdx.x >> 3);
-  if (t >= (x + 1) * total / 8) return false;
+// Tile number t of an order that goes through four tile rows together, so that
+// blocks that run together share operands.
+__device__ __forceinline__ void tile_at(uint32_t t, int tiles_p, int tiles_q, int& tp, int& tq) {
   const uint32_t group = t / (4u * tiles_p), in = t - group * 4u * tiles_p;
   const uint32_t rows = min(4u, (uint32_t)tiles_q - 4u * group), c = in / rows;
   tq = (int)(4u * group + in - c * rows);
   tp = (int)c;
+}
+// The block's `turn`th of the first `total` tiles (under 2^24), for `blocks` blocks (a multiple
+// of 8): the eight XCDs (block b runs on b % 8) get consecutive ranges of that order,
+// and with it their own L2s.  False: none.
+__device__ __forceinline__ bool tile_of(uint32_t total, uint32_t blocks, uint32_t turn, int tiles_p, int tiles_q, int& tp, int& tq) {
+  const uint32_t x = blockIdx.x & 7;
+  const uint32_t t = x * total / 8 + (blockIdx.x >> 3) + turn * (blocks >> 3);
+  if (t >= (x + 1) * total / 8) return false;
+  tile_at(t, tiles_p, tiles_q, tp, tq);
   return true;
 }
 
@@ -73,49 +82,51 @@ template <int EPI> __device__ __forceinline__ int64_t p_row(const TileArgs& a, i
 // Copies of one operand.  ROWS: the contraction runs along the array's rows
 // (else the array's rows are contracted).  A half takes four copies a wave.
 template <bool ROWS, bool PAIRS> struct Side {
-  const uint8_t* base;       // of this tile (PAIRS: of the wave's gate or up rows), at the next step
+  const uint8_t* arr;        // PAIRS: the wave's gate or up rows
+  int64_t bytes, per_tile;   // of the array, from one tile to the next
+  const uint8_t* base;       // of the tile, at the next step
   int64_t left;              // bytes of the array from there
   uint32_t vo[2];            // lane offsets of copies i = 0, 1 of half 0
-  uint32_t ld;
-  uint32_t tail;             // all ones where the lane's chunk lies behind the contraction in the last step
-  uint32_t cut;              // the tail of the current step
+  uint32_t ld, ldv;          // bytes between rows; the same, unknown to the compiler (it would hold every copy's offset in a register)
+  uint32_t tail, cut;        // bit i: the lane's chunk of copies i, i + 2 lies behind the contraction in the last step; in this one
   rsrc_t r;
 
-  __device__ __forceinline__ void init(const uint8_t* arr, int64_t ld_, int64_t bytes, int64_t rows, int tile, int size,
-                                       int lane, int wave, int64_t kbytes) {
+  __device__ __forceinline__ void init(const uint8_t* arr_, int64_t ld_, int64_t bytes_, int size, int lane, int wave, int64_t kbytes) {
+    arr = arr_;
+    bytes = bytes_;
     ld = (uint32_t)ld_;
-    int64_t at;
     tail = 0;
     if (ROWS) {
       // wave w copies rows 16 w .. + 15 of the 64 contracted, four at a time
-      at = (int64_t)tile * size * 2;
+      per_tile = size * 2;
       vo[0] = (uint32_t)(wave * 16 + (lane >> 4)) * ld + 16 * ((lane & 15) ^ (4 * ((lane >> 4) & 3)));
       vo[1] = vo[0] + 4 * ld;
     } else {
       // wave w copies rows 32 w .. + 31 of a half, eight at a time
       const int first = PAIRS ? (wave >> 1) * 32 : wave * 32;
       if (PAIRS && (wave & 1)) arr += bytes;          // the up rows, behind the gate rows
-      at = (int64_t)tile * (PAIRS ? size / 2 : size) * ld_;
+      per_tile = (PAIRS ? size / 2 : size) * ld_;
+      const int in = (int)(kbytes & 127);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int chunk = (lane & 7) ^ ((lane >> 4) | (4 * i));
         vo[i] = (uint32_t)(first + 8 * i + (lane >> 3)) * ld + 16 * chunk;
-      }
-      // whether the chunk's bytes of the last step end behind the contraction (copies i = 0 and 1 differ in chunk)
-      const int in = (int)(kbytes & 127);
-      if (in) {
-        tail = ((16 * ((lane & 7) ^ (lane >> 4))) >= in ? 1u : 0u) | ((16 * ((lane & 7) ^ ((lane >> 4) | 4))) >= in ? 2u : 0u);
+        if (in && 16 * chunk >= in) tail |= 1u << i;
       }
     }
-    base = arr + at;
-    left = bytes - at;
     cut = 0;
-    (void)rows;
   }
-  // The array as step s sees it (steps follow each other from 0); behind the last step everything reads as zero.
-  __device__ __forceinline__ void step(int s, int steps) {
-    r = make_rsrc(base, s < steps && left > 0 ? (uint64_t)left : 0);
-    cut = s == steps - 1 ? tail : 0;
+  // Goes to step s of a tile; none (t < 0): everything reads as zero.
+  __device__ __forceinline__ void tile(int t, int s = 0) {
+    const int64_t at = t * per_tile + s * (ROWS ? 64 * (int64_t)ld : 128);
+    base = arr + (t < 0 ? 0 : at);
+    left = t < 0 ? 0 : bytes - at;
+  }
+  // The array as step s of `all` sees it (steps follow each other); from step `last` on everything reads as zero.
+  __device__ __forceinline__ void step(int s, int last, int all) {
+    r = make_rsrc(base, s < last && left > 0 ? (uint64_t)left : 0);
+    cut = s == all - 1 ? tail : 0;
+    ldv = in_sgpr(ld);
     const int64_t by = ROWS ? 64 * (int64_t)ld : 128;
     base += by;
     left -= by;
@@ -123,44 +134,59 @@ template <bool ROWS, bool PAIRS> struct Side {
   // Copy i (0..3) of half h to the half's place in LDS.
   __device__ __forceinline__ void copy(int h, int i, uint8_t* half, int wave) {
     if (ROWS) {
-      b2lds16(r, vo[i & 1] + (uint32_t)(i & 2) * 4 * ld + (uint32_t)h * 256, 0u, half + (wave * 16 + i * 4) * 256);
+      b2lds16(r, vo[i & 1] + (uint32_t)(i & 2) * 4 * ldv + (uint32_t)h * 256, 0u, half + (wave * 16 + i * 4) * 256);
     } else {
       const uint32_t over = (cut >> (i & 1)) & 1u ? 0xFFFFFFFFu : 0u;
-      b2lds16(r, (vo[i & 1] + ((uint32_t)(i & 2) * 8 + (uint32_t)h * (PAIRS ? 64 : 128)) * ld) | over, 0u,
+      b2lds16(r, (vo[i & 1] + ((uint32_t)(i & 2) * 8 + (uint32_t)h * (PAIRS ? 64 : 128)) * ldv) | over, 0u,
               half + (wave * 32 + i * 8) * 128);
     }
   }
 };
 
-// Operand reads: block b (32 rows) of the wave's 64 rows of a half (w = 0, 1), part ks of the step's four.
+// A transposing read of 16 x 4 values by 16 lanes: lane l supplies the address of row l / 4, columns 4 (l % 4) .. + 3, and gets
+// column l of the four rows.  The restrict gives the read alias information; without any the compiler waits for every
+// copy into LDS that is in flight (the gradient of m = 4096, n = 14336, k = 4096: 2303 us).
+__device__ __forceinline__ u32x2_t read_tr16(const lds_s16x4_t* __restrict__ p) {
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(const_cast<lds_s16x4_t*>(p)));
+}
+
+// Operand reads: block b (32 rows) of the wave's 64 rows of a half (w = 0, 1), part ks of the step's four, from LDS
+// addresses (32 bits; half: a constant that fits the instruction's 16-bit offset).
+typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
 template <bool ROWS> struct Frags {
-  uint32_t at[4];
-  __device__ __forceinline__ void init(int lane, int w) {
-    if (ROWS) {
+  uint32_t at[ROWS ? 2 : 4];
+  __device__ __forceinline__ void init(const uint8_t* lds, int lane, int w) {
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_void_t*)lds;
+    if constexpr (ROWS) {
       // group of 16 lanes: columns 16 (g & 1) .., contraction 8 (g >> 1) ..; lane l of it fetches row l / 4, four columns
       const int g = lane >> 4, l = lane & 15;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int chunk = (w * 8 + b * 4 + 2 * (g & 1) + ((l & 3) >> 1)) ^ (4 * (l >> 2));
-        at[b] = (uint32_t)((8 * (g >> 1) + (l >> 2)) * 256 + chunk * 16 + (l & 1) * 8);
+        at[b] = base + (uint32_t)((8 * (g >> 1) + (l >> 2)) * 256 + chunk * 16 + (l & 1) * 8);
       }
-      at[2] = at[3] = 0;
     } else {
       const int l32 = lane & 31, hi = lane >> 5;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        at[ks] = (uint32_t)((w * 64 + l32) * 128 + 16 * ((2 * ks + hi) ^ ((l32 >> 1) & 7)));
+        at[ks] = base + (uint32_t)((w * 64 + l32) * 128 + 16 * ((2 * ks + hi) ^ ((l32 >> 1) & 7)));
     }
   }
-  __device__ __forceinline__ u32x4_t read(const uint8_t* half, int b, int ks) const {
-    if (ROWS) {
-      const uint8_t* p = half + at[b] + ks * 16 * 256;
-      const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p);
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(p + 4 * 256));
-      const u32x2_t x = __builtin_bit_cast(u32x2_t, lo), y = __builtin_bit_cast(u32x2_t, hi);
+  // The same reads `by` bytes further on.
+  __device__ __forceinline__ Frags moved(uint32_t by) const {
+    Frags f;
+#pragma unroll
+    for (int i = 0; i < (ROWS ? 2 : 4); ++i) f.at[i] = at[i] + by;
+    return f;
+  }
+  __device__ __forceinline__ u32x4_t read(uint32_t half, int b, int ks) const {
+    if constexpr (ROWS) {
+      const uint32_t p = at[b] + half + ks * 16 * 256;
+      const u32x2_t x = read_tr16((const lds_s16x4_t*)p), y = read_tr16((const lds_s16x4_t*)(p + 4 * 256));
       return (u32x4_t){x[0], x[1], y[0], y[1]};
+    } else {
+      return *(const lds_u32x4_t*)(at[ks] + half + b * 32 * 128);
     }
-    return ld16(half + at[ks] + b * 32 * 128);
   }
 };
 
@@ -181,129 +207,129 @@ __device__ __forceinline__ void gated_grad(float g, float u, float dh, float& dg
   dg = dh * u * (sig * __builtin_fmaf(g, rest, 1.0f)) * last;
 }
 
-// The tile's results through LDS (which the copies no longer use) to global memory in whole rows.
-// H halves a side: wave (wp, wq) holds rows 128 h + 64 w + 32 b + ... of each side.
-template <class T, int EPI, int H> struct Epilogue {
-  using Acc = typename Mma<T>::Acc;
-  static constexpr int kSize = 128 * H;                         // rows of the tile, and columns (pairs: of gate and up)
-  static constexpr int kCols = kPairs<EPI> ? kSize / 2 : kSize;  // columns of each output
-  static constexpr int kRowBytes = 2 * kCols, kChunks = kRowBytes / 16;
-  const TileArgs& a;
-  uint8_t* lds;
-  const float *ps, *qs;                                         // the tile's scales
-  int tp, tq, lane, wave, wp, wq, tid;
-
-  // 16-byte chunk c of row r
-  __device__ __forceinline__ int place(int r, int c) const { return r * kRowBytes + 16 * (c ^ (r & (kChunks - 1))); }
-
-  // dh into LDS (EPI_GATED_GRAD)
-  __device__ __forceinline__ void before() {
-    if (EPI != EPI_GATED_GRAD) return;
-    const int64_t c0 = (int64_t)tp * kCols, r0 = (int64_t)tq * kSize;
-    for (int i = tid; i < kSize * kChunks; i += 256) {
-      const int r = i / kChunks, c = i % kChunks;
-      const int64_t row = r0 + r, col = c0 + 8 * c;
-      u32x4_t v = {0u, 0u, 0u, 0u};
-      if (row < a.rows) {
-        const uint16_t* src = a.dh + row * a.cols;
-        if ((a.cols & 7) == 0 && col + 7 < a.cols) {
-          v = ld16(src + col);
-        } else {
+// Eight bf16 values of a row at any 2-byte address (rows of an odd number of
+// columns): the global memory path takes unaligned 16-byte accesses.
+typedef uint32_t u32x4_a2_t __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ void store8(uint16_t* row, int64_t cols, int64_t col, u32x4_t v) {
+  if (col + 7 < cols) {
+    *reinterpret_cast<u32x4_a2_t*>(row + col) = v;
+  } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (col + e < a.cols) v[e >> 1] |= (uint32_t)src[col + e] << (16 * (e & 1));
-        }
-      }
-      st16(lds + place(r, c), v);
-    }
-    __syncthreads();
+    for (int e = 0; e < 8; ++e)
+      if (col + e < cols) row[col + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
   }
+}
+__device__ __forceinline__ u32x4_t load8(const uint16_t* row, int64_t cols, int64_t col) {
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (col + 7 < cols) {
+    v = *reinterpret_cast<const u32x4_a2_t*>(row + col);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (col + e < cols) v[e >> 1] |= (uint32_t)row[col + e] << (16 * (e & 1));
+  }
+  return v;
+}
 
-  // The wave's blocks of P half ph and Q half qh.
-  __device__ __forceinline__ void put(int ph, int qh, const Acc (&acc)[2][2]) {
-    const int l32 = lane & 31, hi = lane >> 5;
+// A lane of a 32 x 32 result holds columns 8 j + 4 (lane / 32) + 0..3 of one output
+// row, two bf16 pairs for each j.  Swapping the upper lanes of an even j's pairs with
+// the lower lanes of the odd j's gives each lane eight columns, 16 (j / 2) + 8 (lane /
+// 32) + 0..7, in one 16-byte register group (and the swap is its own inverse).
+__device__ __forceinline__ u32x4_t eight(u32x2_t even, u32x2_t odd) {
+  const auto lo = __builtin_amdgcn_permlane32_swap(even[0], odd[0], false, false);
+  const auto hi = __builtin_amdgcn_permlane32_swap(even[1], odd[1], false, false);
+  return (u32x4_t){lo[0], hi[0], lo[1], hi[1]};
+}
+
+// Results of a wave's 64 x 64 part of a tile (blocks [P][Q] of 32 x 32) to global
+// memory.  32 output rows at a time go through 4 KiB of LDS that the wave has
+// for itself, so that its stores are whole 128-byte lines (pairs: 64 bytes; 32
+// bytes a row straight from the registers cost 2 us a 256 x 256 tile).
+//   ps: scales of the part's 64 P rows, qs: of its 64 rows; r0, c0: first
+// output row and column; own: the wave's LDS; before: called before the first store.
+constexpr int kOwnBytes = 4096;
+template <class T, int EPI, class Before>
+__device__ __forceinline__ void emit(const TileArgs& a, const typename Mma<T>::Acc (&acc)[2][2], const float* ps,
+                                     const float* qs, int64_t r0, int64_t c0, int lane, uint8_t* own, Before&& before) {
+  constexpr int kN = kPairs<EPI> ? 1 : 2;                       // 32-column blocks of an output
+  constexpr int kOuts = EPI == EPI_GATED_GRAD ? 2 : 1;
+  constexpr int kRow = 64 * kN, kChunks = kRow / 16;            // bytes of a staged row, its 16-byte chunks
+  constexpr int kPass = 64 / kChunks;                           // rows a store instruction covers
+  const int l32 = lane & 31, hi = lane >> 5;
+  const int64_t ld = kOuts * a.cols;
+  auto swz = [](int r) { return kN == 2 ? (r & 7) : ((r >> 1) & 3); };
+  const bool whole = r0 + 64 <= a.rows && c0 + 32 * kN <= a.cols;    // the same for all lanes
+  u32x4_t dh[2][2];
+  if (EPI == EPI_GATED_GRAD) {
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
-      const int r = qh * 128 + wq * 64 + qb * 32 + l32;
-      if (kPairs<EPI>) {
-        const int c0 = (ph * 2 + wp) * 32;
-        const float sq = qs[r];
+    for (int qb = 0; qb < 2; ++qb)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = 8 * j + 4 * hi;
-          const f32x4_t sg = *reinterpret_cast<const f32x4_t*>(ps + 2 * c0 + n);
-          const f32x4_t su = *reinterpret_cast<const f32x4_t*>(ps + 2 * c0 + 32 + n);
-          float g[4], u[4];
+      for (int x = 0; x < 2; ++x) {
+        const int64_t row = r0 + qb * 32 + l32, col = c0 + 16 * x + 8 * hi;
+        if (whole) dh[qb][x] = *reinterpret_cast<const u32x4_a2_t*>(a.dh + row * a.cols + col);
+        else dh[qb][x] = row < a.rows ? load8(a.dh + row * a.cols, a.cols, col) : (u32x4_t){0u, 0u, 0u, 0u};
+      }
+  }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            g[e] = (float)acc[0][qb][4 * j + e] * sq * sg[e];
-            u[e] = (float)acc[1][qb][4 * j + e] * sq * su[e];
-          }
-          uint8_t* at = lds + place(r, (c0 + n) >> 3) + 8 * hi;
-          if (EPI == EPI_GATED) {
-            float h[4];
+  for (int qb = 0; qb < 2; ++qb) {
+    const float sq = std::is_same<T, int8_t>::value ? qs[qb * 32 + l32] : 1.0f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = silu_f(g[e]) * u[e];
-            *reinterpret_cast<u32x2_t*>(at) = (u32x2_t){pack_bf16(h[0], h[1]), pack_bf16(h[2], h[3])};
-          } else {
-            const u32x2_t d = *reinterpret_cast<const u32x2_t*>(at);
-            float dg[4], du[4];
+    for (int pb = 0; pb < kN; ++pb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              gated_grad(g[e], u[e], (e & 1) ? hi_bf16(d[e >> 1]) : lo_bf16(d[e >> 1]), dg[e], du[e]);
-            *reinterpret_cast<u32x2_t*>(at) = (u32x2_t){pack_bf16(dg[0], dg[1]), pack_bf16(dg[2], dg[3])};
-            *reinterpret_cast<u32x2_t*>(at + kSize * kRowBytes) = (u32x2_t){pack_bf16(du[0], du[1]), pack_bf16(du[2], du[3])};
-          }
+      for (int x = 0; x < 2; ++x) {
+        u32x2_t d[2] = {}, o[kOuts][2];
+        if (EPI == EPI_GATED_GRAD) {
+          const u32x4_t t = eight((u32x2_t){dh[qb][x][0], dh[qb][x][1]}, (u32x2_t){dh[qb][x][2], dh[qb][x][3]});
+          d[0] = (u32x2_t){t[0], t[1]};
+          d[1] = (u32x2_t){t[2], t[3]};
         }
-      } else {
 #pragma unroll
-        for (int pb = 0; pb < 2; ++pb) {
-          const int c0 = ph * 128 + wp * 64 + pb * 32;
+        for (int y = 0; y < 2; ++y) {
+          const int j = 2 * x + y, n = 8 * j + 4 * hi;
+          float f[kOuts][4];
+          if constexpr (kPairs<EPI>) {
+            const f32x4_t sg = *reinterpret_cast<const f32x4_t*>(ps + n);
+            const f32x4_t su = *reinterpret_cast<const f32x4_t*>(ps + 32 + n);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int n = 8 * j + 4 * hi;
-            float y[4];
-            if (EPI == EPI_SCALE) {
-              const float sq = qs[r];
-              const f32x4_t sp = *reinterpret_cast<const f32x4_t*>(ps + c0 + n);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = (float)acc[pb][qb][4 * j + e] * sq * sp[e];
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = acc[pb][qb][4 * j + e];
+            for (int e = 0; e < 4; ++e) {
+              const float g = (float)acc[0][qb][4 * j + e] * sq * sg[e], u = (float)acc[1][qb][4 * j + e] * sq * su[e];
+              if constexpr (EPI == EPI_GATED) {
+                f[0][e] = silu_f(g) * u;
+              } else {
+                gated_grad(g, u, (e & 1) ? hi_bf16(d[y][e >> 1]) : lo_bf16(d[y][e >> 1]), f[0][e], f[1][e]);
+              }
             }
-            *reinterpret_cast<u32x2_t*>(lds + place(r, (c0 + n) >> 3) + 8 * hi) =
-                (u32x2_t){pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+          } else if constexpr (EPI == EPI_SCALE) {
+            const f32x4_t sp = *reinterpret_cast<const f32x4_t*>(ps + pb * 32 + n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[0][e] = (float)acc[pb][qb][4 * j + e] * sq * sp[e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[0][e] = acc[pb][qb][4 * j + e];
           }
+#pragma unroll
+          for (int k = 0; k < kOuts; ++k)
+            o[k][y] = (u32x2_t){pack_bf16(f[k][0], f[k][1]), pack_bf16(f[k][2], f[k][3])};
         }
+#pragma unroll
+        for (int k = 0; k < kOuts; ++k)
+          st16(own + k * 32 * kRow + l32 * kRow + 16 * ((4 * pb + 2 * x + hi) ^ swz(l32)), eight(o[k][0], o[k][1]));
       }
-    }
-  }
-
-  __device__ __forceinline__ void store() {
-    __syncthreads();
-    const int64_t c0 = (int64_t)tp * kCols, r0 = (int64_t)tq * kSize;
-    constexpr int kOuts = EPI == EPI_GATED_GRAD ? 2 : 1;
-    const int64_t ld = kOuts * a.cols;
-    for (int i = tid; i < kSize * kChunks; i += 256) {
-      const int r = i / kChunks, c = i % kChunks;
-      const int64_t row = r0 + r, col = c0 + 8 * c;
-      if (row >= a.rows || col >= a.cols) continue;
+    if (qb == 0) before();
+    __asm__ volatile("" ::: "memory");       // the wave's LDS accesses are done in order
 #pragma unroll
-      for (int o = 0; o < kOuts; ++o)
-        store_row8(a.out + row * ld + o * a.cols, ld, a.cols, col, ld16(lds + place(r, c) + o * kSize * kRowBytes));
-    }
-  }
-  // Eight values of a row at col (those under cols): one store where rows and halves are 16-byte aligned.
-  static __device__ __forceinline__ void store_row8(uint16_t* y, int64_t ld, int64_t cols, int64_t col, u32x4_t v) {
-    if ((ld & 7) == 0 && (cols & 7) == 0 && col + 7 < cols) {
-      st16(y + col, v);
-    } else {
+    for (int k = 0; k < kOuts; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (col + e < cols) y[col + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-    }
+      for (int i = 0; i < 32 / kPass; ++i) {
+        const int r = i * kPass + lane / kChunks, c = lane % kChunks;
+        const u32x4_t v = ld16(own + k * 32 * kRow + r * kRow + 16 * (c ^ swz(r)));
+        const int64_t row = r0 + qb * 32 + r, col = c0 + 8 * c;
+        uint16_t* y = a.out + row * ld + k * a.cols;
+        if (whole) *reinterpret_cast<u32x4_a2_t*>(y + col) = v;
+        else if (row < a.rows) store8(y, a.cols, col, v);
+      }
+    __asm__ volatile("" ::: "memory");
   }
-};
+}
 
 }  // namespace hm
