@@ -84,7 +84,7 @@ TileArgs product(const int8_t* x8, const float* xs, const int8_t* w8, const floa
 
 // How a product runs: which tiles, and how the last ones are cut.
 struct Plan {
-  bool big;
+  bool few, big;
   TilePlan tiles;
   size_t part;               // workspace bytes of the cut tiles' sums
 };
@@ -95,8 +95,15 @@ struct Plan {
 constexpr int kCus = 256;
 int64_t small_round(int64_t tiles, int64_t steps) { return steps * (700 + 70 * tiles / kCus) + 2000; }
 int64_t big_round(int64_t tiles, int64_t steps) { return steps * (1070 + 380 * tiles / kCus) + 5500; }
+// Few rows: every block reads its weight rows and all of x, at about 40 bytes a
+// nanosecond a compute unit.
+int64_t few_rounds(int64_t rows, int64_t cols, bool pairs, int64_t k) {
+  const int64_t nb = i8_few_blocks(cols, pairs), blocks = div_up(cols, 16 * (pairs ? nb / 2 : nb));
+  return div_up(blocks, kCus) * k * 16 * (nb + div_up(rows, 16)) / 40;
+}
 
-Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t kbytes) {
+// int8: a product of codes that k_i8_few may run too.
+Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t kbytes, bool int8) {
   const int64_t steps = div_up(kbytes, 128);
   Plan p{};
   p.tiles.tiles_p = (int)div_up(cols, pairs ? kI8Tile / 2 : kI8Tile);
@@ -119,11 +126,14 @@ Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t kbytes) {
   best += tiles / kCus * small_round(kCus, steps);
   const int64_t bigs = div_up(cols, pairs ? kI8Big / 2 : kI8Big) * div_up(rows, kI8Big);
   p.big = bigs / kCus * big_round(kCus, steps) + (bigs % kCus ? big_round(bigs % kCus, steps) : 0) + 1500 < best;
-  if (p.big) p.part = 0;
+  // (measured: the tiles' launches cost 4 us more than the few-row kernel's)
+  p.few = int8 && rows <= kI8Few && few_rounds(rows, cols, pairs, kbytes) < best + 4000;
+  if (p.big || p.few) p.part = 0;
   return p;
 }
 
 hipError_t multiply(const TileArgs& a, const Plan& p, int kind, void* part, hipStream_t st) {
+  if (p.few) return launch_i8_few(a, kind, st);
   if (p.big) return launch_i8_big(a, kind, st);
   TilePlan t = p.tiles;
   t.part = part;
@@ -145,9 +155,9 @@ GradPlan plan_grad(int64_t m, int64_t n, int64_t k) {
     return o;
   };
   g.np = (n % 8) ? (n + 7) / 8 * 8 : 0;
-  g.dw = plan_product(n, k, false, 2 * m);
+  g.dw = plan_product(n, k, false, 2 * m, false);
   if (m == 0) return g;
-  g.dx = plan_product(m, k, false, 2 * (g.np ? g.np : n));
+  g.dx = plan_product(m, k, false, 2 * (g.np ? g.np : n), false);
   g.dyp = take((size_t)m * (size_t)g.np * 2);
   g.w = take((size_t)n * (size_t)k * 2);
   g.x = take((size_t)m * (size_t)k * 2);
@@ -175,7 +185,7 @@ HM_API hm_status hm_quant_int8_rows(const uint16_t* x, int64_t m, int64_t k, int
 HM_API hm_status hm_gemm_int8_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_sizes(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? plan_product(m, n, false, k).part : 0;
+  *bytes = m ? plan_product(m, n, false, k, true).part : 0;
   return HM_OK;
 }
 
@@ -187,7 +197,7 @@ HM_API hm_status hm_gemm_int8(const int8_t* x8, const float* x_scales, const int
   if (!x8 || !x_scales || !w8 || !w_scales || !y) return HM_ERR_NULL;
   if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(y, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const Plan p = plan_product(m, n, false, k);
+  const Plan p = plan_product(m, n, false, k, true);
   const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
@@ -210,7 +220,7 @@ hm_status check_gated(int64_t m, int64_t n, int64_t k) {
 HM_API hm_status hm_gemm_int8_gated_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_gated(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? plan_product(m, n / 2, true, k).part : 0;
+  *bytes = m ? plan_product(m, n / 2, true, k, true).part : 0;
   return HM_OK;
 }
 
@@ -222,7 +232,7 @@ HM_API hm_status hm_gemm_int8_gated(const int8_t* x8, const float* x_scales, con
   if (!x8 || !x_scales || !w8 || !w_scales || !h) return HM_ERR_NULL;
   if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(h, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const Plan p = plan_product(m, n / 2, true, k);
+  const Plan p = plan_product(m, n / 2, true, k, true);
   const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
@@ -237,7 +247,7 @@ HM_API hm_status hm_gemm_int8_gated(const int8_t* x8, const float* x_scales, con
 HM_API hm_status hm_gemm_int8_gated_grad_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_gated(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? plan_product(m, n / 2, true, k).part : 0;
+  *bytes = m ? plan_product(m, n / 2, true, k, false).part : 0;
   return HM_OK;
 }
 
@@ -250,7 +260,7 @@ HM_API hm_status hm_gemm_int8_gated_grad(const uint16_t* dh, const int8_t* x8, c
   if (!aligned(dh, 16) || !aligned(x8, 16) || !aligned(w8, 16) || !aligned(dgu, 16) || !aligned(x_scales, 4) ||
       !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const Plan p = plan_product(m, n / 2, true, k);
+  const Plan p = plan_product(m, n / 2, true, k, false);
   const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;

@@ -209,6 +209,7 @@ __device__ __forceinline__ void gated_grad(float g, float u, float dh, float& dg
 
 // Eight bf16 values of a row at any 2-byte address (rows of an odd number of
 // columns): the global memory path takes unaligned 16-byte accesses.
+typedef uint32_t u32x2_a2_t __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_a2_t __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ void store8(uint16_t* row, int64_t cols, int64_t col, u32x4_t v) {
   if (col + 7 < cols) {
