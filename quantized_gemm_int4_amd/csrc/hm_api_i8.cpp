@@ -159,8 +159,8 @@ GradPlan plan_grad(int64_t m, int64_t n, int64_t k) {
   if (m == 0) return g;
   g.dx = plan_product(m, k, false, 2 * (g.np ? g.np : n), false);
   g.dyp = take((size_t)m * (size_t)g.np * 2);
-  g.w = take((size_t)n * (size_t)k * 2);
-  g.x = take((size_t)m * (size_t)k * 2);
+  g.w = take(g.dx.big ? (size_t)n * (size_t)k * 2 : 0);
+  g.x = take(g.dw.big ? (size_t)m * (size_t)k * 2 : 0);
   g.part = take(std::max(g.dx.part, g.dw.part));
   g.total = at;
   return g;
@@ -323,20 +323,24 @@ HM_API hm_status hm_gemm_int8_grad(const uint16_t* dy, const int8_t* x8, const f
   a.q_ld = 2 * ldy;
   a.q_bytes = 2 * m * ldy;
   a.cols = k;
-  a.p_ld = 2 * k;
+  // P: int8 codes (128 x 128 tiles turn them into bf16 themselves), or their bf16 copy
+  auto side = [&](const Plan& p, const int8_t* q8, const float* scales, int64_t rows, size_t copy) {
+    a.p = p.big ? at + copy : (const uint8_t*)q8;
+    a.p_ld = (p.big ? 2 : 1) * k;
+    a.p_bytes = rows * a.p_ld;
+    a.ps = scales;
+    a.terms = rows;
+    if (p.big && rows && e == hipSuccess) e = launch_i8_dequant_rows(q8, scales, rows, k, (uint16_t*)(at + copy), stream);
+  };
   if (dx && m) {
-    if (e == hipSuccess) e = launch_i8_dequant_rows(w8, w_scales, n, k, (uint16_t*)(at + g.w), stream);
-    a.p = at + g.w;
-    a.p_bytes = 2 * n * k;
+    side(g.dx, w8, w_scales, n, g.w);
     a.rows = m;
     a.kbytes = 2 * ldy;
     a.out = dx;
     if (e == hipSuccess) e = multiply(a, g.dx, I8_DX, at + g.part, stream);
   }
   if (dw) {
-    if (e == hipSuccess && m) e = launch_i8_dequant_rows(x8, x_scales, m, k, (uint16_t*)(at + g.x), stream);
-    a.p = at + g.x;
-    a.p_bytes = 2 * m * k;
+    side(g.dw, x8, x_scales, m, g.x);
     a.rows = n;
     a.kbytes = 2 * m;
     a.out = dw;

@@ -24,8 +24,9 @@ struct TileArgs {
   int64_t q_ld, q_bytes;
   int64_t rows, cols;     // of the output (gated: cols = d, of h or of each of dg and du)
   int64_t kbytes;         // contraction length in bytes of one element row (steps of 128)
-  const float* ps;        // scales (integer products)
+  const float* ps;        // scales (integer products; tiles of 128 of a gradient: of the `terms` rows of P)
   const float* qs;
+  int64_t terms;
   const uint16_t* dh;     // EPI_GATED_GRAD: [rows][cols]
   uint16_t* out;          // bf16 [rows][cols] (EPI_GATED_GRAD: [rows][2 cols])
 };

@@ -8,7 +8,9 @@
 //     meet every bank once;
 //   contraction as rows (bf16, 64 rows c of 128 values): row c at 256 c, chunk x
 //     at place x ^ 4 (c & 3): a transposing read takes 64 bytes of four
-//     neighbouring rows, which so lie in different banks.
+//     neighbouring rows, which so lie in different banks;
+//   the same of int8 codes (64 rows of 128 bytes, 8 KiB): row c at 128 c, chunk x at
+//     place x ^ 2 ((c >> 1) & 3): 32 bytes of eight neighbouring rows.
 // The copies write LDS in lane order; the places come from which chunk a lane
 // fetches, and every copy moves whole lines.
 #pragma once
@@ -150,6 +152,13 @@ __device__ __forceinline__ u32x2_t read_tr16(const lds_s16x4_t* __restrict__ p) 
   return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(const_cast<lds_s16x4_t*>(p)));
 }
 
+// The same of 16 x 8 bytes: lane l supplies the address of row l / 2, bytes 8 (l % 2) .. + 7, and gets byte l of the eight rows.
+typedef int i32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i32x2_t lds_i32x2_t;
+__device__ __forceinline__ u32x2_t read_tr8(const lds_i32x2_t* __restrict__ p) {
+  return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32(const_cast<lds_i32x2_t*>(p)));
+}
+
 // Operand reads: block b (32 rows) of the wave's 64 rows of a half (w = 0, 1), part ks of the step's four, from LDS
 // addresses (32 bits; half: a constant that fits the instruction's 16-bit offset).
 typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
@@ -187,6 +196,64 @@ template <bool ROWS> struct Frags {
     } else {
       return *(const lds_u32x4_t*)(at[ks] + half + b * 32 * 128);
     }
+  }
+};
+
+// An operand of int8 codes with the contraction as rows and a scale for each of
+// those, turned into bf16(scale * code) on the way to the MFMA: copies (two of codes
+// and one of the step's 64 scales, which every wave has for itself), reads, and the conversion.
+struct Codes {
+  static constexpr int kBytes = 8192;
+  const uint8_t* base;
+  int64_t left, ld;
+  rsrc_t r, rs;
+  uint32_t vo, sv;
+  uint32_t at[2], sat;
+
+  // scales: `rows` of them.  lds, slots: addresses of the codes and of the wave's 256-byte scale slot in stage 0.
+  __device__ __forceinline__ void init(const uint8_t* arr, int64_t ld_, int64_t bytes, const float* scales, int64_t rows, int tile,
+                                       int first, int lane, int wave, const uint8_t* lds, const uint8_t* slot) {
+    ld = ld_;
+    const int64_t from = (int64_t)tile * 128 + (int64_t)first * 64 * ld;
+    base = arr + from;
+    left = bytes - from;
+    // wave w copies rows 16 w .. + 15, eight at a time
+    vo = (uint32_t)(wave * 16 + (lane >> 3)) * (uint32_t)ld + 16 * ((lane & 7) ^ (2 * ((lane >> 4) & 3)));
+    rs = make_rsrc(scales, (uint64_t)rows * 4);
+    sv = (uint32_t)first * 256 + lane * 4;
+    const int g = lane >> 4, l = lane & 15;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      at[b] = (uint32_t)(uintptr_t)(lds_void_t*)lds + (8 * (g >> 1) + (l >> 1)) * 128 +
+              32 * (((wave & 1) * 2 + b) ^ ((l >> 2) & 3)) + 16 * (g & 1) + 8 * (l & 1);
+    sat = (uint32_t)(uintptr_t)(lds_void_t*)slot + 32 * (g >> 1);
+  }
+  __device__ __forceinline__ void step(int s, int last) {
+    r = make_rsrc(base, s < last && left > 0 ? (uint64_t)left : 0);
+    base += 64 * ld;
+    left -= 64 * ld;
+  }
+  // i = 0, 1: codes, 2: scales
+  __device__ __forceinline__ void copy(int i, uint8_t* stage, uint8_t* slot, int wave) {
+    if (i < 2) {
+      b2lds16(r, vo + (uint32_t)i * 8 * (uint32_t)ld, 0u, stage + (wave * 16 + i * 8) * 128);
+    } else {
+      b2lds4(rs, sv, 0u, slot);
+      sv += 256;
+    }
+  }
+  __device__ __forceinline__ u32x2_t read(uint32_t by, int b, int ks) const {
+    return read_tr8((const lds_i32x2_t*)(at[b] + by + ks * 16 * 128));
+  }
+  // scales of part ks: contraction 16 ks + 8 (lane / 32) + 4 h .. + 3
+  __device__ __forceinline__ f32x4_t scales(uint32_t by, int ks, int h) const {
+    typedef __attribute__((address_space(3))) f32x4_t lds_f32x4_t;
+    return *(const lds_f32x4_t*)(sat + by + ks * 64 + h * 16);
+  }
+  static __device__ __forceinline__ u32x4_t values(u32x2_t q, f32x4_t lo, f32x4_t hi) {
+    auto sb = [](uint32_t x, int b) { return (float)(int8_t)(x >> (8 * b)); };
+    return (u32x4_t){pack_bf16(sb(q[0], 0) * lo[0], sb(q[0], 1) * lo[1]), pack_bf16(sb(q[0], 2) * lo[2], sb(q[0], 3) * lo[3]),
+                     pack_bf16(sb(q[1], 0) * hi[0], sb(q[1], 1) * hi[1]), pack_bf16(sb(q[1], 2) * hi[2], sb(q[1], 3) * hi[3])};
   }
 };
 

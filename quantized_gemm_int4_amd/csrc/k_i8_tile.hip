@@ -7,7 +7,10 @@
 // rows are the output's columns p, so that a lane holds four neighbouring
 // columns of one output row.  Operands come through LDS in steps of 128 bytes
 // of the contraction by 16-byte direct buffer-to-LDS copies; reads past an
-// array give zeros, so no size has to be padded.  During step s its operands are
+// array give zeros, so no size has to be padded.  Gradients read their int8
+// operand (weights for dx, rows of x for dw) as it is and turn it into bf16 between
+// the MFMAs: the copies are what bounds these tiles (MFMAs take 0.21 us of a step's 0.77), and the 256 x 256
+// tiles' bf16 copy of the operand would cost more than the conversion.  During step s its operands are
 // in registers, those of step s + 1 are read from LDS between the MFMAs, and four
 // stages hold steps s + 1 .. s + 4, so that a copy has three steps to land.
 //
@@ -28,10 +31,13 @@ namespace hm {
 namespace {
 
 constexpr int kStages = 4;
-constexpr int kStage = 2 * kHalfBytes;             // P and Q of one step
-constexpr int kTileLds = kStages * kStage + 1024;  // and 128 + 128 scales
+// P8: P is int8 codes whose rows are contracted (gradients); then a stage also has a slot of 64 scales for each wave
+template <bool P8> constexpr int kP = P8 ? Codes::kBytes : kHalfBytes;
+template <bool P8> constexpr int kStage = kP<P8> + kHalfBytes;             // P and Q of one step
+template <bool P8> constexpr int kScales = kStages * kStage<P8>;           // the slots, or the scales of 128 + 128 results
+template <bool P8> constexpr int kTileLds = kScales<P8> + (P8 ? kStages * 1024 : 1024);
 
-template <class T, bool PS, bool QS, int EPI>
+template <class T, bool P8, bool QS, int EPI>
 __global__ void __launch_bounds__(256, 1)
 k_i8_tile(TileArgs a, TilePlan pl) {
   using Acc = typename Mma<T>::Acc;
@@ -50,21 +56,26 @@ k_i8_tile(TileArgs a, TilePlan pl) {
     last = min(all, first + pl.per);
   }
   const int steps = last - first;
-  float* sc = reinterpret_cast<float*>(lds + kStages * kStage);
+  float* sc = reinterpret_cast<float*>(lds + kScales<P8>);
   if (std::is_same<T, int8_t>::value) {
     if (tid < kI8Tile) sc[tid] = a.ps[p_row<EPI>(a, tp, kI8Tile, tid)];
     else sc[tid] = a.qs[min((int64_t)tq * kI8Tile + tid - kI8Tile, a.rows - 1)];
   }
-  Side<PS, kPairs<EPI>> P;
   Side<QS, false> Q;
-  P.init(a.p, a.p_ld, a.p_bytes, kI8Tile, lane, wave, a.kbytes);
   Q.init(a.q, a.q_ld, a.q_bytes, kI8Tile, lane, wave, a.kbytes);
-  P.tile(tp, first);
   Q.tile(tq, first);
-  Frags<PS> fp;
   Frags<QS> fq;
-  fp.init(lds, lane, wp);
-  fq.init(lds, lane, wq);
+  fq.init(lds + kP<P8>, lane, wq);
+  std::conditional_t<P8, Codes, Side<false, kPairs<EPI>>> P;
+  Frags<false> fp;
+  uint8_t* const slot = lds + kScales<P8> + wave * 256;
+  if constexpr (P8) {
+    P.init(a.p, a.p_ld, a.p_bytes, a.ps, a.terms, tp, first, lane, wave, lds, slot);
+  } else {
+    P.init(a.p, a.p_ld, a.p_bytes, kI8Tile, lane, wave, a.kbytes);
+    P.tile(tp, first);
+    fp.init(lds, lane, wp);
+  }
 
   Acc acc[2][2];
 #pragma unroll
@@ -74,52 +85,76 @@ k_i8_tile(TileArgs a, TilePlan pl) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
-  // steps 0..3; a step past the last copies zeros, so that the waits can count on eight copies a step
+  // Copies of a step, i = 0..7 (codes: seven), into stage `at`; a step past the last copies zeros, so that the
+  // waits can count on as many a step.
+  auto begin = [&](int s) __attribute__((always_inline)) {
+    if constexpr (P8) P.step(first + s, last);
+    else P.step(first + s, last, all);
+    Q.step(first + s, last, all);
+  };
+  auto copy = [&](int i, int at) __attribute__((always_inline)) {
+    uint8_t* st = lds + at * kStage<P8>;
+    if (i & 1) Q.copy(0, i >> 1, st + kP<P8>, wave);
+    else if constexpr (!P8) P.copy(0, i >> 1, st, wave);
+    else if (i < 6) P.copy(i >> 1, st, slot + at * 1024, wave);
+  };
+  constexpr int kCopies = P8 ? 7 : 8;
 #pragma unroll
   for (int s = 0; s < kStages; ++s) {
-    P.step(first + s, last, all);
-    Q.step(first + s, last, all);
+    begin(s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      P.copy(0, i, lds + s * kStage, wave);
-      Q.copy(0, i, lds + s * kStage + kHalfBytes, wave);
+    for (int i = 0; i < 8; ++i) copy(i, s);
+  }
+  // Operands of a step in registers (codes as they are, with their scales).
+  struct Ops {
+    std::conditional_t<P8, u32x2_t, u32x4_t> p[2][4];
+    u32x4_t q[2][4];
+    f32x4_t s[4][2];
+  };
+  // part i = 0..7 of a step's operands, from the stage `by` bytes on
+  auto read = [&](Ops& o, int i, int stage) __attribute__((always_inline)) {
+    const int b = i & 1, ks = i >> 1;
+    if constexpr (P8) {
+      o.p[b][ks] = P.read(stage * kStage<P8>, b, ks);
+      o.s[ks][b] = P.scales(stage * 1024, ks, b);
+    } else {
+      o.p[b][ks] = fp.moved(stage * kStage<P8>).read(0, b, ks);
     }
-  }
-  u32x4_t pa[2][4], pb[2][4], qa[2][4], qb[2][4];
-  __asm__ volatile("s_waitcnt vmcnt(24) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    o.q[b][ks] = fq.moved(stage * kStage<P8>).read(0, b, ks);
+  };
+  Ops a0, a1;
+  __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(3 * kCopies) : "memory");
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    pa[i >> 2][i & 3] = fp.read(0, i >> 2, i & 3);
-    qa[i >> 2][i & 3] = fq.read(kHalfBytes, i >> 2, i & 3);
-  }
-  // one step on operands vp, vq, while those of the next are read into np, nq and step s + 4 is copied
+  for (int i = 0; i < 8; ++i) read(a0, i, 0);
+  // one step on operands o, while those of the next are read and step s + 4 is copied
   int at = 0;                                      // stage of step s
-  auto step = [&](int s, const u32x4_t (&vp)[2][4], const u32x4_t (&vq)[2][4], u32x4_t (&np)[2][4], u32x4_t (&nq)[2][4])
-                  __attribute__((always_inline)) {
-    const int next = (at + 1) & (kStages - 1);
-    uint8_t* st = lds + at * kStage;
-    const Frags<PS> hp = fp.moved(next * kStage);
-    const Frags<QS> hq = fq.moved(next * kStage);
-    P.step(first + s + kStages, last, all);
-    Q.step(first + s + kStages, last, all);
-    // step s + 1 has landed (16 copies are newer), and all waves hold step s in registers
-    __asm__ volatile("s_waitcnt vmcnt(16) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  auto step = [&](int s, const Ops& o, Ops& next) __attribute__((always_inline)) {
+    const int after = (at + 1) & (kStages - 1);
+    begin(s + kStages);
+    // step s + 1 has landed (two steps' copies are newer), and all waves hold step s in registers
+    __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * kCopies) : "memory");
+    u32x4_t vp[2][2];                              // P operands of parts ks and ks + 1
+    auto values = [&](int b, int ks) __attribute__((always_inline)) {
+      if constexpr (P8) vp[ks & 1][b] = Codes::values(o.p[b][ks], o.s[ks][0], o.s[ks][1]);
+      else vp[ks & 1][b] = o.p[b][ks];
+    };
+    values(0, 0);
+    values(1, 0);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int ks = i >> 2, x = (i >> 1) & 1, y = i & 1;
-      acc[x][y] = Mma<T>::run(vp[x][ks], vq[y][ks], acc[x][y]);
-      if ((i & 1) == 0) np[(i >> 1) & 1][i >> 2] = hp.read(0, (i >> 1) & 1, i >> 2);
-      else nq[(i >> 1) & 1][i >> 2] = hq.read(kHalfBytes, (i >> 1) & 1, i >> 2);
-      if ((i & 3) == 1) P.copy(0, i >> 2, st, wave);
-      if ((i & 3) == 3) Q.copy(0, i >> 2, st + kHalfBytes, wave);
+      acc[x][y] = Mma<T>::run(vp[ks & 1][x], o.q[y][ks], acc[x][y]);
+      if (i & 1) read(next, i >> 1, after);
+      else copy(i >> 1, at);
+      if ((i & 1) && ks < 3) values((i >> 1) & 1, ks + 1);
       __builtin_amdgcn_sched_barrier(0);
     }
-    at = next;
+    at = after;
   };
   int s = 0;
   do {                                             // two steps a round; the second may be all zeros
-    step(s, pa, qa, pb, qb);
-    step(s + 1, pb, qb, pa, qa);
+    step(s, a0, a1);
+    step(s + 1, a1, a0);
     s += 2;
   } while (s < steps);
   // the stages have been read by all waves, and no copy is in flight
@@ -203,15 +238,15 @@ k_i8_finish(TileArgs a, TilePlan pl) {
   }
 }
 
-template <class T, bool PS, bool QS, int EPI>
+template <class T, bool P8, bool QS, int EPI>
 hipError_t go(const TileArgs& a, const TilePlan& pl, hipStream_t st) {
-  auto kern = &k_i8_tile<T, PS, QS, EPI>;
+  auto kern = &k_i8_tile<T, P8, QS, EPI>;
   static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, kTileLds);
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, kTileLds<P8>);
   if (attr != hipSuccess) return attr;
   const int64_t split = (int64_t)pl.tiles_p * pl.tiles_q - pl.full;
   const int64_t blocks = 8 * (((int64_t)pl.full + 7) / 8) + split * pl.cut;
-  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), kTileLds, st, a, pl);
+  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(256), kTileLds<P8>, st, a, pl);
   if (split) {
     const int per = kPairs<EPI> ? 4 : 8;           // blocks of a tile: 32 rows, 16 rows
     hipLaunchKernelGGL((&k_i8_finish<T, EPI>), dim3((unsigned)(split * per)), dim3(256), 0, st, a, pl);
