@@ -87,13 +87,18 @@ struct Plan {
   bool few, big;
   TilePlan tiles;
   size_t part;               // workspace bytes of the cut tiles' sums
+  int64_t ns;                // estimate of the time
 };
 
 // Nanoseconds of up to 256 tiles at once, one a compute unit, by the contraction's steps
-// of 128 bytes (fitted to 60 sizes from m = 128, n = 2048, k = 7168 to m = 4096, n = 14336, k = 4096, most
-// within 10 %): copies from L2 bound the small tiles, copies and the matrix cores the large ones.
+// of 128 bytes (fitted to some 100 sizes from m = 16, n = 2048, k = 7168 to m = 4096, n = 14336, k = 4096, most
+// within 15 %): copies from L2 bound the small tiles, the conversion those that
+// turn codes into bf16, copies and the matrix cores the large ones.
 constexpr int kCus = 256;
-int64_t small_round(int64_t tiles, int64_t steps) { return steps * (700 + 70 * tiles / kCus) + 2000; }
+enum Operands { INT8, CODES, COPY };               // int8 products; gradients with P as codes, as a bf16 copy
+int64_t small_round(Operands o, int64_t tiles, int64_t steps) {
+  return steps * ((o == CODES ? 590 : 440) + 70 * tiles / kCus) + 2000 + 1700 * tiles / kCus;
+}
 int64_t big_round(int64_t tiles, int64_t steps) { return steps * (1070 + 380 * tiles / kCus) + 5500; }
 // Few rows: every block reads its weight rows and all of x, at about 40 bytes a
 // nanosecond a compute unit.
@@ -102,17 +107,18 @@ int64_t few_rounds(int64_t rows, int64_t cols, bool pairs, int64_t k) {
   return div_up(blocks, kCus) * k * 16 * (nb + div_up(rows, 16)) / 40;
 }
 
-// int8: a product of codes that k_i8_few may run too.
-Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t kbytes, bool int8) {
+// kbytes: of the contraction, as the operands' rows hold it.
+Plan plan_tiles(int64_t rows, int64_t cols, bool pairs, int64_t kbytes, Operands o) {
   const int64_t steps = div_up(kbytes, 128);
   Plan p{};
   p.tiles.tiles_p = (int)div_up(cols, pairs ? kI8Tile / 2 : kI8Tile);
   p.tiles.tiles_q = (int)div_up(rows, kI8Tile);
+  p.tiles.codes = o == CODES;
   const int64_t tiles = (int64_t)p.tiles.tiles_p * p.tiles.tiles_q, rest = tiles % kCus;
-  int64_t best = rest ? small_round(rest, steps) : 0, cut = 1;
+  int64_t best = rest ? small_round(o, rest, steps) : 0, cut = 1;
   for (int64_t c = 2; c <= 32 && rest && rest * c <= 2 * kCus && steps >= 4 * c; ++c) {
     // a second launch, and the sums written and read again
-    const int64_t t = div_up(rest * c, kCus) * small_round(std::min<int64_t>(rest * c, kCus), div_up(steps, c)) + 3000 +
+    const int64_t t = div_up(rest * c, kCus) * small_round(o, std::min<int64_t>(rest * c, kCus), div_up(steps, c)) + 3000 +
                       30 * rest * c;
     if (t < best) {
       best = t;
@@ -123,13 +129,33 @@ Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t kbytes, bool i
   p.tiles.cut = (int)std::max<int64_t>(1, div_up(steps, p.tiles.per));
   p.tiles.full = (int)(p.tiles.cut > 1 ? tiles - rest : tiles);
   p.part = p.tiles.cut > 1 ? (size_t)rest * p.tiles.cut * kI8Tile * kI8Tile * 4 : 0;
-  best += tiles / kCus * small_round(kCus, steps);
+  p.ns = best + tiles / kCus * small_round(o, kCus, steps);
+  if (o == CODES) return p;                        // the large tiles take no codes
   const int64_t bigs = div_up(cols, pairs ? kI8Big / 2 : kI8Big) * div_up(rows, kI8Big);
-  p.big = bigs / kCus * big_round(kCus, steps) + (bigs % kCus ? big_round(bigs % kCus, steps) : 0) + 1500 < best;
-  // (measured: the tiles' launches cost 4 us more than the few-row kernel's)
-  p.few = int8 && rows <= kI8Few && few_rounds(rows, cols, pairs, kbytes) < best + 4000;
-  if (p.big || p.few) p.part = 0;
+  const int64_t t = bigs / kCus * big_round(kCus, steps) + (bigs % kCus ? big_round(bigs % kCus, steps) : 0) + 1500;
+  if (t < p.ns) {
+    p.big = true;
+    p.ns = t;
+    p.part = 0;
+  }
   return p;
+}
+
+// An int8 product; grad: that of the gated gradient, which has no few-row kernel.
+Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t k, bool grad) {
+  Plan p = plan_tiles(rows, cols, pairs, k, INT8);
+  // (measured: the tiles' launches cost 4 us more than the few-row kernel's)
+  p.few = !grad && rows <= kI8Few && few_rounds(rows, cols, pairs, k) < p.ns + 4000;
+  if (p.few) p.part = 0;
+  return p;
+}
+
+// One of the gradients: `terms` rows of the int8 operand, [terms][cols].
+Plan plan_gradient(int64_t rows, int64_t cols, int64_t kbytes, int64_t terms) {
+  const Plan codes = plan_tiles(rows, cols, false, kbytes, CODES);
+  Plan copy = plan_tiles(rows, cols, false, kbytes, COPY);
+  copy.ns += 3000 + terms * cols * 3 / 5000;       // making the copy, 5 TB/s
+  return codes.ns < copy.ns ? codes : copy;
 }
 
 hipError_t multiply(const TileArgs& a, const Plan& p, int kind, void* part, hipStream_t st) {
@@ -155,12 +181,12 @@ GradPlan plan_grad(int64_t m, int64_t n, int64_t k) {
     return o;
   };
   g.np = (n % 8) ? (n + 7) / 8 * 8 : 0;
-  g.dw = plan_product(n, k, false, 2 * m, false);
+  g.dw = plan_gradient(n, k, 2 * m, m);
   if (m == 0) return g;
-  g.dx = plan_product(m, k, false, 2 * (g.np ? g.np : n), false);
+  g.dx = plan_gradient(m, k, 2 * (g.np ? g.np : n), n);
   g.dyp = take((size_t)m * (size_t)g.np * 2);
-  g.w = take(g.dx.big ? (size_t)n * (size_t)k * 2 : 0);
-  g.x = take(g.dw.big ? (size_t)m * (size_t)k * 2 : 0);
+  g.w = take(!g.dx.tiles.codes ? (size_t)n * (size_t)k * 2 : 0);
+  g.x = take(!g.dw.tiles.codes ? (size_t)m * (size_t)k * 2 : 0);
   g.part = take(std::max(g.dx.part, g.dw.part));
   g.total = at;
   return g;
@@ -185,7 +211,7 @@ HM_API hm_status hm_quant_int8_rows(const uint16_t* x, int64_t m, int64_t k, int
 HM_API hm_status hm_gemm_int8_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_sizes(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? plan_product(m, n, false, k, true).part : 0;
+  *bytes = m ? plan_product(m, n, false, k, false).part : 0;
   return HM_OK;
 }
 
@@ -197,7 +223,7 @@ HM_API hm_status hm_gemm_int8(const int8_t* x8, const float* x_scales, const int
   if (!x8 || !x_scales || !w8 || !w_scales || !y) return HM_ERR_NULL;
   if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(y, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const Plan p = plan_product(m, n, false, k, true);
+  const Plan p = plan_product(m, n, false, k, false);
   const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
@@ -220,7 +246,7 @@ hm_status check_gated(int64_t m, int64_t n, int64_t k) {
 HM_API hm_status hm_gemm_int8_gated_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_gated(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? plan_product(m, n / 2, true, k, true).part : 0;
+  *bytes = m ? plan_product(m, n / 2, true, k, false).part : 0;
   return HM_OK;
 }
 
@@ -232,7 +258,7 @@ HM_API hm_status hm_gemm_int8_gated(const int8_t* x8, const float* x_scales, con
   if (!x8 || !x_scales || !w8 || !w_scales || !h) return HM_ERR_NULL;
   if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(h, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const Plan p = plan_product(m, n / 2, true, k, true);
+  const Plan p = plan_product(m, n / 2, true, k, false);
   const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
@@ -247,7 +273,7 @@ HM_API hm_status hm_gemm_int8_gated(const int8_t* x8, const float* x_scales, con
 HM_API hm_status hm_gemm_int8_gated_grad_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_gated(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? plan_product(m, n / 2, true, k, false).part : 0;
+  *bytes = m ? plan_product(m, n / 2, true, k, true).part : 0;
   return HM_OK;
 }
 
@@ -260,7 +286,7 @@ HM_API hm_status hm_gemm_int8_gated_grad(const uint16_t* dh, const int8_t* x8, c
   if (!aligned(dh, 16) || !aligned(x8, 16) || !aligned(w8, 16) || !aligned(dgu, 16) || !aligned(x_scales, 4) ||
       !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const Plan p = plan_product(m, n / 2, true, k, false);
+  const Plan p = plan_product(m, n / 2, true, k, true);
   const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
@@ -323,14 +349,15 @@ HM_API hm_status hm_gemm_int8_grad(const uint16_t* dy, const int8_t* x8, const f
   a.q_ld = 2 * ldy;
   a.q_bytes = 2 * m * ldy;
   a.cols = k;
-  // P: int8 codes (128 x 128 tiles turn them into bf16 themselves), or their bf16 copy
+  // P: the int8 operand, as codes or as a bf16 copy
   auto side = [&](const Plan& p, const int8_t* q8, const float* scales, int64_t rows, size_t copy) {
-    a.p = p.big ? at + copy : (const uint8_t*)q8;
-    a.p_ld = (p.big ? 2 : 1) * k;
+    const bool codes = p.tiles.codes;
+    a.p = codes ? (const uint8_t*)q8 : at + copy;
+    a.p_ld = (codes ? 1 : 2) * k;
     a.p_bytes = rows * a.p_ld;
     a.ps = scales;
     a.terms = rows;
-    if (p.big && rows && e == hipSuccess) e = launch_i8_dequant_rows(q8, scales, rows, k, (uint16_t*)(at + copy), stream);
+    if (!codes && rows && e == hipSuccess) e = launch_i8_dequant_rows(q8, scales, rows, k, (uint16_t*)(at + copy), stream);
   };
   if (dx && m) {
     side(g.dx, w8, w_scales, n, g.w);

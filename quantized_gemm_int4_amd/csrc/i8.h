@@ -40,6 +40,7 @@ constexpr int kI8Tile = 128;
 struct TilePlan {
   int tiles_p, tiles_q;
   int full, cut, per;
+  int codes;                 // gradients: P is int8 codes with scales ps, not their bf16 copy
   void* part;
 };
 hipError_t launch_i8_tile(const TileArgs& a, const TilePlan& pl, int kind, hipStream_t st);

@@ -159,18 +159,51 @@ __device__ __forceinline__ u32x2_t read_tr8(const lds_i32x2_t* __restrict__ p) {
   return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32(const_cast<lds_i32x2_t*>(p)));
 }
 
-// Operand reads: block b (32 rows) of the wave's 64 rows of a half (w = 0, 1), part ks of the step's four, from LDS
+// Touches 128-byte lines of later steps, so that the copies find them in their
+// XCD's L2 (a line from further away takes longer than a copy has).  The `sharers`
+// blocks that run on the same rows divide a step's lines: this one has lines share,
+// share + sharers, ...  A touch is a 4-byte copy a line to a place in LDS that nothing reads.
+struct Ahead {
+  const uint8_t* base;       // of the tile, at the next step
+  int64_t left, by;          // bytes of the array from there, from one step to the next
+  uint32_t vo[2];
+  bool two;                  // more than 64 lines
+
+  // from: bytes to the tile's first line; per_row lines in each of the rows, `ld` bytes apart
+  __device__ __forceinline__ void init(const uint8_t* arr, int64_t bytes, int64_t from, int64_t by_, int64_t ld, int lines,
+                                       int per_row, int share, int sharers, int lane) {
+    base = arr + from;
+    left = bytes - from;
+    by = by_;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = (lane + 64 * i) * sharers + share;
+      vo[i] = j < lines ? (uint32_t)(j / per_row) * (uint32_t)ld + 128 * (j % per_row) : 0xFFFFFFFFu;
+    }
+    two = 64 * sharers < lines;
+  }
+  __device__ __forceinline__ void touch(uint8_t* place) {
+    const rsrc_t r = make_rsrc(base, left > 0 ? (uint64_t)left : 0);
+    b2lds4(r, vo[0], 0u, place);
+    if (two) b2lds4(r, vo[1], 0u, place);
+    base += by;
+    left -= by;
+  }
+};
+
+// Operand reads: block b (32 rows) of the wave's 32 NB rows of a half, part ks of the step's four, from LDS
 // addresses (32 bits; half: a constant that fits the instruction's 16-bit offset).
 typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
-template <bool ROWS> struct Frags {
-  uint32_t at[ROWS ? 2 : 4];
+template <bool ROWS, int NB = 2> struct Frags {
+  uint32_t at[ROWS ? NB : 4];
+  // w: which 64 rows (NB = 4: 0, all 128)
   __device__ __forceinline__ void init(const uint8_t* lds, int lane, int w) {
     const uint32_t base = (uint32_t)(uintptr_t)(lds_void_t*)lds;
     if constexpr (ROWS) {
       // group of 16 lanes: columns 16 (g & 1) .., contraction 8 (g >> 1) ..; lane l of it fetches row l / 4, four columns
       const int g = lane >> 4, l = lane & 15;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < NB; ++b) {
         const int chunk = (w * 8 + b * 4 + 2 * (g & 1) + ((l & 3) >> 1)) ^ (4 * (l >> 2));
         at[b] = base + (uint32_t)((8 * (g >> 1) + (l >> 2)) * 256 + chunk * 16 + (l & 1) * 8);
       }
@@ -185,7 +218,7 @@ template <bool ROWS> struct Frags {
   __device__ __forceinline__ Frags moved(uint32_t by) const {
     Frags f;
 #pragma unroll
-    for (int i = 0; i < (ROWS ? 2 : 4); ++i) f.at[i] = at[i] + by;
+    for (int i = 0; i < (ROWS ? NB : 4); ++i) f.at[i] = at[i] + by;
     return f;
   }
   __device__ __forceinline__ u32x4_t read(uint32_t half, int b, int ks) const {
@@ -208,7 +241,7 @@ struct Codes {
   int64_t left, ld;
   rsrc_t r, rs;
   uint32_t vo, sv;
-  uint32_t at[2], sat;
+  uint32_t at, sat;          // the wave's 32 columns, its scales
 
   // scales: `rows` of them.  lds, slots: addresses of the codes and of the wave's 256-byte scale slot in stage 0.
   __device__ __forceinline__ void init(const uint8_t* arr, int64_t ld_, int64_t bytes, const float* scales, int64_t rows, int tile,
@@ -222,10 +255,8 @@ struct Codes {
     rs = make_rsrc(scales, (uint64_t)rows * 4);
     sv = (uint32_t)first * 256 + lane * 4;
     const int g = lane >> 4, l = lane & 15;
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-      at[b] = (uint32_t)(uintptr_t)(lds_void_t*)lds + (8 * (g >> 1) + (l >> 1)) * 128 +
-              32 * (((wave & 1) * 2 + b) ^ ((l >> 2) & 3)) + 16 * (g & 1) + 8 * (l & 1);
+    at = (uint32_t)(uintptr_t)(lds_void_t*)lds + (8 * (g >> 1) + (l >> 1)) * 128 + 32 * (wave ^ ((l >> 2) & 3)) +
+         16 * (g & 1) + 8 * (l & 1);
     sat = (uint32_t)(uintptr_t)(lds_void_t*)slot + 32 * (g >> 1);
   }
   __device__ __forceinline__ void step(int s, int last) {
@@ -242,18 +273,18 @@ struct Codes {
       sv += 256;
     }
   }
-  __device__ __forceinline__ u32x2_t read(uint32_t by, int b, int ks) const {
-    return read_tr8((const lds_i32x2_t*)(at[b] + by + ks * 16 * 128));
+  __device__ __forceinline__ u32x2_t read(uint32_t by, int ks) const {
+    return read_tr8((const lds_i32x2_t*)(at + by + ks * 16 * 128));
   }
   // scales of part ks: contraction 16 ks + 8 (lane / 32) + 4 h .. + 3
   __device__ __forceinline__ f32x4_t scales(uint32_t by, int ks, int h) const {
     typedef __attribute__((address_space(3))) f32x4_t lds_f32x4_t;
     return *(const lds_f32x4_t*)(sat + by + ks * 64 + h * 16);
   }
-  static __device__ __forceinline__ u32x4_t values(u32x2_t q, f32x4_t lo, f32x4_t hi) {
+  // four values
+  static __device__ __forceinline__ u32x2_t values(uint32_t q, f32x4_t s) {
     auto sb = [](uint32_t x, int b) { return (float)(int8_t)(x >> (8 * b)); };
-    return (u32x4_t){pack_bf16(sb(q[0], 0) * lo[0], sb(q[0], 1) * lo[1]), pack_bf16(sb(q[0], 2) * lo[2], sb(q[0], 3) * lo[3]),
-                     pack_bf16(sb(q[1], 0) * hi[0], sb(q[1], 1) * hi[1]), pack_bf16(sb(q[1], 2) * hi[2], sb(q[1], 3) * hi[3])};
+    return (u32x2_t){pack_bf16(sb(q, 0) * s[0], sb(q, 1) * s[1]), pack_bf16(sb(q, 2) * s[2], sb(q, 3) * s[3])};
   }
 };
 
@@ -309,28 +340,28 @@ __device__ __forceinline__ u32x4_t eight(u32x2_t even, u32x2_t odd) {
   return (u32x4_t){lo[0], hi[0], lo[1], hi[1]};
 }
 
-// Results of a wave's 64 x 64 part of a tile (blocks [P][Q] of 32 x 32) to global
+// Results of a wave's part of a tile (PB x QB blocks [P][Q] of 32 x 32) to global
 // memory.  32 output rows at a time go through 4 KiB of LDS that the wave has
 // for itself, so that its stores are whole 128-byte lines (pairs: 64 bytes; 32
 // bytes a row straight from the registers cost 2 us a 256 x 256 tile).
-//   ps: scales of the part's 64 P rows, qs: of its 64 rows; r0, c0: first
+//   ps: scales of the part's P rows, qs: of its rows; r0, c0: first
 // output row and column; own: the wave's LDS; before: called before the first store.
 constexpr int kOwnBytes = 4096;
-template <class T, int EPI, class Before>
-__device__ __forceinline__ void emit(const TileArgs& a, const typename Mma<T>::Acc (&acc)[2][2], const float* ps,
+template <class T, int EPI, int PB, int QB, class Before>
+__device__ __forceinline__ void emit(const TileArgs& a, const typename Mma<T>::Acc (&acc)[PB][QB], const float* ps,
                                      const float* qs, int64_t r0, int64_t c0, int lane, uint8_t* own, Before&& before) {
-  constexpr int kN = kPairs<EPI> ? 1 : 2;                       // 32-column blocks of an output
+  constexpr int kN = kPairs<EPI> ? 1 : PB;                      // 32-column blocks of an output
   constexpr int kOuts = EPI == EPI_GATED_GRAD ? 2 : 1;
   constexpr int kRow = 64 * kN, kChunks = kRow / 16;            // bytes of a staged row, its 16-byte chunks
   constexpr int kPass = 64 / kChunks;                           // rows a store instruction covers
   const int l32 = lane & 31, hi = lane >> 5;
   const int64_t ld = kOuts * a.cols;
   auto swz = [](int r) { return kN == 2 ? (r & 7) : ((r >> 1) & 3); };
-  const bool whole = r0 + 64 <= a.rows && c0 + 32 * kN <= a.cols;    // the same for all lanes
-  u32x4_t dh[2][2];
+  const bool whole = r0 + 32 * QB <= a.rows && c0 + 32 * kN <= a.cols;    // the same for all lanes
+  u32x4_t dh[QB][2];
   if (EPI == EPI_GATED_GRAD) {
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb)
+    for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int64_t row = r0 + qb * 32 + l32, col = c0 + 16 * x + 8 * hi;
@@ -339,7 +370,7 @@ __device__ __forceinline__ void emit(const TileArgs& a, const typename Mma<T>::A
       }
   }
 #pragma unroll
-  for (int qb = 0; qb < 2; ++qb) {
+  for (int qb = 0; qb < QB; ++qb) {
     const float sq = std::is_same<T, int8_t>::value ? qs[qb * 32 + l32] : 1.0f;
 #pragma unroll
     for (int pb = 0; pb < kN; ++pb)

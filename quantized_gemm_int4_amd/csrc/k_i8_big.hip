@@ -171,7 +171,7 @@ k_i8_big(TileArgs a, int tiles_p, int tiles_q) {
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       // the copies land before the first store: the waits for them wait for no store
-      emit<T, EPI>(a, acc[h >> 1][h & 1], sc + (h >> 1) * 128 + wp * 64, sc + 256 + (h & 1) * 128 + wq * 64,
+      emit<T, EPI, 2, 2>(a, acc[h >> 1][h & 1], sc + (h >> 1) * 128 + wp * 64, sc + 256 + (h & 1) * 128 + wq * 64,
                    r0 + (h & 1) * 128, c0 + (h >> 1) * kCols, ln, lds + kBigOwn + wave * kOwnBytes, [&]() {
                      if (h == 0) __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
                    });
