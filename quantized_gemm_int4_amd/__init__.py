@@ -161,6 +161,11 @@ def _stream(stream=None):
     return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
+def _raw_stream(dev):
+    # of the device of index dev, which is the current one
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _ok(fn, code):
     if code != 0:
         raise HmError(fn, code)
@@ -648,7 +653,7 @@ def hm_quant_int8_rows(x, x8=None, row_scale=None, stream=None):
     x8 = _new(torch.int8, (m, k), dev) if x8 is None else x8
     row_scale = _new(torch.float32, (m,), dev) if row_scale is None else row_scale
     code = lib.hm_quant_int8_rows(_arg(x, torch.bfloat16, (m, k), "x", dev), m, k, _arg(x8, torch.int8, (m, k), "x8", dev),
-                                  _arg(row_scale, torch.float32, (m,), "row_scale", dev), _stream())
+                                  _arg(row_scale, torch.float32, (m,), "row_scale", dev), _raw_stream(dev))
     _ok("hm_quant_int8_rows", code)
     return x8, row_scale
 
@@ -675,8 +680,7 @@ def hm_gemm_int8_grad_workspace_size(m, n, k):
     return _int8_ws_size("hm_gemm_int8_grad_workspace_size", m, n, k)
 
 
-def _int8_args(x8, x_scales, w8, w_scales, dev):
-    (m, k), n = x8.shape, w8.shape[0]
+def _int8_args(x8, x_scales, w8, w_scales, m, n, k, dev):
     return (_arg(x8, torch.int8, (m, k), "x8", dev), _arg(x_scales, torch.float32, (m,), "x_scales", dev),
             _arg(w8, torch.int8, (n, k), "w8", dev), _arg(w_scales, torch.float32, (n,), "w_scales", dev))
 
@@ -691,8 +695,8 @@ def hm_gemm_int8(x8, x_scales, w8, w_scales, y=None, ws=None, stream=None):
     (m, k), (n, _), dev = _dims(x8, "x8"), _dims(w8, "w8"), x8.get_device()
     y = _new(torch.bfloat16, (m, n), dev) if y is None else y
     wsp, wsb, ws = _ws(ws, hm_gemm_int8_workspace_size, (m, n, k), dev)
-    code = lib.hm_gemm_int8(*_int8_args(x8, x_scales, w8, w_scales, dev), m, n, k,
-                            _arg(y, torch.bfloat16, (m, n), "y", dev), wsp, wsb, _stream())
+    code = lib.hm_gemm_int8(*_int8_args(x8, x_scales, w8, w_scales, m, n, k, dev), m, n, k,
+                            _arg(y, torch.bfloat16, (m, n), "y", dev), wsp, wsb, _raw_stream(dev))
     _ok("hm_gemm_int8", code)
     return y
 
@@ -707,8 +711,8 @@ def hm_gemm_int8_gated(x8, x_scales, w8, w_scales, h=None, ws=None, stream=None)
     (m, k), (n, _), dev = _dims(x8, "x8"), _dims(w8, "w8"), x8.get_device()
     h = _new(torch.bfloat16, (m, n // 2), dev) if h is None else h
     wsp, wsb, ws = _ws(ws, hm_gemm_int8_gated_workspace_size, (m, n, k), dev)
-    code = lib.hm_gemm_int8_gated(*_int8_args(x8, x_scales, w8, w_scales, dev), m, n, k,
-                                  _arg(h, torch.bfloat16, (m, n // 2), "h", dev), wsp, wsb, _stream())
+    code = lib.hm_gemm_int8_gated(*_int8_args(x8, x_scales, w8, w_scales, m, n, k, dev), m, n, k,
+                                  _arg(h, torch.bfloat16, (m, n // 2), "h", dev), wsp, wsb, _raw_stream(dev))
     _ok("hm_gemm_int8_gated", code)
     return h
 
@@ -724,8 +728,8 @@ def hm_gemm_int8_gated_grad(dh, x8, x_scales, w8, w_scales, dgu=None, ws=None, s
     dgu = _new(torch.bfloat16, (m, n), dev) if dgu is None else dgu
     wsp, wsb, ws = _ws(ws, hm_gemm_int8_gated_grad_workspace_size, (m, n, k), dev)
     code = lib.hm_gemm_int8_gated_grad(_arg(dh, torch.bfloat16, (m, n // 2), "dh", dev),
-                                       *_int8_args(x8, x_scales, w8, w_scales, dev), m, n, k,
-                                       _arg(dgu, torch.bfloat16, (m, n), "dgu", dev), wsp, wsb, _stream())
+                                       *_int8_args(x8, x_scales, w8, w_scales, m, n, k, dev), m, n, k,
+                                       _arg(dgu, torch.bfloat16, (m, n), "dgu", dev), wsp, wsb, _raw_stream(dev))
     _ok("hm_gemm_int8_gated_grad", code)
     return dgu
 
@@ -744,9 +748,9 @@ def hm_gemm_int8_grad(dy, x8, x_scales, w8, w_scales, dx=None, dw=None, need_dx=
     dx = _new(bf, (m, k), dev) if need_dx and dx is None else dx
     dw = _new(bf, (n, k), dev) if need_dw and dw is None else dw
     wsp, wsb, ws = _ws(ws, hm_gemm_int8_grad_workspace_size, (m, n, k), dev)
-    code = lib.hm_gemm_int8_grad(_arg(dy, bf, (m, n), "dy", dev), *_int8_args(x8, x_scales, w8, w_scales, dev), m, n, k,
+    code = lib.hm_gemm_int8_grad(_arg(dy, bf, (m, n), "dy", dev), *_int8_args(x8, x_scales, w8, w_scales, m, n, k, dev), m, n, k,
                                  None if dx is None else _arg(dx, bf, (m, k), "dx", dev),
-                                 None if dw is None else _arg(dw, bf, (n, k), "dw", dev), wsp, wsb, _stream())
+                                 None if dw is None else _arg(dw, bf, (n, k), "dw", dev), wsp, wsb, _raw_stream(dev))
     _ok("hm_gemm_int8_grad", code)
     return dx, dw
 

@@ -154,7 +154,7 @@ Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t k, bool grad) 
 Plan plan_gradient(int64_t rows, int64_t cols, int64_t kbytes, int64_t terms) {
   const Plan codes = plan_tiles(rows, cols, false, kbytes, CODES);
   Plan copy = plan_tiles(rows, cols, false, kbytes, COPY);
-  copy.ns += 3000 + terms * cols * 3 / 5000;       // making the copy, 5 TB/s
+  copy.ns += 3000 + terms * cols * 3 / 6000;       // making the copy: 6 TB/s
   return codes.ns < copy.ns ? codes : copy;
 }
 

@@ -55,13 +55,16 @@ __device__ __forceinline__ void tile_at(uint32_t t, int tiles_p, int tiles_q, in
   tq = (int)(4u * group + in - c * rows);
   tp = (int)c;
 }
-// The block's `turn`th of the first `total` tiles (under 2^24), for `blocks` blocks (a multiple
-// of 8): the eight XCDs (block b runs on b % 8) get consecutive ranges of that order,
-// and with it their own L2s.  False: none.
+// A block's number among `total` (under 2^24) that are dealt out to `blocks` blocks (a
+// multiple of 8) over several turns, so that the eight XCDs (block b runs on b % 8) get
+// consecutive ranges, and with them operands of their own L2s.  total: none.
+__device__ __forceinline__ uint32_t number_of(uint32_t total, uint32_t block, uint32_t blocks, uint32_t turn) {
+  const uint32_t x = block & 7, t = x * total / 8 + (block >> 3) + turn * (blocks >> 3);
+  return t < (x + 1) * total / 8 ? t : total;
+}
 __device__ __forceinline__ bool tile_of(uint32_t total, uint32_t blocks, uint32_t turn, int tiles_p, int tiles_q, int& tp, int& tq) {
-  const uint32_t x = blockIdx.x & 7;
-  const uint32_t t = x * total / 8 + (blockIdx.x >> 3) + turn * (blocks >> 3);
-  if (t >= (x + 1) * total / 8) return false;
+  const uint32_t t = number_of(total, blockIdx.x, blocks, turn);
+  if (t >= total) return false;
   tile_at(t, tiles_p, tiles_q, tp, tq);
   return true;
 }
@@ -289,20 +292,19 @@ struct Codes {
 };
 
 // Gate, up and the gradient of h to those of both, with sig = 1 / (1 + e^-g)
-// from e = e^-|g| <= 1, so that neither sig nor 1 - sig overflows or cancels.
-// Beyond |g| = 64, where e would leave the normal range, e 2^64 is held and the
-// results of negative gates are scaled back last.  The fast exponential and
-// the hardware reciprocal (a few 2^-23 together) stay far below the bf16
-// rounding of the results.
+// from e = e^-|g| <= 1, so that neither sig nor 1 - sig overflows or cancels.  The
+// exponential is taken as 2^(64 - |g| log2 e), which the hardware's leaves in the
+// normal range to |g| = 131, and scaled back by a product, which keeps subnormal
+// results (with e^-|g| itself dg of a gate of -88 was 0 for -1e-37).  Its error (the
+// rounding of an argument up to 64, 2^-18) and the reciprocal's stay far below the
+// bf16 rounding of the results.
 __device__ __forceinline__ void gated_grad(float g, float u, float dh, float& dg, float& du) {
-  const bool far = fabsf(g) > 64.0f, pos = g >= 0.0f;
-  const float back = far ? 5.421010862427522e-20f : 1.0f;
-  const float e = __expf((far ? 44.3614195558365f : 0.0f) - fabsf(g));
-  const float s = __builtin_amdgcn_rcpf(1.0f + e * back), es = e * s;
-  const float sig = pos ? s : es, last = pos ? 1.0f : back;
-  const float rest = pos ? es * back : s;                              // 1 - sig
-  du = dh * (g * sig) * last;
-  dg = dh * u * (sig * __builtin_fmaf(g, rest, 1.0f)) * last;
+  const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(-fabsf(g), 1.4426950408889634f, 64.0f)) * 0x1p-64f;
+  const float s = __builtin_amdgcn_rcpf(1.0f + e), es = e * s;
+  const bool pos = g >= 0.0f;
+  const float sig = pos ? s : es, rest = pos ? es : s;                 // sig and 1 - sig
+  du = dh * (g * sig);
+  dg = dh * u * (sig * __builtin_fmaf(g, rest, 1.0f));
 }
 
 // Eight bf16 values of a row at any 2-byte address (rows of an odd number of
@@ -346,9 +348,24 @@ __device__ __forceinline__ u32x4_t eight(u32x2_t even, u32x2_t odd) {
 // bytes a row straight from the registers cost 2 us a 256 x 256 tile).
 //   ps: scales of the part's P rows, qs: of its rows; r0, c0: first
 // output row and column; own: the wave's LDS; before: called before the first store.
+//   dh: the part's values of dh (EPI_GATED_GRAD), from load_dh.
 constexpr int kOwnBytes = 4096;
+template <int EPI, int QB>
+__device__ __forceinline__ void load_dh(const TileArgs& a, u32x4_t (&dh)[QB][2], int64_t r0, int64_t c0, int lane) {
+  if (EPI != EPI_GATED_GRAD) return;
+  const int l32 = lane & 31, hi = lane >> 5;
+  const bool whole = r0 + 32 * QB <= a.rows && c0 + 32 <= a.cols;    // the same for all lanes
+#pragma unroll
+  for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int64_t row = r0 + qb * 32 + l32, col = c0 + 16 * x + 8 * hi;
+      if (whole) dh[qb][x] = *reinterpret_cast<const u32x4_a2_t*>(a.dh + row * a.cols + col);
+      else dh[qb][x] = row < a.rows ? load8(a.dh + row * a.cols, a.cols, col) : (u32x4_t){0u, 0u, 0u, 0u};
+    }
+}
 template <class T, int EPI, int PB, int QB, class Before>
-__device__ __forceinline__ void emit(const TileArgs& a, const typename Mma<T>::Acc (&acc)[PB][QB], const float* ps,
+__device__ __forceinline__ void emit(const TileArgs& a, const typename Mma<T>::Acc (&acc)[PB][QB], const u32x4_t (&dh)[QB][2], const float* ps,
                                      const float* qs, int64_t r0, int64_t c0, int lane, uint8_t* own, Before&& before) {
   constexpr int kN = kPairs<EPI> ? 1 : PB;                      // 32-column blocks of an output
   constexpr int kOuts = EPI == EPI_GATED_GRAD ? 2 : 1;
@@ -358,17 +375,6 @@ __device__ __forceinline__ void emit(const TileArgs& a, const typename Mma<T>::A
   const int64_t ld = kOuts * a.cols;
   auto swz = [](int r) { return kN == 2 ? (r & 7) : ((r >> 1) & 3); };
   const bool whole = r0 + 32 * QB <= a.rows && c0 + 32 * kN <= a.cols;    // the same for all lanes
-  u32x4_t dh[QB][2];
-  if (EPI == EPI_GATED_GRAD) {
-#pragma unroll
-    for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int64_t row = r0 + qb * 32 + l32, col = c0 + 16 * x + 8 * hi;
-        if (whole) dh[qb][x] = *reinterpret_cast<const u32x4_a2_t*>(a.dh + row * a.cols + col);
-        else dh[qb][x] = row < a.rows ? load8(a.dh + row * a.cols, a.cols, col) : (u32x4_t){0u, 0u, 0u, 0u};
-      }
-  }
 #pragma unroll
   for (int qb = 0; qb < QB; ++qb) {
     const float sq = std::is_same<T, int8_t>::value ? qs[qb * 32 + l32] : 1.0f;

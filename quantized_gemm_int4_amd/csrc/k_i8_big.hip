@@ -168,10 +168,13 @@ k_i8_big(TileArgs a, int tiles_p, int tiles_q) {
     const int64_t c0 = kPairs<EPI> ? (int64_t)tp * (kI8Big / 2) + wp * 32 : (int64_t)tp * kI8Big + wp * 64;
     constexpr int kCols = kPairs<EPI> ? 64 : 128;      // output columns of a P half
     const int ln = (int)in_vgpr((uint32_t)lane);       // (what is worked out again needs no registers in between)
+    u32x4_t dh[4][2][2];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) load_dh<EPI>(a, dh[h], r0 + (h & 1) * 128, c0 + (h >> 1) * kCols, ln);
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       // the copies land before the first store: the waits for them wait for no store
-      emit<T, EPI, 2, 2>(a, acc[h >> 1][h & 1], sc + (h >> 1) * 128 + wp * 64, sc + 256 + (h & 1) * 128 + wq * 64,
+      emit<T, EPI, 2, 2>(a, acc[h >> 1][h & 1], dh[h], sc + (h >> 1) * 128 + wp * 64, sc + 256 + (h & 1) * 128 + wq * 64,
                    r0 + (h & 1) * 128, c0 + (h >> 1) * kCols, ln, lds + kBigOwn + wave * kOwnBytes, [&]() {
                      if (h == 0) __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
                    });

@@ -94,9 +94,14 @@ k_i8_tile(TileArgs a, TilePlan pl) {
   if (blockIdx.x < whole) {
     if (!tile_of(pl.full, whole, 0, pl.tiles_p, pl.tiles_q, tp, tq)) return;
   } else {
-    item = blockIdx.x - whole;
-    tile_at(pl.full + item / pl.cut, pl.tiles_p, pl.tiles_q, tp, tq);
-    first = (item % pl.cut) * pl.per;
+    // the tiles of one part of the contraction after each other: neighbours share operands
+    const uint32_t rest = (uint32_t)(pl.tiles_p * pl.tiles_q - pl.full), total = rest * pl.cut;
+    const uint32_t j = number_of(total, blockIdx.x - whole, gridDim.x - whole, 0);
+    if (j >= total) return;
+    const uint32_t part = j / rest, t = j - part * rest;
+    tile_at(pl.full + t, pl.tiles_p, pl.tiles_q, tp, tq);
+    item = (int)(t * pl.cut + part);
+    first = (int)part * pl.per;
     last = min(all, first + pl.per);
   }
   const int steps = last - first;
@@ -234,7 +239,9 @@ k_i8_tile(TileArgs a, TilePlan pl) {
   }
   const int64_t r0 = (int64_t)tq * kI8Tile + wq * 64;
   const int64_t c0 = kPairs<EPI> ? (int64_t)tp * (kI8Tile / 2) + wp * 32 : (int64_t)tp * kI8Tile + wp * 32 * PB;
-  emit<T, EPI, PB, QB>(a, acc, sc + wp * 64, sc + kI8Tile + wq * 64, r0, c0, lane, lds + wave * kOwnBytes, [] {});
+  u32x4_t dh[QB][2];
+  load_dh<EPI>(a, dh, r0, c0, lane);
+  emit<T, EPI, PB, QB>(a, acc, dh, sc + wp * 64, sc + kI8Tile + wq * 64, r0, c0, lane, lds + wave * kOwnBytes, [] {});
 }
 
 // The tiles that were split: the sums of their parts, in order, and what the
@@ -313,7 +320,7 @@ hipError_t go(const TileArgs& a, const TilePlan& pl, hipStream_t st) {
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (attr != hipSuccess) return attr;
   const int64_t split = (int64_t)pl.tiles_p * pl.tiles_q - pl.full;
-  const int64_t blocks = 8 * (((int64_t)pl.full + 7) / 8) + split * pl.cut;
+  const int64_t blocks = 8 * (((int64_t)pl.full + 7) / 8 + (split * pl.cut + 7) / 8);
   hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(320), kLds, st, a, pl);
   if (split) {
     const int per = kPairs<EPI> ? 8 : 16;          // blocks of a tile: 16 rows, 8 rows
