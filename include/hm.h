@@ -543,7 +543,7 @@ hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const uint16_t
  *
  * Sizes of all of them: 0 <= m <= 8388480; 1 <= n <= 2^22; k a multiple of 128,
  * 128 .. 130944 (every sum of k products then fits an int32: sums are exact);
- * ceil(m/128) ceil(n/128) < 2^24 - 8, and the same of (m, k) and (n, k) for the
+ * ceil(m/128) ceil(n/128) <= 2^23, and the same of (m, k) and (n, k) for the
  * gradient.  HM_ERR_SHAPE otherwise.  Codes may be any int8, scales any finite
  * fp32; a NaN or infinite scale makes its row (token) or column (channel) of
  * the results NaN or infinite and leaves the others alone, but where it is
@@ -612,6 +612,19 @@ hm_status hm_gemm_int8_grad_workspace_size(int64_t m, int64_t n, int64_t k, size
 hm_status hm_gemm_int8_grad(const uint16_t* dy, const int8_t* x8, const float* x_scales, const int8_t* w8,
                             const float* w_scales, int64_t m, int64_t n, int64_t k, uint16_t* dx, uint16_t* dw,
                             void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Which of the int8 calls a plan is asked for. */
+typedef enum hm_int8_op {
+  HM_INT8_GEMM = 0,        /* hm_gemm_int8 */
+  HM_INT8_GATED = 1,       /* hm_gemm_int8_gated */
+  HM_INT8_GATED_GRAD = 2,  /* hm_gemm_int8_gated_grad */
+  HM_INT8_GRAD = 3         /* hm_gemm_int8_grad: both gradients, dx first */
+} hm_int8_op;
+
+/* A short text naming the kernels and tiles that the call runs for these sizes
+ * (no device access); HM_ERR_SHAPE for sizes that the call refuses, HM_ERR_UNSUPPORTED for
+ * another op, HM_ERR_NULL without a buffer. */
+hm_status hm_gemm_int8_plan(int32_t op, int64_t m, int64_t n, int64_t k, char* buf, size_t buf_len);
 
 /* ------------------------------------------------------------ measurement */
 

@@ -25,6 +25,7 @@ WFMT = {"int4_sym": HM_W_INT4_SYM, "uint4_zp": HM_W_UINT4_ZP, "mxfp4": HM_W_MXFP
 CODE_BITS = {HM_W_UINT3_ZP: 3, HM_W_UINT2_ZP: 2, HM_W_INT8_SYM: 8}     # other formats: 4
 STATUS = {0: "HM_OK", 1: "HM_ERR_NULL", 2: "HM_ERR_SHAPE", 3: "HM_ERR_ALIGN",
           4: "HM_ERR_UNSUPPORTED", 5: "HM_ERR_WORKSPACE", 6: "HM_ERR_HIP", 7: "HM_ERR_ABI", 8: "HM_ERR_TUNING"}
+HM_INT8_GEMM, HM_INT8_GATED, HM_INT8_GATED_GRAD, HM_INT8_GRAD = range(4)
 HM_PATH_STREAM, HM_PATH_MID, HM_PATH_BIG, HM_PATH_TILE = 1, 2, 3, 4
 
 
@@ -133,6 +134,7 @@ def _load():
         "hm_gemm_int8_gated_grad_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],
         "hm_gemm_int8_gated_grad": [P, P, P, P, P, I64, I64, I64, P, P, SZ, P],
         "hm_gemm_int8_grad_workspace_size": [I64, I64, I64, ctypes.POINTER(SZ)],
+        "hm_gemm_int8_plan": [I32, I64, I64, I64, ctypes.c_char_p, SZ],
         "hm_gemm_int8_grad": [P, P, P, P, P, I64, I64, I64, P, P, P, SZ, P],
         "hm_moe_gemm_static": [D, P, I32, P, P, I32, I64, I32, P, P, P, T, P],
     }
@@ -678,6 +680,13 @@ def hm_gemm_int8_gated_grad_workspace_size(m, n, k):
 
 def hm_gemm_int8_grad_workspace_size(m, n, k):
     return _int8_ws_size("hm_gemm_int8_grad_workspace_size", m, n, k)
+
+
+def hm_gemm_int8_plan(op, m, n, k):
+    """What the call (an HM_INT8_* value) runs for these sizes, as a text."""
+    buf = ctypes.create_string_buffer(256)
+    _ok("hm_gemm_int8_plan", lib.hm_gemm_int8_plan(int(op), int(m), int(n), int(k), buf, 256))
+    return buf.value.decode()
 
 
 def _int8_args(x8, x_scales, w8, w_scales, m, n, k, dev):

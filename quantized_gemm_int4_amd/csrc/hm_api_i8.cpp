@@ -2,6 +2,7 @@
 // layout and launches.  Every check runs before any launch; nothing is
 // allocated.
 #include <hip/hip_runtime.h>
+#include <stdio.h>
 
 #include <algorithm>
 #include <initializer_list>
@@ -44,10 +45,10 @@ bool overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) 
 constexpr int64_t kMaxRows = 8388480;         // 65535 x 128, as hm_gemm
 constexpr int64_t kMaxCols = 1ll << 22;       // 256 rows of bf16 gradients stay under 2^31 bytes
 constexpr int64_t kMaxK = 130944;             // below 2^31 / 128^2: no sum of products of two int8 leaves the int32 range
-constexpr int64_t kMaxBlocks = (1ll << 24) - 1;   // of a launch: 2^32 threads
+constexpr int64_t kMaxTiles = 1ll << 23;      // of 320 threads each: a launch has less than 2^32
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
-bool tiles_fit(int64_t rows, int64_t cols) { return div_up(rows, kI8Tile) * div_up(cols, kI8Tile) + 7 <= kMaxBlocks; }
+bool tiles_fit(int64_t rows, int64_t cols) { return div_up(rows, kI8Tile) * div_up(cols, kI8Tile) <= kMaxTiles; }
 
 // n: rows of the weights (gated: 2 d)
 hm_status check_sizes(int64_t m, int64_t n, int64_t k) {
@@ -374,4 +375,36 @@ HM_API hm_status hm_gemm_int8_grad(const uint16_t* dy, const int8_t* x8, const f
     if (e == hipSuccess) e = multiply(a, g.dw, I8_DW, at + g.part, stream);
   }
   return done(e);
+}
+
+// ----------------------------------------------------------------------- plan
+
+namespace {
+
+int say(const Plan& p, bool pairs, int64_t rows, int64_t cols, char* buf, size_t len) {
+  if (p.few)
+    return snprintf(buf, len, "few rows: row blocks %d, weight blocks %d", (int)div_up(rows, 16), i8_few_blocks(cols, pairs));
+  if (p.big) return snprintf(buf, len, "tiles 256x256: %lld", (long long)(div_up(rows, kI8Big) * div_up(cols, pairs ? kI8Big / 2 : kI8Big)));
+  return snprintf(buf, len, "tiles 128x128%s: %d whole, %d in %d parts", p.tiles.codes ? " of codes" : "", p.tiles.full,
+                  p.tiles.tiles_p * p.tiles.tiles_q - p.tiles.full, p.tiles.cut);
+}
+
+}  // namespace
+
+HM_API hm_status hm_gemm_int8_plan(int32_t op, int64_t m, int64_t n, int64_t k, char* buf, size_t buf_len) {
+  if (op < HM_INT8_GEMM || op > HM_INT8_GRAD) return HM_ERR_UNSUPPORTED;
+  const bool pairs = op == HM_INT8_GATED || op == HM_INT8_GATED_GRAD;
+  if (hm_status s = op == HM_INT8_GRAD ? check_grad(m, n, k) : pairs ? check_gated(m, n, k) : check_sizes(m, n, k)) return s;
+  if (!buf || !buf_len) return HM_ERR_NULL;
+  if (op != HM_INT8_GRAD) {
+    if (m == 0) snprintf(buf, buf_len, "nothing");
+    else say(plan_product(m, pairs ? n / 2 : n, pairs, k, op == HM_INT8_GATED_GRAD), pairs, m, pairs ? n / 2 : n, buf, buf_len);
+    return HM_OK;
+  }
+  const GradPlan g = plan_grad(m, n, k);
+  char dx[80] = "nothing", dw[80];
+  if (m) say(g.dx, false, m, k, dx, sizeof dx);
+  say(g.dw, false, n, k, dw, sizeof dw);
+  snprintf(buf, buf_len, "dx %s; dw %s", dx, dw);
+  return HM_OK;
 }

@@ -1,0 +1,140 @@
+"""The 8-bit integer layers at sizes that reach every kernel and way to cut the
+work (the plan's text says which), against the definition in 64 bits on the GPU.
+
+Bounds as in test_gpu_int8_layers: u = 2^-8 half a bf16 step, e = 2^-24 half an
+fp32 step."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+U, E = 2.0 ** -8, 2.0 ** -24
+F = torch.float64
+
+
+def _layer(seed, m, n, k):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    q = lambda r: (torch.randn(r, k, generator=g, device="cuda") * 40).round().clamp(-128, 127).to(torch.int8)     # noqa: E731
+    s = lambda r, top: (torch.rand(r, generator=g, device="cuda") + 0.01) * top                                     # noqa: E731
+    rows = lambda r, c: torch.randn(r, c, generator=g, device="cuda").to(torch.bfloat16)                            # noqa: E731
+    return (q(m), s(m, 1 / 40), q(n), s(n, 1 / (40 * k ** 0.5))), rows
+
+
+def _hats(a):
+    return a[0].to(F) * a[1].to(F)[:, None], a[2].to(F) * a[3].to(F)[:, None]
+
+
+def _product(a):
+    """The whole-number sums (exact in fp64 in any order) times both scales."""
+    return (a[0].to(F) @ a[2].to(F).t()) * a[1].to(F)[:, None] * a[3].to(F)
+
+
+def _close(got, ref, lim, what):
+    bad = ~((got.to(F) - ref).abs() <= lim)
+    assert not bool(bad.any()), (what, int(bad.sum()), bad.nonzero()[:3].tolist(), got[bad][:3].tolist(), ref[bad][:3].tolist())
+
+
+FORWARD = [
+    (16, 700, 128, "few rows: row blocks 1, weight blocks 1"), (17, 7001, 384, "few rows: row blocks 2, weight blocks 2"),
+    (40, 13003, 128, "few rows: row blocks 3, weight blocks 4"), (64, 12400, 640, "few rows: row blocks 4, weight blocks 4"),
+    (9, 12288, 256, "few rows: row blocks 1, weight blocks 4"), (33, 6200, 384, "few rows: row blocks 3, weight blocks 2"),
+    (300, 700, 128, "whole, 0 in 1"), (1000, 4100, 640, "264 whole, 0 in 1"), (150, 600, 4096, "0 whole, 10 in"),
+    (1021, 4099, 7168, "256 whole, 8 in"), (520, 300, 8320, "0 whole, 15 in"),
+    (2000, 5201, 256, "256x256: 168"), (2100, 9002, 384, "256x256: 324"), (4097, 5000, 128, "256x256: 340"),
+    (2049, 7169, 2176, "128x128: 969 whole"), (2305, 7000, 1152, "256x256: 280")]
+
+
+@pytest.mark.parametrize("m,n,k,plan", FORWARD)
+def test_product(m, n, k, plan):
+    import quantized_gemm_int4_amd as hm
+    assert plan in hm.hm_gemm_int8_plan(hm.HM_INT8_GEMM, m, n, k)
+    a, _ = _layer(m + n + k, m, n, k)
+    ref = _product(a)
+    y = torch.full((m + 1, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    hm.hm_gemm_int8(*a, y=y[:m])
+    _close(y[:m], ref, ref.abs() * (U + 4 * E), "y")
+    assert bool((y[m] == 7).all())
+    again = hm.hm_gemm_int8(*a)
+    assert torch.equal(again, y[:m])
+
+
+GATED = [(16, 7000, 256, "few rows: row blocks 1, weight blocks 4"), (50, 1100, 384, "few rows: row blocks 4, weight blocks 2"),
+         (300, 350, 128, "whole, 0 in 1"), (150, 300, 4096, "0 whole, 10 in"), (1021, 2049, 7168, "256 whole, 8 in"),
+         (2000, 2601, 256, "256x256: 168"), (2100, 4501, 384, "256x256: 324")]
+
+
+@pytest.mark.parametrize("m,d,k,plan", GATED)
+def test_gated_and_its_gradient(m, d, k, plan):
+    import quantized_gemm_int4_amd as hm
+    assert plan in hm.hm_gemm_int8_plan(hm.HM_INT8_GATED, m, 2 * d, k)
+    if "few" not in plan:
+        assert plan in hm.hm_gemm_int8_plan(hm.HM_INT8_GATED_GRAD, m, 2 * d, k)
+    a, rows = _layer(m + d + k, m, 2 * d, k)
+    g, u = _product(a).chunk(2, 1)
+    s, rest = torch.sigmoid(g), torch.sigmoid(-g)
+    c = (60 + 4 * g.abs()) * 2 * E
+    h = torch.full((m + 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    hm.hm_gemm_int8_gated(*a, h=h[:m])
+    ref = g * s * u
+    _close(h[:m], ref, ref.abs() * (U + c) + 1e-30, "h")
+    dh = rows(m, d)
+    out = torch.full((m + 1, 2 * d), 7.0, dtype=torch.bfloat16, device="cuda")
+    hm.hm_gemm_int8_gated_grad(dh, *a, dgu=out[:m])
+    f = dh.to(F)
+    du, dg = f * g * s, f * u * s * (1 + g * rest)
+    _close(out[:m, d:], du, du.abs() * (U + c) + 1e-30, "du")
+    _close(out[:m, :d], dg, dg.abs() * U + (f * u).abs() * s * (1 + g.abs() * rest) * 2 * c + 1e-30, "dg")
+    assert bool((h[m] == 7).all()) and bool((out[m] == 7).all())
+
+
+GRAD = [(100, 300, 256, "dx tiles 128x128 of codes", "dw tiles 128x128 of codes"), (520, 4096, 384, "of codes: 0 whole, 15 in", "of codes"),
+        (1500, 6000, 2048, "dx tiles 128x128: 192 whole", "dw tiles 256x256: 192"),
+        (3000, 5003, 1024, "dx tiles 128x128: 192 whole", "dw tiles 128x128: 256 whole, 64 in 3"),
+        (4096, 4100, 1152, "dx tiles 128x128: 256 whole, 32 in", "dw tiles 128x128: 256 whole, 41 in"),
+        (2600, 2600, 4096, "dx tiles 256x256: 176", "dw tiles 256x256: 176"), (5100, 4100, 4096, "dx tiles 256x256: 320", "dw tiles"),
+        (64, 14336, 1024, "of codes", "dw")]
+
+
+@pytest.mark.parametrize("m,n,k,dxp,dwp", GRAD)
+def test_gradient(m, n, k, dxp, dwp):
+    import quantized_gemm_int4_amd as hm
+    one, two = hm.hm_gemm_int8_plan(hm.HM_INT8_GRAD, m, n, k).split("; ")
+    assert dxp in one and dwp in two, (one, two)
+    a, rows = _layer(m + n + k, m, n, k)
+    x, w = _hats(a)
+    dy = rows(m, n) * 0.05
+    f = dy.to(F)
+    dx = torch.full((m + 1, k), 7.0, dtype=torch.bfloat16, device="cuda")
+    dw = torch.full((n + 1, k), 7.0, dtype=torch.bfloat16, device="cuda")
+    hm.hm_gemm_int8_grad(dy, *a, dx=dx[:m], dw=dw[:n])
+    for name, got, ref, b, terms in (("dx", dx[:m], f @ w, f.abs() @ w.abs(), n), ("dw", dw[:n], f.t() @ x, f.abs().t() @ x.abs(), m)):
+        _close(got, ref, b * (U + (terms + 2) * 2 * E) * (1 + U) + ref.abs() * U + 1e-30, name)
+        # two independent roundings of at most u, see test_gpu_int8_layers
+        assert float((got.to(F) - ref).norm() / ref.norm()) <= U, name
+    assert bool((dx[m] == 7).all()) and bool((dw[n] == 7).all())
+    # one of the two alone, and again: the same bits
+    one, _ = hm.hm_gemm_int8_grad(dy, *a, need_dw=False)
+    _, two = hm.hm_gemm_int8_grad(dy, *a, need_dx=False)
+    assert torch.equal(one, dx[:m]) and torch.equal(two, dw[:n])
+
+
+def test_gradient_against_differences():
+    """A loss of the product along random directions of x_hat and w_hat: its
+    central difference is the gradient's inner product with the direction (the
+    loss is quadratic, so the difference has no error of its own)."""
+    import quantized_gemm_int4_amd as hm
+    m, n, k = 300, 520, 384
+    a, rows = _layer(5, m, n, k)
+    x, w = _hats(a)
+    dy = rows(m, n)
+    dx, dw = hm.hm_gemm_int8_grad(dy, *a)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    vx, vw = torch.randn(m, k, generator=g, device="cuda", dtype=F), torch.randn(n, k, generator=g, device="cuda", dtype=F)
+    loss = lambda p, q: float((dy.to(F) * (p @ q.t())).sum())                                   # noqa: E731
+    for got, v, diff in ((dx, vx, loss(x + vx, w) - loss(x - vx, w)), (dw, vw, loss(x, w + vw) - loss(x, w - vw))):
+        # every element of the gradient is off by at most 2 u (1 + u) of its terms' absolute sum, which its own
+        # rounding noise stays under by the square root of their number; bounded here by the sum over all elements
+        inner = float((got.to(F) * v).sum())
+        size = float((got.to(F).abs() * v.abs()).sum())
+        assert abs(inner - diff / 2) <= 2 * U * size, (inner, diff / 2, size)
