@@ -138,3 +138,29 @@ def test_gradient_against_differences():
         inner = float((got.to(F) * v).sum())
         size = float((got.to(F).abs() * v.abs()).sum())
         assert abs(inner - diff / 2) <= 2 * U * size, (inner, diff / 2, size)
+
+
+def test_adapters_beside_an_int8_layer():
+    """An adapter trained on a layer whose weights stay in 8 bits: the layer's
+    product is the adapters' base, its gradient their dx_base."""
+    import quantized_gemm_int4_amd as hm
+    m, n, k, rank, L = 130, 260, 384, 16, 3
+    a, rows = _layer(9, m, n, k)
+    x = (a[0].float() * a[1][:, None]).to(torch.bfloat16)
+    ids = (torch.arange(m, device="cuda") % (L + 1) - 1).to(torch.int32)
+    A, B = rows(L, rank * k).view(L, rank, k) * k ** -0.5, rows(L, n * rank).view(L, n, rank) * 0.1
+    A, B, sc = A.contiguous(), B.contiguous(), torch.ones(L, device="cuda")
+    d, h = hm.lora_desc(n, k, rank, L), torch.empty(m, rank, device="cuda")
+    base = hm.hm_gemm_int8(*a)
+    y = hm.hm_lora(d, x, ids, A, B, sc, base=base, h=h)
+    dy = rows(m, n)
+    dxb, _ = hm.hm_gemm_int8_grad(dy, *a, need_dw=False)
+    dx, da, db = hm.hm_lora_grad(d, dy, x, h, ids, A, B, sc, dx_base=dxb)
+    yr, dxr = base.to(F), dxb.to(F)
+    for e in range(L):
+        r = (ids == e).nonzero()[:, 0]
+        yr[r] += x[r].to(F) @ A[e].to(F).t() @ B[e].to(F).t()
+        dxr[r] += dy[r].to(F) @ B[e].to(F) @ A[e].to(F)
+    # sums of a few hundred terms in fp32, one rounding: 2 u of the result and its base cover both
+    assert bool(((y.to(F) - yr).abs() <= U * yr.abs() + 2.0 ** -12 * (yr.abs() + base.to(F).abs() + 1)).all())
+    assert bool(((dx.to(F) - dxr).abs() <= U * dxr.abs() + 2.0 ** -12 * (dxr.abs() + dxb.to(F).abs() + 1)).all())
