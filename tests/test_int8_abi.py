@@ -94,11 +94,28 @@ def test_workspace(fn, m):
 
 
 def test_gradient_of_one_side():
-    fn = "hm_gemm_int8_grad"
-    assert _call(fn, dx=None, w8=None, ws_=None, wsb=0) == WORKSPACE      # the checks of the pointers are behind it
-    assert _call(fn, dw=None, x8=None, xs=None, wsb=0) == WORKSPACE
-    assert _call(fn, dx=None, dw=None) == NULL
-    assert _call(fn, dw=None, w8=None) == NULL and _call(fn, dx=None, xs=None) == NULL
+    fn, odd = "hm_gemm_int8_grad", dict(n=257)                 # (rows that are padded: a workspace is needed)
+    assert hm.hm_gemm_int8_grad_workspace_size(4, 257, 512) > 0
+    assert _call(fn, odd, dx=None, w8=None, ws_=None, wsb=0) == WORKSPACE      # the checks of the pointers are behind it
+    assert _call(fn, odd, dw=None, x8=None, xs=None, wsb=0) == WORKSPACE
+    assert _call(fn, odd, dx=None, dw=None) == NULL
+    assert _call(fn, odd, dw=None, w8=None) == NULL and _call(fn, odd, dx=None, xs=None) == NULL
+
+
+def test_plan():
+    buf = ctypes.create_string_buffer(200)
+    plan = hm.lib.hm_gemm_int8_plan
+    for op in range(4):
+        assert plan(op, 100, 256, 512, buf, 200) == 0 and b"tiles" in buf.value
+        assert plan(op, 0, 256, 512, buf, 200) == 0
+        assert plan(op, 100, 256, 500, buf, 200) == SHAPE and plan(op, -1, 256, 512, buf, 200) == SHAPE
+        assert plan(op, 100, 256, 512, None, 200) == NULL and plan(op, 100, 256, 512, buf, 0) == NULL
+        assert plan(op, 100, 256, 512, buf, 4) == 0 and len(buf.value) < 4         # cut to the buffer
+    assert plan(4, 100, 256, 512, buf, 200) == UNSUPPORTED and plan(-1, 100, 256, 512, buf, 200) == UNSUPPORTED
+    assert "few" in hm.hm_gemm_int8_plan(hm.HM_INT8_GEMM, 1, 14336, 4096)
+    for op in (hm.HM_INT8_GATED, hm.HM_INT8_GATED_GRAD):
+        with pytest.raises(hm.HmError):
+            hm.hm_gemm_int8_plan(op, 100, 257, 512)
 
 
 def test_binding_refusals():
