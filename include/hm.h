@@ -547,7 +547,9 @@ hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const uint16_t
  * gradient.  HM_ERR_SHAPE otherwise.  Codes may be any int8, scales any finite
  * fp32; a NaN or infinite scale makes its row (token) or column (channel) of
  * the results NaN or infinite and leaves the others alone, but where it is
- * summed over (hm_gemm_int8_grad) unspecified.  bf16 and int8 arrays and h are
+ * summed over (hm_gemm_int8_grad) unspecified.  ws: at least the bytes that the
+ * _workspace_size call names (NULL if 0), overwritten; calls that may run at the
+ * same time need one each.  bf16 and int8 arrays are
  * 16-byte aligned, scales 4-byte, ws 256-byte (HM_ERR_ALIGN).  No output nor ws
  * may overlap an input or another output (HM_ERR_UNSUPPORTED). */
 

@@ -86,6 +86,7 @@ TileArgs product(const int8_t* x8, const float* xs, const int8_t* w8, const floa
 // How a product runs: which tiles, and how the last ones are cut.
 struct Plan {
   bool few, big;
+  FewPlan fewer;
   TilePlan tiles;
   size_t part;               // workspace bytes of the cut tiles' sums
   int64_t ns;                // estimate of the time
@@ -95,17 +96,37 @@ struct Plan {
 // of 128 bytes (fitted to some 100 sizes from m = 16, n = 2048, k = 7168 to m = 4096, n = 14336, k = 4096, most
 // within 15 %): copies from L2 bound the small tiles, the conversion those that
 // turn codes into bf16, copies and the matrix cores the large ones.
+// Both take steps in twos.
 constexpr int kCus = 256;
-enum Operands { INT8, CODES, COPY };               // int8 products; gradients with P as codes, as a bf16 copy
+enum Operands { INT8, INT8_GRAD, CODES, COPY };    // int8 products, the gated gradient; gradients with P as codes, as a bf16 copy
 int64_t small_round(Operands o, int64_t tiles, int64_t steps) {
-  return steps * ((o == CODES ? 590 : 440) + 70 * tiles / kCus) + 2000 + 1700 * tiles / kCus;
+  return (steps + 1) / 2 * 2 * ((o == CODES ? 590 : 440) + 70 * tiles / kCus) + (o == INT8_GRAD ? 3400 : 2000) + 1700 * tiles / kCus;
 }
-int64_t big_round(int64_t tiles, int64_t steps) { return steps * (1070 + 380 * tiles / kCus) + 5500; }
-// Few rows: every block reads its weight rows and all of x, at about 40 bytes a
-// nanosecond a compute unit.
-int64_t few_rounds(int64_t rows, int64_t cols, bool pairs, int64_t k) {
-  const int64_t nb = i8_few_blocks(cols, pairs), blocks = div_up(cols, 16 * (pairs ? nb / 2 : nb));
-  return div_up(blocks, kCus) * k * 16 * (nb + div_up(rows, 16)) / 40;
+int64_t big_round(Operands o, int64_t tiles, int64_t steps) {
+  return (steps + 1) / 2 * 2 * (1070 + 380 * tiles / kCus) + (o == INT8_GRAD ? 12000 : 5500);
+}
+// Few rows: nanoseconds of the blocks one compute unit has, as many at a time as LDS takes.  A block reads
+// its weights at 40 bytes a nanosecond and its rows of x, which others have brought into L2, at 100,
+// and all of them no faster than the memory gives the weights (k = 6656, m = 11, n = 8256: three blocks of 16
+// weight rows a block 13.6 us, one 13.8, two, which leave two units with twice the work, 15.6, four 15.2).
+int64_t memory_time(int64_t cols, bool pairs, int64_t k) { return cols * (pairs ? 2 : 1) * k / 4900; }
+int64_t few_time(int64_t rows, int64_t cols, bool pairs, int64_t k, FewPlan& p) {
+  const int64_t blocks = div_up(rows, 16), least = div_up(blocks, 8), memory = memory_time(cols, pairs, k);
+  int64_t best = 0;
+  for (int64_t g = least; g <= 4 * least && g <= blocks; g *= 2) {
+    const int64_t mb = div_up(blocks, g), groups = div_up(blocks, mb), rb = std::min(16 * mb, rows);
+    for (int64_t nb = pairs ? 2 : 1; nb <= i8_few_most((int)mb, pairs); nb += pairs ? 2 : 1) {
+      const int64_t rounds = div_up(div_up(cols, 16 * (pairs ? nb / 2 : nb)) * groups, kCus);
+      const int64_t at_once = std::max<int64_t>(1, 160 / std::max(8 * (nb + mb), 4 * nb * mb));
+      const int64_t base = div_up(rounds, at_once) * (3300 + 200 * nb + 80 * nb * mb);
+      const int64_t t = std::max(rounds * (k * (nb * 40 + rb) / 100), memory) + base;
+      if (!best || t < best) {
+        best = t;
+        p = {(int)groups, (int)(16 * mb), (int)nb};
+      }
+    }
+  }
+  return best;
 }
 
 // kbytes: of the contraction, as the operands' rows hold it.
@@ -133,7 +154,7 @@ Plan plan_tiles(int64_t rows, int64_t cols, bool pairs, int64_t kbytes, Operands
   p.ns = best + tiles / kCus * small_round(o, kCus, steps);
   if (o == CODES) return p;                        // the large tiles take no codes
   const int64_t bigs = div_up(cols, pairs ? kI8Big / 2 : kI8Big) * div_up(rows, kI8Big);
-  const int64_t t = bigs / kCus * big_round(kCus, steps) + (bigs % kCus ? big_round(bigs % kCus, steps) : 0) + 1500;
+  const int64_t t = bigs / kCus * big_round(o, kCus, steps) + (bigs % kCus ? big_round(o, bigs % kCus, steps) : 0) + 1500;
   if (t < p.ns) {
     p.big = true;
     p.ns = t;
@@ -142,12 +163,14 @@ Plan plan_tiles(int64_t rows, int64_t cols, bool pairs, int64_t kbytes, Operands
   return p;
 }
 
-// An int8 product; grad: that of the gated gradient, which has no few-row kernel.
-Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t k, bool grad) {
-  Plan p = plan_tiles(rows, cols, pairs, k, INT8);
-  // (measured: the tiles' launches cost 4 us more than the few-row kernel's)
-  p.few = !grad && rows <= kI8Few && few_rounds(rows, cols, pairs, k) < p.ns + 4000;
-  if (p.few) p.part = 0;
+// An int8 product.
+Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t k, Operands o = INT8) {
+  Plan p = plan_tiles(rows, cols, pairs, k, o);
+  // (2300: a launch, which few_time counts and the tiles' estimates do not)
+  if (rows <= kI8Few && few_time(rows, cols, pairs, k, p.fewer) < std::max(p.ns, memory_time(cols, pairs, k) + 3000) + 2300) {
+    p.few = true;
+    p.part = 0;
+  }
   return p;
 }
 
@@ -160,7 +183,7 @@ Plan plan_gradient(int64_t rows, int64_t cols, int64_t kbytes, int64_t terms) {
 }
 
 hipError_t multiply(const TileArgs& a, const Plan& p, int kind, void* part, hipStream_t st) {
-  if (p.few) return launch_i8_few(a, kind, st);
+  if (p.few) return launch_i8_few(a, p.fewer, kind, st);
   if (p.big) return launch_i8_big(a, kind, st);
   TilePlan t = p.tiles;
   t.part = part;
@@ -212,7 +235,7 @@ HM_API hm_status hm_quant_int8_rows(const uint16_t* x, int64_t m, int64_t k, int
 HM_API hm_status hm_gemm_int8_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_sizes(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? plan_product(m, n, false, k, false).part : 0;
+  *bytes = m ? plan_product(m, n, false, k).part : 0;
   return HM_OK;
 }
 
@@ -224,7 +247,7 @@ HM_API hm_status hm_gemm_int8(const int8_t* x8, const float* x_scales, const int
   if (!x8 || !x_scales || !w8 || !w_scales || !y) return HM_ERR_NULL;
   if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(y, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const Plan p = plan_product(m, n, false, k, false);
+  const Plan p = plan_product(m, n, false, k);
   const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
@@ -247,7 +270,7 @@ hm_status check_gated(int64_t m, int64_t n, int64_t k) {
 HM_API hm_status hm_gemm_int8_gated_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_gated(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? plan_product(m, n / 2, true, k, false).part : 0;
+  *bytes = m ? plan_product(m, n / 2, true, k).part : 0;
   return HM_OK;
 }
 
@@ -259,7 +282,7 @@ HM_API hm_status hm_gemm_int8_gated(const int8_t* x8, const float* x_scales, con
   if (!x8 || !x_scales || !w8 || !w_scales || !h) return HM_ERR_NULL;
   if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(h, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const Plan p = plan_product(m, n / 2, true, k, false);
+  const Plan p = plan_product(m, n / 2, true, k);
   const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
@@ -274,7 +297,7 @@ HM_API hm_status hm_gemm_int8_gated(const int8_t* x8, const float* x_scales, con
 HM_API hm_status hm_gemm_int8_gated_grad_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (hm_status s = check_gated(m, n, k)) return s;
   if (!bytes) return HM_ERR_NULL;
-  *bytes = m ? plan_product(m, n / 2, true, k, true).part : 0;
+  *bytes = m ? plan_product(m, n / 2, true, k, INT8_GRAD).part : 0;
   return HM_OK;
 }
 
@@ -287,7 +310,7 @@ HM_API hm_status hm_gemm_int8_gated_grad(const uint16_t* dh, const int8_t* x8, c
   if (!aligned(dh, 16) || !aligned(x8, 16) || !aligned(w8, 16) || !aligned(dgu, 16) || !aligned(x_scales, 4) ||
       !aligned(w_scales, 4))
     return HM_ERR_ALIGN;
-  const Plan p = plan_product(m, n / 2, true, k, true);
+  const Plan p = plan_product(m, n / 2, true, k, INT8_GRAD);
   const size_t need = p.part;
   if (hm_status s = check_ws(ws, ws_bytes, need)) return s;
   const uint64_t um = m, un = n, uk = k;
@@ -383,7 +406,7 @@ namespace {
 
 int say(const Plan& p, bool pairs, int64_t rows, int64_t cols, char* buf, size_t len) {
   if (p.few)
-    return snprintf(buf, len, "few rows: row blocks %d, weight blocks %d", (int)div_up(rows, 16), i8_few_blocks(cols, pairs));
+    return snprintf(buf, len, "few rows: %d groups of %d row blocks, weight blocks %d", p.fewer.groups, p.fewer.rows / 16, p.fewer.nb);
   if (p.big) return snprintf(buf, len, "tiles 256x256: %lld", (long long)(div_up(rows, kI8Big) * div_up(cols, pairs ? kI8Big / 2 : kI8Big)));
   return snprintf(buf, len, "tiles 128x128%s: %d whole, %d in %d parts", p.tiles.codes ? " of codes" : "", p.tiles.full,
                   p.tiles.tiles_p * p.tiles.tiles_q - p.tiles.full, p.tiles.cut);
@@ -398,7 +421,7 @@ HM_API hm_status hm_gemm_int8_plan(int32_t op, int64_t m, int64_t n, int64_t k, 
   if (!buf || !buf_len) return HM_ERR_NULL;
   if (op != HM_INT8_GRAD) {
     if (m == 0) snprintf(buf, buf_len, "nothing");
-    else say(plan_product(m, pairs ? n / 2 : n, pairs, k, op == HM_INT8_GATED_GRAD), pairs, m, pairs ? n / 2 : n, buf, buf_len);
+    else say(plan_product(m, pairs ? n / 2 : n, pairs, k, op == HM_INT8_GATED_GRAD ? INT8_GRAD : INT8), pairs, m, pairs ? n / 2 : n, buf, buf_len);
     return HM_OK;
   }
   const GradPlan g = plan_grad(m, n, k);

@@ -48,16 +48,15 @@ hipError_t launch_i8_tile(const TileArgs& a, const TilePlan& pl, int kind, hipSt
 constexpr int kI8Big = 256;
 hipError_t launch_i8_big(const TileArgs& a, int kind, hipStream_t st);
 
-// Up to 64 rows, I8_FORWARD or I8_GATED: weights straight from global memory.
-constexpr int kI8Few = 64;
-hipError_t launch_i8_few(const TileArgs& a, int kind, hipStream_t st);
-// Blocks of 16 weight rows a wave takes: as many as leave most compute units a
-// block, since every block reads all of x (m = 64, k = 4096: n = 14336 with four 19 us, two 24, one 38; n =
-// 4096 with four 17.4, two 13.4, one 11.4).  Pairs of gate and up rows: two or four.
-inline int i8_few_blocks(int64_t cols, bool pairs) {
-  const int64_t blocks = (cols + 15) / 16 * (pairs ? 2 : 1);
-  return blocks >= 4 * 192 ? 4 : (pairs || blocks >= 2 * 192 ? 2 : 1);
-}
+// Products (not I8_DX, I8_DW) of up to kI8Few rows: blocks of a few weight rows against groups of up to 128 rows of x.
+constexpr int64_t kI8Few = 1024;
+struct FewPlan {
+  int groups, rows;          // groups, rows of each (but the last), a multiple of 16
+  int nb;                    // blocks of 16 weight rows (pairs: of gate and up) a block takes, 1 .. 4, pairs two or four
+};
+// The most blocks of weights a block takes: more share its rows of x, of which few rows have too little.
+constexpr int i8_few_most(int row_blocks, bool pairs) { return row_blocks >= 4 ? 4 : pairs || row_blocks == 1 ? 2 : 3; }
+hipError_t launch_i8_few(const TileArgs& a, const FewPlan& p, int kind, hipStream_t st);
 
 // bf16 rows -> int8 codes and fp32 scales
 hipError_t launch_i8_quant_rows(const uint16_t* x, int64_t m, int64_t k, int8_t* x8, float* s, hipStream_t st);

@@ -291,20 +291,17 @@ struct Codes {
   }
 };
 
-// Gate, up and the gradient of h to those of both, with sig = 1 / (1 + e^-g)
-// from e = e^-|g| <= 1, so that neither sig nor 1 - sig overflows or cancels.  The
-// exponential is taken as 2^(64 - |g| log2 e), which the hardware's leaves in the
-// normal range to |g| = 131, and scaled back by a product, which keeps subnormal
-// results (with e^-|g| itself dg of a gate of -88 was 0 for -1e-37).  Its error (the
-// rounding of an argument up to 64, 2^-18) and the reciprocal's stay far below the
+// Gate, up and the gradient of h to those of both, with sig = 1 / (1 + e^-g).  It is taken as 2^-64 /
+// (2^-64 + 2^(-64 - g log2 e)), whose terms stay in the normal range for g > -131 (with e^-g
+// itself dg of a gate of -88 was 0 for -1e-37); the last product, by 2^-64, keeps subnormal results.  sig
+// has no cancellation, and 1 - sig is off by less than a rounding of 1, which g (1 - sig) is added to.  The errors
+// of the exponential (the rounding of an argument up to 128, 2^-17) and of the reciprocal stay far below the
 // bf16 rounding of the results.
 __device__ __forceinline__ void gated_grad(float g, float u, float dh, float& dg, float& du) {
-  const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(-fabsf(g), 1.4426950408889634f, 64.0f)) * 0x1p-64f;
-  const float s = __builtin_amdgcn_rcpf(1.0f + e), es = e * s;
-  const bool pos = g >= 0.0f;
-  const float sig = pos ? s : es, rest = pos ? es : s;                 // sig and 1 - sig
-  du = dh * (g * sig);
-  dg = dh * u * (sig * __builtin_fmaf(g, rest, 1.0f));
+  const float sig = __builtin_amdgcn_rcpf(0x1p-64f + __builtin_amdgcn_exp2f(__builtin_fmaf(g, -1.4426950408889634f, -64.0f))) * 0x1p-64f;
+  const float t = g * sig;
+  du = dh * t;
+  dg = dh * u * __builtin_fmaf(t, 1.0f - sig, sig);
 }
 
 // Eight bf16 values of a row at any 2-byte address (rows of an odd number of

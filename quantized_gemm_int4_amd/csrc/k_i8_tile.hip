@@ -9,10 +9,15 @@
 // of the contraction by 16-byte direct buffer-to-LDS copies; reads past an
 // array give zeros, so no size has to be padded.  Gradients of few tiles read
 // their int8 operand (weights for dx, rows of x for dw) as it is and turn it into bf16
-// between the MFMAs (a step of 0.75 us for 0.48, but no bf16 copy of the operand to make
-// first: m = 128, n = 14336, k = 4096 dx 35 us for 60; m = 1024 184 for 151).  During step s its operands are
+// between the MFMAs (a step of 0.66 us for 0.51 on a full card, but no bf16 copy of the operand to make
+// first: m = 128, n = 14336, k = 4096 dx 33 us for 63; m = 1024 161 for 145).  During step s its operands are
 // in registers, those of step s + 1 are read from LDS between the MFMAs, and four
-// stages hold steps s + 1 .. s + 4, so that a copy has three steps to land.
+// stages hold steps s + 1 .. s + 4, so that a copy has three steps to land.  A fifth wave
+// touches later steps' lines (Ahead; product of m = 1021, n = 4099, k = 7168 58 us without it, 44 with).
+//
+// Against the 256 x 256 tiles: int8 product m = 1024, n = 7168, k = 2048 22.6 us for 28.4, m = 2048 44 for 33.
+// What bounds a step is the copies' 32 KiB from L2: at the 64 bytes a clock that a compute unit takes, 0.22 us, and
+// twice that with all of them at it.
 //
 // Tiles that do not fill the card's 256 compute units in a last round (or all of
 // them, where there are fewer) are split along the contraction: `cut` blocks a

@@ -103,7 +103,9 @@ hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void** args, si
   } else if (name.find("k_i8_few") != name.npos) {
     const auto& a = *static_cast<hm::TileArgs*>(args[0]);
     need(a.rows >= 1 && a.rows <= hm::kI8Few && a.kbytes % 128 == 0 && a.p_ld == a.kbytes, "few rows");
-    need((uint64_t)a.rows * a.kbytes < (1ull << 32), "x in 32 bits");
+    const int64_t total = *static_cast<uint32_t*>(args[1]), groups = *static_cast<int*>(args[2]), per = *static_cast<int*>(args[3]);
+    need(per % 16 == 0 && per <= 128 && groups * per >= a.rows && (groups - 1) * per < a.rows, "groups of rows, none empty");
+    need(grid.x % 8 == 0 && (int64_t)grid.x >= total && total % groups == 0 && total / groups * 64 >= a.cols, "blocks of the groups");
   } else if (name.find("k_i8_dequant") != name.npos) {
     const int64_t rows = *static_cast<int64_t*>(args[2]), kc = *static_cast<int64_t*>(args[3]);
     g_copy = (uintptr_t)*static_cast<uint16_t**>(args[4]);
@@ -177,7 +179,7 @@ static void call(int64_t m, int64_t n, int64_t k) {
 }
 
 int main() {
-  for (int64_t m : {0, 1, 16, 64, 65, 8388480})
+  for (int64_t m : {0, 1, 16, 64, 65, 1024, 1025, 8388480})
     for (int64_t n : {1, 2, 255, 1 << 22})
       for (int64_t k : {128, 130944}) call(m, n, k);
   for (int i = 0; i < 60000; ++i) call(draw(0, 9000000), draw(1, (1 << 22) + 100), 128 * draw(1, 1024));
@@ -191,10 +193,9 @@ int main() {
   }
   long total = 0;
   for (const auto& k : g_launches) total += k.second;
-  for (const auto& k : names()) {
+  for (const auto& k : names())
     if (!g_launches.count(k.second)) printf("never launched: %s\n", k.second.c_str());
-    need(g_launches.count(k.second) != 0, "a kernel that no call reaches");
-  }
+  need(g_launches.size() == names().size(), "kernels that no call reaches");
   printf("int8 sweep ok: %ld launches of %zu kernels\n", total, g_launches.size());
   return 0;
 }

@@ -34,12 +34,40 @@ def _close(got, ref, lim, what):
     assert not bool(bad.any()), (what, int(bad.sum()), bad.nonzero()[:3].tolist(), got[bad][:3].tolist(), ref[bad][:3].tolist())
 
 
-FORWARD = [
-    (16, 700, 128, "few rows: row blocks 1, weight blocks 1"), (17, 7001, 384, "few rows: row blocks 2, weight blocks 2"),
-    (40, 13003, 128, "few rows: row blocks 3, weight blocks 4"), (64, 12400, 640, "few rows: row blocks 4, weight blocks 4"),
-    (9, 12288, 256, "few rows: row blocks 1, weight blocks 4"), (33, 6200, 384, "few rows: row blocks 3, weight blocks 2"),
-    (300, 700, 128, "whole, 0 in 1"), (1000, 4100, 640, "264 whole, 0 in 1"), (150, 600, 4096, "0 whole, 10 in"),
-    (1021, 4099, 7168, "256 whole, 8 in"), (520, 300, 8320, "0 whole, 15 in"),
+# every kernel for few rows: row blocks (of one group), weight blocks, one block or several to a compute unit
+FEW = [
+    (1, 4129, 128, "1 groups of 1 row blocks, weight blocks 1"), (1, 2, 384, "1 groups of 1 row blocks, weight blocks 1"),
+    (11, 4222, 2560, "1 groups of 1 row blocks, weight blocks 2"), (43, 2093, 128, "2 groups of 2 row blocks, weight blocks 1"),
+    (35, 1, 128, "2 groups of 2 row blocks, weight blocks 1"), (66, 12359, 128, "3 groups of 2 row blocks, weight blocks 2"),
+    (19, 4131, 1920, "1 groups of 2 row blocks, weight blocks 2"), (196, 6275, 128, "7 groups of 2 row blocks, weight blocks 3"),
+    (30, 8481, 2304, "1 groups of 2 row blocks, weight blocks 3"), (33, 4135, 128, "1 groups of 3 row blocks, weight blocks 1"),
+    (33, 2082, 128, "1 groups of 3 row blocks, weight blocks 1"), (129, 6842, 128, "3 groups of 3 row blocks, weight blocks 2"),
+    (46, 4097, 1024, "1 groups of 3 row blocks, weight blocks 2"), (169, 8255, 128, "4 groups of 3 row blocks, weight blocks 3"),
+    (46, 8374, 1024, "1 groups of 3 row blocks, weight blocks 3"), (51, 10317, 128, "1 groups of 4 row blocks, weight blocks 1"),
+    (49, 2094, 384, "1 groups of 4 row blocks, weight blocks 1"), (97, 10515, 128, "2 groups of 4 row blocks, weight blocks 2"),
+    (59, 4237, 896, "1 groups of 4 row blocks, weight blocks 2"), (638, 2446, 640, "10 groups of 4 row blocks, weight blocks 3"),
+    (115, 4107, 896, "2 groups of 4 row blocks, weight blocks 3"), (289, 5894, 128, "5 groups of 4 row blocks, weight blocks 4"),
+    (294, 2831, 1664, "5 groups of 4 row blocks, weight blocks 4"), (65, 6873, 128, "1 groups of 5 row blocks, weight blocks 1"),
+    (65, 2771, 256, "1 groups of 5 row blocks, weight blocks 1"), (65, 13037, 256, "1 groups of 5 row blocks, weight blocks 2"),
+    (79, 4105, 768, "1 groups of 5 row blocks, weight blocks 2"), (147, 10159, 128, "2 groups of 5 row blocks, weight blocks 3"),
+    (69, 8558, 896, "1 groups of 5 row blocks, weight blocks 3"), (129, 12314, 128, "2 groups of 5 row blocks, weight blocks 4"),
+    (133, 6345, 1664, "2 groups of 5 row blocks, weight blocks 4"), (97, 6263, 256, "1 groups of 7 row blocks, weight blocks 1"),
+    (97, 3105, 384, "1 groups of 7 row blocks, weight blocks 1"), (98, 12297, 128, "1 groups of 7 row blocks, weight blocks 2"),
+    (101, 4103, 768, "1 groups of 7 row blocks, weight blocks 2"), (99, 8254, 640, "1 groups of 7 row blocks, weight blocks 3"),
+    (202, 6265, 1408, "2 groups of 7 row blocks, weight blocks 4")]
+FEW_GATED = [
+    (1, 4117, 128, "1 groups of 1 row blocks, weight blocks 2"), (1, 1, 256, "1 groups of 1 row blocks, weight blocks 2"),
+    (33, 2257, 128, "2 groups of 2 row blocks, weight blocks 2"), (65, 1, 128, "3 groups of 2 row blocks, weight blocks 2"),
+    (34, 6413, 128, "1 groups of 3 row blocks, weight blocks 2"), (33, 2063, 256, "1 groups of 3 row blocks, weight blocks 2"),
+    (49, 10251, 128, "1 groups of 4 row blocks, weight blocks 2"), (49, 2171, 384, "1 groups of 4 row blocks, weight blocks 2"),
+    (50, 12461, 128, "1 groups of 4 row blocks, weight blocks 4"), (51, 4157, 2048, "1 groups of 4 row blocks, weight blocks 4"),
+    (65, 4237, 384, "1 groups of 5 row blocks, weight blocks 2"), (68, 2727, 384, "1 groups of 5 row blocks, weight blocks 2"),
+    (65, 10067, 128, "1 groups of 5 row blocks, weight blocks 4"), (75, 4137, 1664, "1 groups of 5 row blocks, weight blocks 4"),
+    (194, 3075, 128, "2 groups of 7 row blocks, weight blocks 2"), (97, 2275, 512, "1 groups of 7 row blocks, weight blocks 2"),
+    (204, 2185, 1408, "2 groups of 7 row blocks, weight blocks 4")]
+FORWARD = FEW + [
+    (1030, 700, 128, "54 whole, 0 in 1"), (1000, 4100, 640, "264 whole, 0 in 1"), (1050, 600, 4096, "0 whole, 45 in 4"),
+    (1021, 4099, 7168, "256 whole, 8 in"), (1100, 300, 8320, "0 whole, 27 in 5"),
     (2000, 5201, 256, "256x256: 168"), (2100, 9002, 384, "256x256: 324"), (4097, 5000, 128, "256x256: 340"),
     (2049, 7169, 2176, "128x128: 969 whole"), (2305, 7000, 1152, "256x256: 280")]
 
@@ -58,17 +86,16 @@ def test_product(m, n, k, plan):
     assert torch.equal(again, y[:m])
 
 
-GATED = [(16, 7000, 256, "few rows: row blocks 1, weight blocks 4"), (50, 1100, 384, "few rows: row blocks 4, weight blocks 2"),
-         (300, 350, 128, "whole, 0 in 1"), (150, 300, 4096, "0 whole, 10 in"), (1021, 2049, 7168, "256 whole, 8 in"),
-         (2000, 2601, 256, "256x256: 168"), (2100, 4501, 384, "256x256: 324")]
+GATED = FEW_GATED + [
+         (1030, 350, 128, "54 whole, 0 in 1"), (1050, 300, 4096, "0 whole, 45 in 4"), (1021, 2049, 7168, "256 whole, 8 in"),
+         (2000, 2601, 256, "256x256: 168"), (1090, 9985, 256, "256x256: 395")]
 
 
 @pytest.mark.parametrize("m,d,k,plan", GATED)
 def test_gated_and_its_gradient(m, d, k, plan):
     import quantized_gemm_int4_amd as hm
     assert plan in hm.hm_gemm_int8_plan(hm.HM_INT8_GATED, m, 2 * d, k)
-    if "few" not in plan:
-        assert plan in hm.hm_gemm_int8_plan(hm.HM_INT8_GATED_GRAD, m, 2 * d, k)
+    assert plan in hm.hm_gemm_int8_plan(hm.HM_INT8_GATED_GRAD, m, 2 * d, k)
     a, rows = _layer(m + d + k, m, 2 * d, k)
     g, u = _product(a).chunk(2, 1)
     s, rest = torch.sigmoid(g), torch.sigmoid(-g)
