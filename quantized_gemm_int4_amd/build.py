@@ -16,7 +16,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libhm.so")
 SOURCES = ["k_weights.hip", "k_fp8.hip", "k_moe.hip", "k_rows.hip", "k_lora.hip", "k_lora_grad.hip", "k_gemm_stream.hip", "k_gemm_tile.hip",
-           "k_gemm_mid.hip", "k_gemm_big.hip", "k_block.hip", "k_i8_rows.hip", "k_i8_tile.hip", "k_i8_big.hip", "k_i8_few.hip", "plan_host.cpp", "hm_api.cpp", "hm_api_rows.cpp",
+           "k_gemm_mid.hip", "k_gemm_big.hip", "k_block.hip", "k_i8_rows.hip", "k_i8_tile.hip", "k_i8_big.hip", "k_i8_few.hip", "k_i8_few_dx.hip", "plan_host.cpp", "hm_api.cpp", "hm_api_rows.cpp",
            "hm_api_lora.cpp", "hm_api_i8.cpp"]
 ARCH = "gfx950"
 

@@ -87,6 +87,7 @@ TileArgs product(const int8_t* x8, const float* xs, const int8_t* w8, const floa
 struct Plan {
   bool few, big;
   FewPlan fewer;
+  int few_dx;                // rows of a group of the kernel for few rows of a gradient, 0: tiles
   TilePlan tiles;
   size_t part;               // workspace bytes of the cut tiles' sums
   int64_t ns;                // estimate of the time
@@ -174,6 +175,21 @@ Plan plan_product(int64_t rows, int64_t cols, bool pairs, int64_t k, Operands o 
   return p;
 }
 
+// dx of few rows: groups of 32, 64 or 128 rows, of which a compute unit takes steps of 64 of the contraction in so
+// many nanoseconds.
+int64_t few_dx_time(int64_t rows, int64_t cols, int64_t kbytes, int& group) {
+  int64_t best = 0;
+  for (int r = 32; r <= 128; r *= 2) {
+    const int64_t n = cols / 64 * div_up(rows, r), c = r == 32 ? 155 : r == 64 ? 190 : 260 + 160 * std::min<int64_t>(n, kCus) / kCus;
+    const int64_t t = div_up(n, kCus) * (div_up(kbytes, 128) * c + (r == 32 ? 1000 : 3000)) + 3500;
+    if (!best || t < best) {
+      best = t;
+      group = r;
+    }
+  }
+  return best;
+}
+
 // One of the gradients: `terms` rows of the int8 operand, [terms][cols].
 Plan plan_gradient(int64_t rows, int64_t cols, int64_t kbytes, int64_t terms) {
   const Plan codes = plan_tiles(rows, cols, false, kbytes, CODES);
@@ -184,6 +200,7 @@ Plan plan_gradient(int64_t rows, int64_t cols, int64_t kbytes, int64_t terms) {
 
 hipError_t multiply(const TileArgs& a, const Plan& p, int kind, void* part, hipStream_t st) {
   if (p.few) return launch_i8_few(a, p.fewer, kind, st);
+  if (p.few_dx) return launch_i8_few_dx(a, p.few_dx, st);
   if (p.big) return launch_i8_big(a, kind, st);
   TilePlan t = p.tiles;
   t.part = part;
@@ -208,6 +225,12 @@ GradPlan plan_grad(int64_t m, int64_t n, int64_t k) {
   g.dw = plan_gradient(n, k, 2 * m, m);
   if (m == 0) return g;
   g.dx = plan_gradient(m, k, 2 * (g.np ? g.np : n), n);
+  int group = 0;
+  if (m <= 2 * kI8Few && few_dx_time(m, k, 2 * n, group) < g.dx.ns + 2300) {
+    g.dx.few_dx = group;
+    g.dx.tiles.codes = 1;
+    g.dx.part = 0;
+  }
   g.dyp = take((size_t)m * (size_t)g.np * 2);
   g.w = take(!g.dx.tiles.codes ? (size_t)n * (size_t)k * 2 : 0);
   g.x = take(!g.dw.tiles.codes ? (size_t)m * (size_t)k * 2 : 0);
@@ -362,40 +385,50 @@ HM_API hm_status hm_gemm_int8_grad(const uint16_t* dy, const int8_t* x8, const f
               {{dy, 2 * um * un}, {x8, um * uk}, {x_scales, 4 * um}, {w8, un * uk}, {w_scales, 4 * un}}))
     return HM_ERR_UNSUPPORTED;
   uint8_t* at = (uint8_t*)ws;
-  hipError_t e = hipSuccess;
-  const uint16_t* dyp = dy;
+  // what the products read in place of the arguments, in one launch
+  I8Copies c{};
+  c.kc = k / 16;
+  c.dy = dy;
+  c.pad = (uint16_t*)(at + g.dyp);
+  c.m = m;
+  c.n = n;
+  c.nc = g.np / 8;
+  auto copy = [&](int i, const int8_t* q, const float* s, int64_t rows, size_t to) {
+    c.q[i] = q;
+    c.s[i] = s;
+    c.rows[i] = rows;
+    c.out[i] = (uint16_t*)(at + to);
+  };
+  if (dx && m && !g.dx.tiles.codes) copy(0, w8, w_scales, n, g.w);
+  if (dw && !g.dw.tiles.codes) copy(1, x8, x_scales, m, g.x);
+  hipError_t e = launch_i8_copies(c, stream);
   const int64_t ldy = g.np ? g.np : n;
-  if (g.np && m) {
-    dyp = (const uint16_t*)(at + g.dyp);
-    e = launch_i8_pad_rows(dy, m, n, g.np, (uint16_t*)(at + g.dyp), stream);
-  }
-  a.q = (const uint8_t*)dyp;
+  a.q = g.np && m ? (const uint8_t*)c.pad : (const uint8_t*)dy;
   a.q_ld = 2 * ldy;
   a.q_bytes = 2 * m * ldy;
   a.cols = k;
-  // P: the int8 operand, as codes or as a bf16 copy
-  auto side = [&](const Plan& p, const int8_t* q8, const float* scales, int64_t rows, size_t copy) {
+  // P: the int8 operand, as codes or as its bf16 copy
+  auto side = [&](const Plan& p, const int8_t* q8, const float* scales, int64_t rows, size_t to) {
     const bool codes = p.tiles.codes;
-    a.p = codes ? (const uint8_t*)q8 : at + copy;
+    a.p = codes ? (const uint8_t*)q8 : at + to;
     a.p_ld = (codes ? 1 : 2) * k;
     a.p_bytes = rows * a.p_ld;
     a.ps = scales;
     a.terms = rows;
-    if (!codes && rows && e == hipSuccess) e = launch_i8_dequant_rows(q8, scales, rows, k, (uint16_t*)(at + copy), stream);
   };
-  if (dx && m) {
+  if (dx && m && e == hipSuccess) {
     side(g.dx, w8, w_scales, n, g.w);
     a.rows = m;
     a.kbytes = 2 * ldy;
     a.out = dx;
-    if (e == hipSuccess) e = multiply(a, g.dx, I8_DX, at + g.part, stream);
+    e = multiply(a, g.dx, I8_DX, at + g.part, stream);
   }
-  if (dw) {
+  if (dw && e == hipSuccess) {
     side(g.dw, x8, x_scales, m, g.x);
     a.rows = n;
     a.kbytes = 2 * m;
     a.out = dw;
-    if (e == hipSuccess) e = multiply(a, g.dw, I8_DW, at + g.part, stream);
+    e = multiply(a, g.dw, I8_DW, at + g.part, stream);
   }
   return done(e);
 }
@@ -407,6 +440,7 @@ namespace {
 int say(const Plan& p, bool pairs, int64_t rows, int64_t cols, char* buf, size_t len) {
   if (p.few)
     return snprintf(buf, len, "few rows: %d groups of %d row blocks, weight blocks %d", p.fewer.groups, p.fewer.rows / 16, p.fewer.nb);
+  if (p.few_dx) return snprintf(buf, len, "few rows: groups of %d", p.few_dx);
   if (p.big) return snprintf(buf, len, "tiles 256x256: %lld", (long long)(div_up(rows, kI8Big) * div_up(cols, pairs ? kI8Big / 2 : kI8Big)));
   return snprintf(buf, len, "tiles 128x128%s: %d whole, %d in %d parts", p.tiles.codes ? " of codes" : "", p.tiles.full,
                   p.tiles.tiles_p * p.tiles.tiles_q - p.tiles.full, p.tiles.cut);

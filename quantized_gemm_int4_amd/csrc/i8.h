@@ -58,11 +58,22 @@ struct FewPlan {
 constexpr int i8_few_most(int row_blocks, bool pairs) { return row_blocks >= 4 ? 4 : pairs || row_blocks == 1 ? 2 : 3; }
 hipError_t launch_i8_few(const TileArgs& a, const FewPlan& p, int kind, hipStream_t st);
 
+// I8_DX for few rows, P as codes: blocks of 64 columns against groups of `rows` rows (32, 64 or 128)
+hipError_t launch_i8_few_dx(const TileArgs& a, int rows, hipStream_t st);
+
 // bf16 rows -> int8 codes and fp32 scales
 hipError_t launch_i8_quant_rows(const uint16_t* x, int64_t m, int64_t k, int8_t* x8, float* s, hipStream_t st);
-// int8 rows -> bf16(scale * code), [rows][k], k a multiple of 16
-hipError_t launch_i8_dequant_rows(const int8_t* q, const float* s, int64_t rows, int64_t k, uint16_t* out, hipStream_t st);
-// bf16 rows of n values -> rows of np >= n (a multiple of 8), zeros behind
-hipError_t launch_i8_pad_rows(const uint16_t* x, int64_t rows, int64_t n, int64_t np, uint16_t* out, hipStream_t st);
+// Copies for a gradient: two arrays of int8 rows of 16 kc codes -> bf16(scale * code), none where rows = 0, and m rows
+// of n bf16 values -> rows of 8 nc >= n, zeros behind, none where nc = 0.
+struct I8Copies {
+  const int8_t* q[2];
+  const float* s[2];
+  uint16_t* out[2];
+  int64_t rows[2], kc;
+  const uint16_t* dy;
+  uint16_t* pad;
+  int64_t m, n, nc;
+};
+hipError_t launch_i8_copies(const I8Copies& c, hipStream_t st);
 
 }  // namespace hm

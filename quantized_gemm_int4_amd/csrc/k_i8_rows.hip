@@ -1,6 +1,6 @@
 // Rows of the 8-bit integer layers: quantization per token (the codes that the
 // product multiplies, and what a training step keeps of its activations), the
-// bf16 form of 8-bit rows for the gradients, and padded copies of odd rows.
+// copies that the gradients need (bf16 forms of 8-bit rows, padded odd rows).
 #include <hip/hip_runtime.h>
 
 #include "common.h"
@@ -163,33 +163,31 @@ hipError_t launch_i8_quant_rows(const uint16_t* x, int64_t m, int64_t k, int8_t*
 
 namespace {
 
-// bf16(scale * code): one rounding of the fp32 product, 16 codes a thread.
+// The copies that a gradient needs, in one launch.  Codes: bf16(scale * code), one
+// rounding of the fp32 product, 16 a thread.  Rows of n values into rows of 8 nc, zeros behind: eight a thread.
 __global__ void __launch_bounds__(256)
-k_i8_dequant_rows(const int8_t* __restrict__ q, const float* __restrict__ s, int64_t rows, int64_t kc,
-                  uint16_t* __restrict__ out) {
-  const int64_t n = rows * kc;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const float sc = s[i / kc];
-    const u32x4_t v = ld16(q + 16 * i);
-    st16(out + 16 * i, i8x8_bf16_scaled(v[0], v[1], sc));
-    st16(out + 16 * i + 8, i8x8_bf16_scaled(v[2], v[3], sc));
-  }
-}
-
-// Rows of n values into rows of np, zeros behind: eight values a thread.
-__global__ void __launch_bounds__(256)
-k_i8_pad_rows(const uint16_t* __restrict__ x, int64_t rows, int64_t n, int64_t nc, uint16_t* __restrict__ out) {
-  const int64_t total = rows * nc;
+k_i8_copies(I8Copies c) {
+  const int64_t n0 = c.rows[0] * c.kc, n1 = n0 + c.rows[1] * c.kc, total = n1 + c.m * c.nc;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / nc, c = (i - row * nc) * 8;
-    const uint16_t* xr = x + row * n;
-    u32x4_t v;
+    if (i < n1) {
+      const int w = i >= n0;
+      const int64_t at = w ? i - n0 : i;
+      const float sc = (w ? c.s[1] : c.s[0])[at / c.kc];
+      const u32x4_t v = ld16((w ? c.q[1] : c.q[0]) + 16 * at);
+      uint16_t* out = (w ? c.out[1] : c.out[0]) + 16 * at;
+      st16(out, i8x8_bf16_scaled(v[0], v[1], sc));
+      st16(out + 8, i8x8_bf16_scaled(v[2], v[3], sc));
+    } else {
+      const int64_t at = i - n1, row = at / c.nc, col = (at - row * c.nc) * 8;
+      const uint16_t* xr = c.dy + row * c.n;
+      u32x4_t v;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = c + 2 * j < n ? xr[c + 2 * j] : 0u, hi = c + 2 * j + 1 < n ? xr[c + 2 * j + 1] : 0u;
-      v[j] = lo | (hi << 16);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = col + 2 * j < c.n ? xr[col + 2 * j] : 0u, hi = col + 2 * j + 1 < c.n ? xr[col + 2 * j + 1] : 0u;
+        v[j] = lo | (hi << 16);
+      }
+      st16(c.pad + 8 * at, v);
     }
-    st16(out + 8 * i, v);
   }
 }
 
@@ -200,14 +198,10 @@ unsigned blocks_for(int64_t threads) {
 
 }  // namespace
 
-hipError_t launch_i8_dequant_rows(const int8_t* q, const float* s, int64_t rows, int64_t k, uint16_t* out, hipStream_t st) {
-  const int64_t kc = k / 16;
-  hipLaunchKernelGGL(k_i8_dequant_rows, dim3(blocks_for(rows * kc)), dim3(256), 0, st, q, s, rows, kc, out);
-  return hipGetLastError();
-}
-
-hipError_t launch_i8_pad_rows(const uint16_t* x, int64_t rows, int64_t n, int64_t np, uint16_t* out, hipStream_t st) {
-  hipLaunchKernelGGL(k_i8_pad_rows, dim3(blocks_for(rows * (np / 8))), dim3(256), 0, st, x, rows, n, np / 8, out);
+hipError_t launch_i8_copies(const I8Copies& c, hipStream_t st) {
+  const int64_t threads = (c.rows[0] + c.rows[1]) * c.kc + c.m * c.nc;
+  if (!threads) return hipSuccess;
+  hipLaunchKernelGGL(k_i8_copies, dim3(blocks_for(threads)), dim3(256), 0, st, c);
   return hipGetLastError();
 }
 

@@ -22,7 +22,8 @@ static std::map<const void*, std::string>& names() {
   return m;
 }
 static std::map<std::string, long> g_launches;
-static uintptr_t g_ws = 0, g_ws_end = 0, g_copy = 0, g_copy_end = 0, g_pad = 0, g_pad_end = 0;
+static uintptr_t g_ws = 0, g_ws_end = 0;
+static struct { uintptr_t from, to; } g_copies[3];
 static char g_what[256] = "";
 
 static void need(bool ok, const char* what) {
@@ -49,7 +50,7 @@ static void check_tile(const std::string& name, const hm::TileArgs& a, const hm:
   if (rest) {
     const uintptr_t p = (uintptr_t)pl.part, e = p + (uint64_t)rest * pl.cut * 65536;
     need(in_ws(p, e - p), "parts in the workspace");
-    need(apart(p, e, g_copy, g_copy_end) && apart(p, e, g_pad, g_pad_end), "parts apart from the copies");
+    for (const auto& c : g_copies) need(apart(p, e, c.from, c.to), "parts apart from the copies");
   }
 }
 static void check_operand(const hm::TileArgs& a) {
@@ -100,22 +101,31 @@ hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3 block, void** args, si
     check_operand(a);
     need(grid.x % 8 == 0 && grid.x <= 256 && (int64_t)tp * tq >= 1 && (int64_t)tq * 256 >= a.rows, "256 x 256 tiles");
     need(grid.x == 256 || grid.x >= (unsigned)(tp * tq), "a block for every tile");
+  } else if (name.find("k_i8_few_dx") != name.npos) {
+    const auto& a = *static_cast<hm::TileArgs*>(args[0]);
+    const int64_t total = *static_cast<uint32_t*>(args[1]), groups = *static_cast<int*>(args[2]);
+    check_operand(a);
+    need(a.p_ld == a.cols && a.cols % 64 == 0 && a.terms * a.cols == a.p_bytes, "codes of the weights");
+    need(groups * 128 >= a.rows && (groups - 1) * 32 < a.rows && total == a.cols / 64 * groups && grid.x >= total, "groups of rows");
   } else if (name.find("k_i8_few") != name.npos) {
     const auto& a = *static_cast<hm::TileArgs*>(args[0]);
     need(a.rows >= 1 && a.rows <= hm::kI8Few && a.kbytes % 128 == 0 && a.p_ld == a.kbytes, "few rows");
     const int64_t total = *static_cast<uint32_t*>(args[1]), groups = *static_cast<int*>(args[2]), per = *static_cast<int*>(args[3]);
     need(per % 16 == 0 && per <= 128 && groups * per >= a.rows && (groups - 1) * per < a.rows, "groups of rows, none empty");
     need(grid.x % 8 == 0 && (int64_t)grid.x >= total && total % groups == 0 && total / groups * 64 >= a.cols, "blocks of the groups");
-  } else if (name.find("k_i8_dequant") != name.npos) {
-    const int64_t rows = *static_cast<int64_t*>(args[2]), kc = *static_cast<int64_t*>(args[3]);
-    g_copy = (uintptr_t)*static_cast<uint16_t**>(args[4]);
-    g_copy_end = g_copy + rows * kc * 32;
-    need(rows >= 1 && kc >= 8 && in_ws(g_copy, g_copy_end - g_copy) && apart(g_copy, g_copy_end, g_pad, g_pad_end), "copy in the workspace");
-  } else if (name.find("k_i8_pad") != name.npos) {
-    const int64_t rows = *static_cast<int64_t*>(args[1]), n = *static_cast<int64_t*>(args[2]), nc = *static_cast<int64_t*>(args[3]);
-    g_pad = (uintptr_t)*static_cast<uint16_t**>(args[4]);
-    g_pad_end = g_pad + rows * nc * 16;
-    need(rows >= 1 && nc * 8 >= n && nc * 8 < n + 8 && in_ws(g_pad, g_pad_end - g_pad), "padded rows in the workspace");
+  } else if (name.find("k_i8_copies") != name.npos) {
+    const auto& c = *static_cast<hm::I8Copies*>(args[0]);
+    uintptr_t from[3] = {(uintptr_t)c.out[0], (uintptr_t)c.out[1], (uintptr_t)c.pad}, to[3];
+    for (int i = 0; i < 2; ++i) to[i] = from[i] + c.rows[i] * c.kc * 32;
+    to[2] = from[2] + c.m * c.nc * 16;
+    need(c.nc == 0 || (c.nc * 8 >= c.n && c.nc * 8 < c.n + 8), "padded rows");
+    need(c.rows[0] >= 0 && c.rows[1] >= 0 && c.kc >= 8 && (to[0] > from[0] || to[1] > from[1] || to[2] > from[2]), "something to copy");
+    for (int i = 0; i < 3; ++i) {
+      if (to[i] == from[i]) continue;
+      need(in_ws(from[i], to[i] - from[i]), "copy in the workspace");
+      g_copies[i] = {from[i], to[i]};
+      for (int j = 0; j < i; ++j) need(to[j] == from[j] || apart(from[i], to[i], from[j], to[j]), "copies apart");
+    }
   }
   return hipSuccess;
 }
@@ -154,7 +164,7 @@ static void call(int64_t m, int64_t n, int64_t k) {
   auto run = [&](hm_status expect, hm_status query, int op, auto&& go) {
     need(query == expect, "size query");
     need(hm_gemm_int8_plan(op, m, n, k, text, sizeof text) == expect, "plan");
-    g_copy = g_copy_end = g_pad = g_pad_end = 0;
+    memset(g_copies, 0, sizeof g_copies);
     g_ws_end = g_ws + bytes;
     need(go(bytes) == expect, "call");
     if (bytes && expect == HM_OK) need(go(bytes - 1) == HM_ERR_WORKSPACE, "a byte less");

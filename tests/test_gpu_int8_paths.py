@@ -114,7 +114,10 @@ def test_gated_and_its_gradient(m, d, k, plan):
     assert bool((h[m] == 7).all()) and bool((out[m] == 7).all())
 
 
-GRAD = [(100, 300, 256, "dx tiles 128x128 of codes", "dw tiles 128x128 of codes"), (520, 4096, 384, "of codes: 0 whole, 15 in", "of codes"),
+GRAD = [(100, 300, 256, "dx few rows: groups of 32", "dw tiles 128x128 of codes"), (1, 7, 128, "dx few rows: groups of 32", "of codes"),
+        (1100, 4096, 384, "dx few rows: groups of 32", "of codes"), (333, 7168, 2048, "dx few rows: groups of 64", "dw tiles 256x256: 224"),
+        (244, 2065, 3840, "dx few rows: groups of 64", "of codes"), (851, 3968, 1792, "dx few rows: groups of 128", "dw tiles 128x128: 434"),
+        (361, 2405, 4224, "dx few rows: groups of 128", "dw tiles 256x256: 170"), (300, 6000, 640, "of codes: 0 whole, 15 in", "of codes"),
         (1500, 6000, 2048, "dx tiles 128x128: 192 whole", "dw tiles 256x256: 192"),
         (3000, 5003, 1024, "dx tiles 128x128: 192 whole", "dw tiles 128x128: 256 whole, 64 in 3"),
         (4096, 4100, 1152, "dx tiles 128x128: 256 whole, 32 in", "dw tiles 128x128: 256 whole, 41 in"),

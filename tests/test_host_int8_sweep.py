@@ -11,7 +11,7 @@ import pytest
 
 from test_host_sanitize import CSRC, HOST_SAN, ROOT, _tools
 
-SOURCES = ["hm_api_i8.cpp", "k_i8_rows.hip", "k_i8_tile.hip", "k_i8_big.hip", "k_i8_few.hip"]
+SOURCES = ["hm_api_i8.cpp", "k_i8_rows.hip", "k_i8_tile.hip", "k_i8_big.hip", "k_i8_few.hip", "k_i8_few_dx.hip"]
 
 
 @pytest.mark.parametrize("san", [False, True])
