@@ -103,8 +103,16 @@ enum Operands { INT8, INT8_GRAD, CODES, COPY };    // int8 products, the gated g
 int64_t small_round(Operands o, int64_t tiles, int64_t steps) {
   return (steps + 1) / 2 * 2 * ((o == CODES ? 590 : 440) + 70 * tiles / kCus) + (o == INT8_GRAD ? 3400 : 2000) + 1700 * tiles / kCus;
 }
+// Two blocks a compute unit, up to 512 tiles at once: the start and the end of one go with the other's steps, but each
+// has only half of the copies on their way.
+int64_t two_round(Operands o, int64_t tiles, int64_t steps) {
+  const int64_t one = std::min<int64_t>(tiles, kCus), more = tiles - one, grad = o == INT8_GRAD;
+  const int64_t step = o == CODES ? (more ? 930 + 170 * more / kCus : 600 + 160 * one / kCus)
+                                  : (more ? 830 + 150 * more / kCus : 500 + 130 * one / kCus);
+  return (steps + 1) / 2 * 2 * step + 1700 + 1400 * grad + (1700 * one + (200 + 1600 * grad) * more) / kCus;
+}
 int64_t big_round(Operands o, int64_t tiles, int64_t steps) {
-  return (steps + 1) / 2 * 2 * (1070 + 380 * tiles / kCus) + (o == INT8_GRAD ? 12000 : 5500);
+  return (steps + 1) / 2 * 2 * (1100 + 430 * tiles / kCus) + (o == INT8_GRAD ? 16000 : 9500);
 }
 // Few rows: nanoseconds of the blocks one compute unit has, as many at a time as LDS takes.  A block reads
 // its weights at 40 bytes a nanosecond and its rows of x, which others have brought into L2, at 100,
@@ -141,7 +149,7 @@ Plan plan_tiles(int64_t rows, int64_t cols, bool pairs, int64_t kbytes, Operands
   int64_t best = rest ? small_round(o, rest, steps) : 0, cut = 1;
   for (int64_t c = 2; c <= 32 && rest && rest * c <= 2 * kCus && steps >= 4 * c; ++c) {
     // a second launch, and the sums written and read again
-    const int64_t t = div_up(rest * c, kCus) * small_round(o, std::min<int64_t>(rest * c, kCus), div_up(steps, c)) + 3000 +
+    const int64_t t = div_up(rest * c, kCus) * small_round(o, std::min<int64_t>(rest * c, kCus), div_up(steps, c)) + 4000 +
                       30 * rest * c;
     if (t < best) {
       best = t;
@@ -153,9 +161,19 @@ Plan plan_tiles(int64_t rows, int64_t cols, bool pairs, int64_t kbytes, Operands
   p.tiles.full = (int)(p.tiles.cut > 1 ? tiles - rest : tiles);
   p.part = p.tiles.cut > 1 ? (size_t)rest * p.tiles.cut * kI8Tile * kI8Tile * 4 : 0;
   p.ns = best + tiles / kCus * small_round(o, kCus, steps);
+  const int64_t last = tiles % (2 * kCus);
+  const int64_t two = tiles / (2 * kCus) * two_round(o, 2 * kCus, steps) + (last ? two_round(o, last, steps) : 0);
+  if (two < p.ns) {
+    p.tiles.two = 1;
+    p.tiles.full = (int)tiles;
+    p.tiles.cut = 1;
+    p.tiles.per = (int)std::max<int64_t>(1, steps);
+    p.part = 0;
+    p.ns = two;
+  }
   if (o == CODES) return p;                        // the large tiles take no codes
   const int64_t bigs = div_up(cols, pairs ? kI8Big / 2 : kI8Big) * div_up(rows, kI8Big);
-  const int64_t t = bigs / kCus * big_round(o, kCus, steps) + (bigs % kCus ? big_round(o, bigs % kCus, steps) : 0) + 1500;
+  const int64_t t = bigs / kCus * big_round(o, kCus, steps) + (bigs % kCus ? big_round(o, bigs % kCus, steps) : 0);
   if (t < p.ns) {
     p.big = true;
     p.ns = t;
@@ -442,7 +460,7 @@ int say(const Plan& p, bool pairs, int64_t rows, int64_t cols, char* buf, size_t
     return snprintf(buf, len, "few rows: %d groups of %d row blocks, weight blocks %d", p.fewer.groups, p.fewer.rows / 16, p.fewer.nb);
   if (p.few_dx) return snprintf(buf, len, "few rows: groups of %d", p.few_dx);
   if (p.big) return snprintf(buf, len, "tiles 256x256: %lld", (long long)(div_up(rows, kI8Big) * div_up(cols, pairs ? kI8Big / 2 : kI8Big)));
-  return snprintf(buf, len, "tiles 128x128%s: %d whole, %d in %d parts", p.tiles.codes ? " of codes" : "", p.tiles.full,
+  return snprintf(buf, len, "tiles 128x128%s%s: %d whole, %d in %d parts", p.tiles.codes ? " of codes" : "", p.tiles.two ? ", two at once" : "", p.tiles.full,
                   p.tiles.tiles_p * p.tiles.tiles_q - p.tiles.full, p.tiles.cut);
 }
 

@@ -40,6 +40,7 @@ constexpr int kI8Tile = 128;
 struct TilePlan {
   int tiles_p, tiles_q;
   int full, cut, per;
+  int two;                   // two blocks a compute unit, of two stages each
   int codes;                 // gradients: P is int8 codes with scales ps, not their bf16 copy
   void* part;
 };

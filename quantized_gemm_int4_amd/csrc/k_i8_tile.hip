@@ -35,15 +35,14 @@ namespace hm {
 
 namespace {
 
-constexpr int kStages = 4;
 // How P is held: contracted along its rows, int8 codes whose rows are contracted, bf16 whose rows are.
 enum PMode : int { P_ROWS, P_CODES, P_BF16 };
 // P8: P is int8 codes whose rows are contracted (gradients); then a stage also has a slot of 64 scales for each wave
 template <bool P8> constexpr int kP = P8 ? Codes::kBytes : kHalfBytes;
 template <bool P8> constexpr int kStage = kP<P8> + kHalfBytes;             // P and Q of one step
-template <bool P8> constexpr int kScales = kStages * kStage<P8>;           // the slots, or the scales of 128 + 128 results
-template <bool P8> constexpr int kTileLds = kScales<P8> + (P8 ? kStages * 1024 : 1024) + 256;   // (and what is touched)
-constexpr int kAhead = 4;                          // steps between a touch and its copy
+template <bool P8, int ST> constexpr int kScales = ST * kStage<P8>;        // the slots, or the scales of 128 + 128 results
+template <bool P8, int ST> constexpr int kTileLds = kScales<P8, ST> + (P8 ? ST * 1024 : 1024) + 256;   // (and what is touched)
+constexpr int kAhead = 4, kStages = 4;             // steps between a touch and its copy, between a copy and its use
 
 // The lines of step first + kStages + kAhead on, a step at each of the compute waves' barriers.
 template <int PM, bool QS, int EPI>
@@ -83,8 +82,8 @@ __device__ void run_ahead(const TileArgs& a, int tp, int tq, int first, int step
   __asm__ volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <class T, int PM, bool QS, int EPI>
-__global__ void __launch_bounds__(320, 1)
+template <class T, int PM, bool QS, int EPI, int ST>
+__global__ void __launch_bounds__(ST == 4 ? 320 : 256, ST == 4 ? 1 : 2)
 k_i8_tile(TileArgs a, TilePlan pl) {
   constexpr bool P8 = PM == P_CODES, PS = PM == P_BF16;
   // blocks of 32 of a wave: 2 x 2, codes 1 x 4 (no other wave converts the same ones)
@@ -110,14 +109,16 @@ k_i8_tile(TileArgs a, TilePlan pl) {
     last = min(all, first + pl.per);
   }
   const int steps = last - first;
-  float* sc = reinterpret_cast<float*>(lds + kScales<P8>);
+  float* sc = reinterpret_cast<float*>(lds + kScales<P8, ST>);
   if (std::is_same<T, int8_t>::value) {
     if (tid < kI8Tile) sc[tid] = a.ps[p_row<EPI>(a, tp, kI8Tile, tid)];
     else if (tid < 2 * kI8Tile) sc[tid] = a.qs[min((int64_t)tq * kI8Tile + tid - kI8Tile, a.rows - 1)];
   }
-  if (wave == 4) {
-    run_ahead<PM, QS, EPI>(a, tp, tq, first, steps, pl.tiles_p, pl.tiles_q, lane, lds + kTileLds<P8> - 256);
-    return;
+  if constexpr (ST == 4) {
+    if (wave == 4) {
+      run_ahead<PM, QS, EPI>(a, tp, tq, first, steps, pl.tiles_p, pl.tiles_q, lane, lds + kTileLds<P8, ST> - 256);
+      return;
+    }
   }
   Side<QS, false> Q;
   Q.init(a.q, a.q_ld, a.q_bytes, kI8Tile, lane, wave, a.kbytes);
@@ -126,7 +127,7 @@ k_i8_tile(TileArgs a, TilePlan pl) {
   fq.init(lds + kP<P8>, lane, wq);
   std::conditional_t<P8, Codes, Side<PS, kPairs<EPI>>> P;
   Frags<PS> fp;
-  uint8_t* const slot = lds + kScales<P8> + wave * 256;
+  uint8_t* const slot = lds + kScales<P8, ST> + wave * 256;
   if constexpr (P8) {
     P.init(a.p, a.p_ld, a.p_bytes, a.ps, a.terms, tp, first, lane, wave, lds, slot);
   } else {
@@ -158,7 +159,7 @@ k_i8_tile(TileArgs a, TilePlan pl) {
   };
   constexpr int kCopies = P8 ? 7 : 8;
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) {
+  for (int s = 0; s < ST; ++s) {
     begin(s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) copy(i, s);
@@ -183,16 +184,16 @@ k_i8_tile(TileArgs a, TilePlan pl) {
     }
   };
   Ops a0, a1;
-  __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(3 * kCopies) : "memory");
+  __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((ST - 1) * kCopies) : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) read(a0, i, 0);
   // one step on operands o, while those of the next are read and step s + 4 is copied
   int at = 0;                                      // stage of step s
   auto step = [&](int s, const Ops& o, Ops& next) __attribute__((always_inline)) {
-    const int after = (at + 1) & (kStages - 1);
-    begin(s + kStages);
+    const int after = (at + 1) & (ST - 1);
+    begin(s + ST);
     // step s + 1 has landed (two steps' copies are newer), and all waves hold step s in registers
-    __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * kCopies) : "memory");
+    __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((ST - 2) * kCopies) : "memory");
     u32x4_t v[2];                                  // codes: values of parts ks and ks + 1
     auto values = [&](int ks, int h) __attribute__((always_inline)) {
       if constexpr (P8) {
@@ -317,16 +318,23 @@ k_i8_finish(TileArgs a, TilePlan pl) {
   }
 }
 
-template <class T, int PM, bool QS, int EPI>
-hipError_t go(const TileArgs& a, const TilePlan& pl, hipStream_t st) {
-  constexpr int kLds = kTileLds<PM == P_CODES>;
-  auto kern = &k_i8_tile<T, PM, QS, EPI>;
+template <class T, int PM, bool QS, int EPI, int ST>
+hipError_t run(const TileArgs& a, const TilePlan& pl, unsigned blocks, hipStream_t st) {
+  constexpr int kLds = kTileLds<PM == P_CODES, ST>;
+  auto kern = &k_i8_tile<T, PM, QS, EPI, ST>;
   static const hipError_t attr = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL(kern, dim3(blocks), dim3(ST == 4 ? 320 : 256), kLds, st, a, pl);
+  return hipGetLastError();
+}
+
+template <class T, int PM, bool QS, int EPI>
+hipError_t go(const TileArgs& a, const TilePlan& pl, hipStream_t st) {
   const int64_t split = (int64_t)pl.tiles_p * pl.tiles_q - pl.full;
   const int64_t blocks = 8 * (((int64_t)pl.full + 7) / 8 + (split * pl.cut + 7) / 8);
-  hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(320), kLds, st, a, pl);
+  const hipError_t e = pl.two ? run<T, PM, QS, EPI, 2>(a, pl, (unsigned)blocks, st) : run<T, PM, QS, EPI, 4>(a, pl, (unsigned)blocks, st);
+  if (e != hipSuccess) return e;
   if (split) {
     const int per = kPairs<EPI> ? 8 : 16;          // blocks of a tile: 16 rows, 8 rows
     hipLaunchKernelGGL((&k_i8_finish<T, EPI>), dim3((unsigned)(split * per)), dim3(256), 0, st, a, pl);

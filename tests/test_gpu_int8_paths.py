@@ -62,14 +62,14 @@ FEW_GATED = [
     (49, 10251, 128, "1 groups of 4 row blocks, weight blocks 2"), (49, 2171, 384, "1 groups of 4 row blocks, weight blocks 2"),
     (50, 12461, 128, "1 groups of 4 row blocks, weight blocks 4"), (51, 4157, 2048, "1 groups of 4 row blocks, weight blocks 4"),
     (65, 4237, 384, "1 groups of 5 row blocks, weight blocks 2"), (68, 2727, 384, "1 groups of 5 row blocks, weight blocks 2"),
-    (65, 10067, 128, "1 groups of 5 row blocks, weight blocks 4"), (75, 4137, 1664, "1 groups of 5 row blocks, weight blocks 4"),
+    (65, 10766, 128, "1 groups of 5 row blocks, weight blocks 4"), (75, 4137, 1664, "1 groups of 5 row blocks, weight blocks 4"),
     (194, 3075, 128, "2 groups of 7 row blocks, weight blocks 2"), (97, 2275, 512, "1 groups of 7 row blocks, weight blocks 2"),
     (204, 2185, 1408, "2 groups of 7 row blocks, weight blocks 4")]
 FORWARD = FEW + [
-    (1030, 700, 128, "54 whole, 0 in 1"), (1000, 4100, 640, "264 whole, 0 in 1"), (1050, 600, 4096, "0 whole, 45 in 4"),
-    (1021, 4099, 7168, "256 whole, 8 in"), (1100, 300, 8320, "0 whole, 27 in 5"),
-    (2000, 5201, 256, "256x256: 168"), (2100, 9002, 384, "256x256: 324"), (4097, 5000, 128, "256x256: 340"),
-    (2049, 7169, 2176, "128x128: 969 whole"), (2305, 7000, 1152, "256x256: 280")]
+    (1030, 700, 128, "at once: 54 whole, 0 in 1"), (1232, 101, 640, "128x128: 10 whole"), (1050, 600, 4096, "0 whole, 45 in 4"),
+    (1021, 4099, 7168, "256 whole, 8 in"), (1100, 300, 8320, "0 whole, 27 in 5"), (1025, 1300, 128, "at once: 99 whole"),
+    (2000, 5201, 256, "at once: 656"), (2049, 7169, 2176, "at once: 969 whole"), (3528, 4489, 640, "256x256: 252"),
+    (4090, 8101, 1152, "256x256: 512"), (4097, 5000, 128, "at once: 1320")]
 
 
 @pytest.mark.parametrize("m,n,k,plan", FORWARD)
@@ -87,8 +87,9 @@ def test_product(m, n, k, plan):
 
 
 GATED = FEW_GATED + [
-         (1030, 350, 128, "54 whole, 0 in 1"), (1050, 300, 4096, "0 whole, 45 in 4"), (1021, 2049, 7168, "256 whole, 8 in"),
-         (2000, 2601, 256, "256x256: 168"), (1090, 9985, 256, "256x256: 395")]
+         (1030, 350, 128, "at once: 54 whole, 0 in 1"), (1232, 101, 640, "128x128: 20 whole"), (1050, 300, 4096, "0 whole, 45 in 4"),
+         (1021, 2049, 7168, "256 whole, 8 in"), (2000, 2601, 256, "at once: 656"), (3528, 2245, 1664, "256x256: 252"),
+         (4090, 4001, 2304, "256x256: 512")]
 
 
 @pytest.mark.parametrize("m,d,k,plan", GATED)
@@ -114,15 +115,16 @@ def test_gated_and_its_gradient(m, d, k, plan):
     assert bool((h[m] == 7).all()) and bool((out[m] == 7).all())
 
 
-GRAD = [(100, 300, 256, "dx few rows: groups of 32", "dw tiles 128x128 of codes"), (1, 7, 128, "dx few rows: groups of 32", "of codes"),
-        (1100, 4096, 384, "dx few rows: groups of 32", "of codes"), (333, 7168, 2048, "dx few rows: groups of 64", "dw tiles 256x256: 224"),
-        (244, 2065, 3840, "dx few rows: groups of 64", "of codes"), (851, 3968, 1792, "dx few rows: groups of 128", "dw tiles 128x128: 434"),
-        (361, 2405, 4224, "dx few rows: groups of 128", "dw tiles 256x256: 170"), (300, 6000, 640, "of codes: 0 whole, 15 in", "of codes"),
-        (1500, 6000, 2048, "dx tiles 128x128: 192 whole", "dw tiles 256x256: 192"),
-        (3000, 5003, 1024, "dx tiles 128x128: 192 whole", "dw tiles 128x128: 256 whole, 64 in 3"),
-        (4096, 4100, 1152, "dx tiles 128x128: 256 whole, 32 in", "dw tiles 128x128: 256 whole, 41 in"),
-        (2600, 2600, 4096, "dx tiles 256x256: 176", "dw tiles 256x256: 176"), (5100, 4100, 4096, "dx tiles 256x256: 320", "dw tiles"),
-        (64, 14336, 1024, "of codes", "dw")]
+GRAD = [(100, 300, 256, "few rows: groups of 32", "of codes"), (1, 7, 128, "few rows: groups of 32", "of codes, two at once: 1 whole"),
+        (1100, 4096, 384, "few rows: groups of 32", "of codes"), (333, 7168, 2048, "few rows: groups of 64", "of codes, two at once: 896"),
+        (244, 2065, 3840, "few rows: groups of 64", "of codes"), (851, 3968, 1792, "few rows: groups of 128", "of codes, two at once"),
+        (646, 6806, 2048, "few rows: groups of 128", "256x256: 216"), (131, 2584, 1408, "few rows: groups of 32", "of codes: 231 whole"),
+        (64, 14336, 1024, "of codes: 0 whole, 8 in", "dw"), (1315, 1, 128, "few rows", "of codes: 0 whole, 1 in 4"),
+        (2121, 1, 128, "of codes, two at once: 17 whole", "of codes: 0 whole, 1 in"), (1368, 129, 2688, "of codes: 231 whole", "of codes: 42 whole"),
+        (1500, 6000, 2048, "128x128: 192 whole", "dw"), (3000, 5003, 1024, "128x128: 192 whole", "128x128, two at once: 320 whole"),
+        (4096, 4100, 1152, "128x128: 256 whole, 32 in", "128x128: 256 whole, 41 in"), (2828, 3620, 384, "of codes: 0 whole, 69 in", "128x128: 87 whole"),
+        (5100, 4100, 4096, "128x128, two at once: 1280", "128x128: 1024 whole, 32 in"), (2600, 2600, 4096, "256x256: 176", "256x256: 176"),
+        (5100, 4100, 6016, "256x256: 480", "256x256: 408")]
 
 
 @pytest.mark.parametrize("m,n,k,dxp,dwp", GRAD)

@@ -106,7 +106,7 @@ def test_plan():
     buf = ctypes.create_string_buffer(200)
     plan = hm.lib.hm_gemm_int8_plan
     for op in range(4):
-        assert plan(op, 100, 256, 512, buf, 200) == 0 and b"tiles" in buf.value
+        assert plan(op, 2000, 256, 512, buf, 200) == 0 and b"tiles" in buf.value
         assert plan(op, 0, 256, 512, buf, 200) == 0
         assert plan(op, 100, 256, 500, buf, 200) == SHAPE and plan(op, -1, 256, 512, buf, 200) == SHAPE
         assert plan(op, 100, 256, 512, None, 200) == NULL and plan(op, 100, 256, 512, buf, 0) == NULL
