@@ -1,7 +1,6 @@
 // Products of 8-bit integer layers and of their gradients, 128 x 128 output
 // tiles: O[q][p] = sum_c Q[q][c] P[p][c] on 32x32 MFMAs, int8 codes with exact
-// integer sums (32x32x32) or bf16 with fp32 sums (32x32x16).  For calls with too
-// few 256 x 256 tiles to fill the card: bound by the latency of their copies.
+// integer sums (32x32x32) or bf16 with fp32 sums (32x32x16).
 //
 // A block of four waves, one a SIMD, each with 64 x 64 of the tile.  The MFMA's
 // rows are the output's columns p, so that a lane holds four neighbouring
@@ -11,13 +10,16 @@
 // their int8 operand (weights for dx, rows of x for dw) as it is and turn it into bf16
 // between the MFMAs (a step of 0.66 us for 0.51 on a full card, but no bf16 copy of the operand to make
 // first: m = 128, n = 14336, k = 4096 dx 33 us for 63; m = 1024 161 for 145).  During step s its operands are
-// in registers, those of step s + 1 are read from LDS between the MFMAs, and four
-// stages hold steps s + 1 .. s + 4, so that a copy has three steps to land.  A fifth wave
-// touches later steps' lines (Ahead; product of m = 1021, n = 4099, k = 7168 58 us without it, 44 with).
+// in registers, those of step s + 1 are read from LDS between the MFMAs, and ST
+// stages hold steps s + 1 .. s + ST, so that a copy has ST - 1 steps to land.
 //
-// Against the 256 x 256 tiles: int8 product m = 1024, n = 7168, k = 2048 22.6 us for 28.4, m = 2048 44 for 33.
-// What bounds a step is the copies' 32 KiB from L2: at the 64 bytes a clock that a compute unit takes, 0.22 us, and
-// twice that with all of them at it.
+// Where one round of tiles has the card, a block has a compute unit for itself and four
+// stages, and a fifth wave touches later steps' lines (Ahead; product of m = 1021, n = 4099, k = 7168 58 us
+// without it, 44 with): a step's 32 KiB take 0.22 us from L2 at the 64 bytes a clock that a compute unit gets, twice that with
+// all of them at it.  Where more tiles follow, two blocks with two stages each share one, so that
+// the start and the end of one (4 us) go with the other's steps: product m = 4313, n = 5402, k = 256 20.1 us
+// for 30.7 with four stages, m = 755, n = 9616, k = 6272 51.6 for 59.3, dw m = 359, n = 1600, k = 5504 17.1 for 22.2; but 220 tiles of
+// k = 5632 32.8 for 28.5.  Against the 256 x 256 tiles: m = 4313 as above 28.6 us, m = 1364, n = 20992, k = 3968 125.4 here for 113.8.
 //
 // Tiles that do not fill the card's 256 compute units in a last round (or all of
 // them, where there are fewer) are split along the contraction: `cut` blocks a

@@ -133,7 +133,7 @@ def test_product_more_tiles(m, n, k):
     _close(hm.hm_gemm_int8(*_dev(a)), ref, np.abs(ref) * (U + 4 * E) + TINY, "y")
 
 
-@pytest.mark.parametrize("m", [1, 40, 200])
+@pytest.mark.parametrize("m", [1, 40, 200, 1030])
 def test_product_largest_sum(m):
     """k at its limit with every code at -128: the sum is 2^14 (2^17 - 2^7), just inside an int32."""
     import quantized_gemm_int4_amd as hm
@@ -146,7 +146,7 @@ def test_product_largest_sum(m):
     _close(y, np.full((m, n), ref), np.full((m, n), ref * (U + 4 * E)), "y")
 
 
-@pytest.mark.parametrize("m", [3, 50, 150])
+@pytest.mark.parametrize("m", [3, 50, 150, 1030])
 def test_scales_that_are_not_finite_stay_in_their_row_and_column(m):
     import quantized_gemm_int4_amd as hm
     n, k = 200, 256
@@ -199,7 +199,7 @@ def test_gated_gradient(m, d, k):
     assert (out[m] == 7).all()
 
 
-@pytest.mark.parametrize("m", [1, 20, 140])
+@pytest.mark.parametrize("m", [1, 20, 140, 1030])
 def test_gates_far_out(m):
     """Gates to +-1e4 and beyond the exponential's range; a gate of exactly 0."""
     import quantized_gemm_int4_amd as hm
@@ -237,7 +237,8 @@ def _check_grad(got, dyb, a, what):
             # averages out (equal codes are rounded alike, in every result) and only the worst case holds: the
             # term's rounding and the result's, (1 + u)^2 - 1 <= 2 u (1 + u).
             err, size = np.linalg.norm(_val(bits_of(y)) - ref), np.linalg.norm(ref)
-            assert err <= (U if terms >= 16 else 2 * U * (1 + U)) * size or terms in range(2, 16), (what, name, err / size)
+            if terms == 1 or terms >= 16:
+                assert err <= (U if terms >= 16 else 2 * U * (1 + U)) * size, (what, name, err / size)
 
 
 @pytest.mark.parametrize("m", ROWS)
@@ -350,11 +351,12 @@ def test_block_step(m, d, k):
         assert rel < 8 * 0.01, (name, rel)
 
 
-def test_block_step_captured_and_replayed():
+@pytest.mark.parametrize("m", [70, 1100])
+def test_block_step_captured_and_replayed(m):
     """The step in a graph, replayed with new inputs, eager work and
     synchronizations between: the bits of the eager step each time."""
     import quantized_gemm_int4_amd as hm
-    m, d, k = 70, 256, 384
+    d, k = 256, 384
     buf = _block_inputs(m, d, k, 0)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -376,10 +378,11 @@ def test_block_step_captured_and_replayed():
             assert torch.equal(got, ref)
 
 
-def test_two_streams_and_repeated_calls():
+@pytest.mark.parametrize("m", [90, 1100])
+def test_two_streams_and_repeated_calls(m):
     """Calls on two streams at once, and the same call again, give equal bits."""
     import quantized_gemm_int4_amd as hm
-    ins = [_block_inputs(90, 256, 256, s) for s in (1, 2)]
+    ins = [_block_inputs(m, 256, 256, s) for s in (1, 2)]
     want = [[t.clone() for t in _block(hm, *i)] for i in ins]
     streams = [torch.cuda.Stream() for _ in ins]
     torch.cuda.synchronize()

@@ -150,6 +150,20 @@ def test_gradient(m, n, k, dxp, dwp):
     assert torch.equal(one, dx[:m]) and torch.equal(two, dw[:n])
 
 
+@pytest.mark.parametrize("m,n,k", [g[:3] for g in GRAD if g[0] > 2])
+def test_an_infinity_at_the_start_of_a_row_stays_in_it(m, n, k):
+    """Behind the end of the row before it: the tile of that row must not see it."""
+    import quantized_gemm_int4_amd as hm
+    a, rows = _layer(m + n + k, m, n, k)
+    dy = rows(m, n)
+    dy[1, 0] = float("inf")
+    dx, dw = hm.hm_gemm_int8_grad(dy, *a)
+    dx, dw = dx.isfinite().all(1), dw.isfinite().all(1)
+    assert int((~dx).sum()) == 1 and not bool(dx[1]), (~dx).nonzero()[:5]
+    assert int((~dw).sum()) == 1 and not bool(dw[0]), (~dw).nonzero()[:5]
+
+
+
 def test_gradient_against_differences():
     """A loss of the product along random directions of x_hat and w_hat: its
     central difference is the gradient's inner product with the direction (the
