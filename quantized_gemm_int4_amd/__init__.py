@@ -163,9 +163,7 @@ def _stream(stream=None):
     return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
-def _raw_stream(dev):
-    # of the device of index dev, which is the current one
-    return torch._C._cuda_getCurrentRawStream(dev)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)    # of a device index (torch without a GPU backend: none)
 
 
 def _ok(fn, code):
@@ -439,7 +437,7 @@ def _elsewhere(t, stream):
     if not t.is_cuda:
         raise ValueError("need CUDA tensors")
     if stream is None:
-        return None if t.get_device() == torch.cuda.current_device() else _other(t.device, None)
+        return None if t.get_device() == torch._C._cuda_getDevice() else _other(t.device, None)
     if stream.device != t.device:
         raise ValueError("stream: of another device than the tensors")
     return _other(t.device, stream)

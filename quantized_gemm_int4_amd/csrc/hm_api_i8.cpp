@@ -116,8 +116,8 @@ int64_t big_round(Operands o, int64_t tiles, int64_t steps) {
 }
 // Few rows: nanoseconds of the blocks one compute unit has, as many at a time as LDS takes.  A block reads
 // its weights at 40 bytes a nanosecond and its rows of x, which others have brought into L2, at 100,
-// and all of them no faster than the memory gives the weights (k = 6656, m = 11, n = 8256: three blocks of 16
-// weight rows a block 13.6 us, one 13.8, two, which leave two units with twice the work, 15.6, four 15.2).
+// and all of them no faster than the memory gives the weights (k = 4096, m = 64, n = 14336: four blocks of 16
+// weight rows a block 17.8 us, two 20.2, one 26.6; k = 5248, m = 48, n = 3985: one 9.5, two 11.1).
 int64_t memory_time(int64_t cols, bool pairs, int64_t k) { return cols * (pairs ? 2 : 1) * k / 4900; }
 int64_t few_time(int64_t rows, int64_t cols, bool pairs, int64_t k, FewPlan& p) {
   const int64_t blocks = div_up(rows, 16), least = div_up(blocks, 8), memory = memory_time(cols, pairs, k);
