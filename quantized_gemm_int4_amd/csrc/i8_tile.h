@@ -291,17 +291,29 @@ struct Codes {
   }
 };
 
-// Gate, up and the gradient of h to those of both, with sig = 1 / (1 + e^-g).  It is taken as 2^-64 /
-// (2^-64 + 2^(-64 - g log2 e)), whose terms stay in the normal range for g > -131 (with e^-g
-// itself dg of a gate of -88 was 0 for -1e-37); the last product, by 2^-64, keeps subnormal results.  sig
-// has no cancellation, and 1 - sig is off by less than a rounding of 1, which g (1 - sig) is added to.  The errors
-// of the exponential (the rounding of an argument up to 128, 2^-17) and of the reciprocal stay far below the
-// bf16 rounding of the results.
+// sig(g) = 1 / (1 + e^-g) as s post.  From g = -87 on post = 1, and s and everything on the way to it is in
+// fp32's normal range; below, where 1 + e^g is 1, s = e^g 2^125 and post = 2^-125, which the caller multiplies by last:
+// a product with a large up value or gradient can be an ordinary number where sig(g) itself has lost bits (g < -87) or
+// is 0 (g < -104).  s stays normal down to g = -173, where a result needs |dh u| > 2^117 to be normal itself.  s <= 1, so
+// no product overflows that would not without post.  The error of the exponential is the rounding of an
+// argument up to 125 and of log2 e (4e-6 in all), far below the bf16 rounding of the results.
+struct Sigmoid {
+  float s, post;
+};
+__device__ __forceinline__ Sigmoid sigmoid(float g) {
+  const bool near = g >= -87.0f;
+  const float e = __builtin_amdgcn_exp2f(near ? g * -1.4426950408889634f : __builtin_fmaf(g, 1.4426950408889634f, 125.0f));
+  return {near ? __builtin_amdgcn_rcpf(1.0f + e) : e, near ? 1.0f : 0x1p-125f};
+}
+
+// Gate, up and the gradient of h to those of both, with sig = 1 / (1 + e^-g):
+//   du = dh g sig,  dg = dh u (sig + g sig (1 - sig)).
+// sig has no cancellation, and 1 - sig is off by less than a rounding of 1, which g (1 - sig) is added to.
 __device__ __forceinline__ void gated_grad(float g, float u, float dh, float& dg, float& du) {
-  const float sig = __builtin_amdgcn_rcpf(0x1p-64f + __builtin_amdgcn_exp2f(__builtin_fmaf(g, -1.4426950408889634f, -64.0f))) * 0x1p-64f;
-  const float t = g * sig;
-  du = dh * t;
-  dg = dh * u * __builtin_fmaf(t, 1.0f - sig, sig);
+  const Sigmoid sig = sigmoid(g);
+  const float t = g * sig.s;
+  du = dh * t * sig.post;
+  dg = dh * u * __builtin_fmaf(t, __builtin_fmaf(-sig.s, sig.post, 1.0f), sig.s) * sig.post;
 }
 
 // Eight bf16 values of a row at any 2-byte address (rows of an odd number of
