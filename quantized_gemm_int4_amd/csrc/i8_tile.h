@@ -306,6 +306,12 @@ __device__ __forceinline__ Sigmoid sigmoid(float g) {
   return {near ? __builtin_amdgcn_rcpf(1.0f + e) : e, near ? 1.0f : 0x1p-125f};
 }
 
+// silu(g) u.
+__device__ __forceinline__ float gated(float g, float u) {
+  const Sigmoid sig = sigmoid(g);
+  return g * sig.s * u * sig.post;
+}
+
 // Gate, up and the gradient of h to those of both, with sig = 1 / (1 + e^-g):
 //   du = dh g sig,  dg = dh u (sig + g sig (1 - sig)).
 // sig has no cancellation, and 1 - sig is off by less than a rounding of 1, which g (1 - sig) is added to.
@@ -408,7 +414,7 @@ __device__ __forceinline__ void emit(const TileArgs& a, const typename Mma<T>::A
             for (int e = 0; e < 4; ++e) {
               const float g = (float)acc[0][qb][4 * j + e] * sq * sg[e], u = (float)acc[1][qb][4 * j + e] * sq * su[e];
               if constexpr (EPI == EPI_GATED) {
-                f[0][e] = silu_f(g) * u;
+                f[0][e] = gated(g, u);
               } else {
                 gated_grad(g, u, (e & 1) ? hi_bf16(d[y][e >> 1]) : lo_bf16(d[y][e >> 1]), f[0][e], f[1][e]);
               }

@@ -142,7 +142,7 @@ k_i8_few(TileArgs a, uint32_t total, int groups, int per) {
       f[0][e] = (float)s[0][e] * sq * a.ps[c];
       if constexpr (kPairs<EPI>) {
         const float g = f[0][e], u = (float)s[1][e] * sq * a.ps[a.cols + c];
-        if constexpr (EPI == EPI_GATED) f[0][e] = silu_f(g) * u;
+        if constexpr (EPI == EPI_GATED) f[0][e] = gated(g, u);
         else gated_grad(g, u, bf16_to_f32(a.dh[m * a.cols + c]), f[0][e], f[1][e]);
       }
     }

@@ -304,7 +304,7 @@ k_i8_finish(TileArgs a, TilePlan pl) {
       f[0][e] = (float)s[0][e] * sq * a.ps[n];
     } else {
       const float g = (float)s[0][e] * sq * a.ps[n], u = (float)s[1][e] * sq * a.ps[a.cols + n];
-      if constexpr (EPI == EPI_GATED) f[0][e] = silu_f(g) * u;
+      if constexpr (EPI == EPI_GATED) f[0][e] = gated(g, u);
       else gated_grad(g, u, bf16_to_f32(a.dh[row * a.cols + n]), f[0][e], f[1][e]);
     }
   }

@@ -51,3 +51,12 @@ def test_gradient(m, d, k, plan):
     du, dg = f * gate * s, f * up * s * (1 + gate * rest)
     _close(dgu[:, d:], du, du.abs() * (U + c) + TINY, "du")
     _close(dgu[:, :d], dg, dg.abs() * U + (f * up).abs() * s * (1 + gate.abs() * rest) * 2 * c + TINY, "dg")
+
+
+@pytest.mark.parametrize("m,d,k,plan", SIZES)
+def test_forward(m, d, k, plan):
+    import quantized_gemm_int4_amd as hm
+    assert plan in hm.hm_gemm_int8_plan(hm.HM_INT8_GATED, m, 2 * d, k)
+    a, gate, up, c, _ = _far(m, d, k)
+    ref = gate * torch.sigmoid(gate) * up
+    _close(hm.hm_gemm_int8_gated(*a), ref, ref.abs() * (U + c) + TINY, "h")
