@@ -546,8 +546,10 @@ hm_status hm_lora_grad(const hm_lora_desc* d, const uint16_t* dy, const uint16_t
  * ceil(m/128) ceil(n/128) <= 2^23, and the same of (m, k) and (n, k) for the
  * gradient.  HM_ERR_SHAPE otherwise.  Codes may be any int8, scales any finite
  * fp32; a NaN or infinite scale makes its row (token) or column (channel) of
- * the results NaN or infinite and leaves the others alone, but where it is
- * summed over (hm_gemm_int8_grad) unspecified.  ws: at least the bytes that the
+ * the results NaN or infinite and leaves the others alone (of the gated
+ * calls: a gate row's scale column i of h and columns i and d + i of dgu, an up
+ * row's column i of h and of dgu, since du does not depend on u); where it is
+ * summed over (hm_gemm_int8_grad) the sums are unspecified.  ws: at least the bytes that the
  * _workspace_size call names (NULL if 0), overwritten; calls that may run at the
  * same time need one each.  bf16 and int8 arrays are
  * 16-byte aligned, scales 4-byte, ws 256-byte (HM_ERR_ALIGN).  No output nor ws
