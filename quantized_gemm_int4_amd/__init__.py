@@ -756,7 +756,8 @@ def hm_gemm_int8_grad(dy, x8, x_scales, w8, w_scales, dx=None, dw=None, need_dx=
     dw = _new(bf, (n, k), dev) if need_dw and dw is None else dw
     wsp, wsb, ws = _ws(ws, hm_gemm_int8_grad_workspace_size, (m, n, k), dev)
     code = lib.hm_gemm_int8_grad(_arg(dy, bf, (m, n), "dy", dev), *_int8_args(x8, x_scales, w8, w_scales, m, n, k, dev), m, n, k,
-                                 None if dx is None else _arg(dx, bf, (m, k), "dx", dev),
+                                 # (a dx of no rows has no address, but NULL would say that it is not wanted: any aligned one)
+                                 None if dx is None else _arg(dx, bf, (m, k), "dx", dev) or 16,
                                  None if dw is None else _arg(dw, bf, (n, k), "dw", dev), wsp, wsb, _raw_stream(dev))
     _ok("hm_gemm_int8_grad", code)
     return dx, dw
