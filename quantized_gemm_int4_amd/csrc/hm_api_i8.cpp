@@ -94,9 +94,11 @@ struct Plan {
 };
 
 // Nanoseconds of up to 256 tiles at once, one a compute unit, by the contraction's steps
-// of 128 bytes, taken in twos.  Fitted to some 300 measured sizes from m = 16, n = 256, k = 256 to m = 8192, n = 14336,
-// k = 4096; of 230 others the choice took at most 8 % longer than the best alternative in nine of ten, and up to 40 % for
-// the worst.  Copies from L2 bound the small tiles, the conversion those that turn codes into bf16, copies
+// of 128 bytes, taken in twos: estimates fitted to measured calls, which choose between kernels that all give the
+// same results (gradients: up to the order of their sums).  Of 400 choices at 80 drawn sizes (m 1 to 8192, n 64 to
+// 14336, k 256 to 7168; product, gated block, its gradient, dx, dw) half took within 1.5 % of the fastest of all kernels
+// forced in turn, nine of ten within 10 %, the worst 1.3 times it, but for one of a call of 4 us (1.6).
+// Copies from L2 bound the small tiles, the conversion those that turn codes into bf16, copies
 // and the matrix cores the large ones.
 constexpr int kCus = 256;
 enum Operands { INT8, INT8_GRAD, CODES, COPY };    // int8 products, the gated gradient; gradients with P as codes, as a bf16 copy

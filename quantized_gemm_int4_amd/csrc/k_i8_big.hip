@@ -1,13 +1,13 @@
 // The products of k_i8_tile.hip on 256 x 256 output tiles, for calls with
-// tiles enough to fill the card: bound by the matrix cores, and by the power they
-// may draw (int8 product m = 8192, n = 14336, k = 4096: 393 us with Gaussian codes, 2.45 Pop/s
-// 308 with zeros; gated block m = 4096 401, its gradient 444, with an epilogue of four bf16 results a pair;
-// bf16 gradients m = 4096, same n and k: 362 us dx, 400 dw, 1.33 and 1.20 PFLOP/s).
+// tiles enough to fill the card: the matrix cores are busy in 61 % of its cycles, and power sets the clock (int8
+// product m = 8192, n = 14336, k = 4096, calls in a row: 400 us with Gaussian codes, 2.4 Pop/s at about 1.9 GHz, 296 with
+// zeros; gated block m = 4096 409, its gradient 451, with an epilogue of four bf16 results a pair; bf16 gradients m = 4096, same n and
+// k, one call at a time: 366 us dx, 396 dw, 1.31 and 1.22 PFLOP/s).
 //
 // Four waves, one per SIMD, each with 128 x 128 of the tile (256 accumulators a
-// lane): every 16-byte operand read from LDS feeds two (halves: four) MFMAs, so that
-// LDS carries 1536 cycles of traffic for 2048 cycles of MFMA a step of 128
-// bytes.  (64 x 64 a wave, as in the 128 x 128 kernel: 768 for 512.)
+// lane): every 16-byte operand read from LDS feeds two (halves: four) MFMAs.  A read of 1 KiB takes
+// LDS four cycles (its counter), so a step of 128 bytes has 512 cycles of reads for 2048 of MFMA, and 64 KiB of
+// copies into LDS.  (64 x 64 a wave, as in the 128 x 128 kernel: 256 for 512, and 32 KiB.)
 //
 // A step is cut into four phases, one for each pair of P and Q halves, 16 MFMAs of 32
 // cycles each.  Every phase reads the operands of the next one between its

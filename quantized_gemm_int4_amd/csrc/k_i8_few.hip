@@ -1,8 +1,8 @@
-// Products of 8-bit integer layers for few rows (decoding: up to 128): bound by
-// reading the weights once.
+// Products of 8-bit integer layers for few rows (up to 1024): bound by reading the
+// weights, once where the rows are one group (up to 128), from L2 for the other groups.
 //
-// A block has 16 NB weight rows (pairs: 16 gate rows and the 16 up rows that
-// belong to them) against all rows of x, and its four waves split the contraction:
+// A block has 16 NB weight rows, NB = 1 .. 4 (pairs: NB = 2 or 4, half of them gate rows and half the up rows that
+// belong to them) against a group of up to 128 rows of x, and its four waves split the contraction:
 // wave w takes the steps w, w + 4, ... of 128 bytes of every row, each by itself, so that
 // the block reads its rows from end to end.  Direct buffer-to-LDS copies bring them
 // in, eight lanes a line, and the operands of the 16x16x64 MFMA (lane L: row L % 16, 16

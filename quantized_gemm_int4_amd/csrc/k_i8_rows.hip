@@ -13,8 +13,9 @@ namespace {
 
 // The code of x in a row with largest magnitude amax is the whole number
 // nearest to v = 127 x / amax, ties to even.  v is a ratio of whole numbers:
-// with 8-bit significands X and A, v = 127 X / (A 2^c), and for a tie j + 1/2 that v
-// does not meet, |v - (j + 1/2)| >= 1 / (A 2^c) = v / (127 X) > v 2^-15.  The fp32
+// with 8-bit significands X and A, v = 127 X / (A 2^c), c >= 0, and v - (j + 1/2) =
+// (254 X - (2j + 1) A 2^c) / (2 A 2^c).  For a tie that v does not meet the numerator is a whole number
+// other than 0, so the distance is at least 1 / (2 A 2^c) = v / (254 X) > v 2^-16.  The fp32
 // product x (127 / amax) has two roundings, at most 2^-23 of v.  So rounding it to 19
 // significant bits (the integer add and mask; it moves a value by at most 2^-19
 // of itself) brings every tie to its exact value and moves nothing else across
@@ -164,7 +165,7 @@ hipError_t launch_i8_quant_rows(const uint16_t* x, int64_t m, int64_t k, int8_t*
 namespace {
 
 // The copies that a gradient needs, in one launch.  Codes: bf16(scale * code), one
-// rounding of the fp32 product, 16 a thread.  Rows of n values into rows of 8 nc, zeros behind: eight a thread.
+// rounding of the fp32 product (a factor of the bf16 MFMA, see Codes), 16 a thread.  Rows of n values into rows of 8 nc, zeros behind: eight a thread.
 __global__ void __launch_bounds__(256)
 k_i8_copies(I8Copies c) {
   const int64_t n0 = c.rows[0] * c.kc, n1 = n0 + c.rows[1] * c.kc, total = n1 + c.m * c.nc;
