@@ -296,18 +296,19 @@ struct Codes {
 };
 
 // sig(g) = 1 / (1 + e^-g) as s post.  From g = -87 on post = 1, and s and everything on the way to it is in
-// fp32's normal range; below, where 1 + e^g is 1, s = e^g 2^125 and post = 2^-125, which the caller multiplies by last:
+// fp32's normal range; below, where 1 + e^g is 1, s = e^g 2^119 and post = 2^-119, which the caller multiplies by last:
 // a product with a large up value or gradient can be an ordinary number where sig(g) itself has lost bits (g < -87) or
-// is 0 (g < -104).  s stays normal down to g = -173, where a result needs |dh u| > 2^117 to be normal itself.  s <= 1, so
-// no product overflows that would not without post.  The error of the exponential is the rounding of an
-// argument up to 125 and of log2 e (4e-6 in all), far below the bf16 rounding of the results.
+// is 0 (g < -104).  |g| s stays under 1 there (87 x 2^(119 - 125.5) at the border), so no product overflows on the way.  The exponential is
+// taken 64 times larger, since it flushes results under 2^-126 and a product does not: s has 18 bits or more
+// down to g = -174, where a result needs |dh u| > 2^117 to be normal itself.  The exponential's error is the
+// rounding of an argument up to 126 and of log2 e (4e-6 in all), far below the bf16 rounding of the results.
 struct Sigmoid {
   float s, post;
 };
 __device__ __forceinline__ Sigmoid sigmoid(float g) {
   const bool near = g >= -87.0f;
   const float e = __builtin_amdgcn_exp2f(near ? g * -1.4426950408889634f : __builtin_fmaf(g, 1.4426950408889634f, 125.0f));
-  return {near ? __builtin_amdgcn_rcpf(1.0f + e) : e, near ? 1.0f : 0x1p-125f};
+  return {near ? __builtin_amdgcn_rcpf(1.0f + e) : e * 0x1p-6f, near ? 1.0f : 0x1p-119f};
 }
 
 // silu(g) u.

@@ -60,3 +60,28 @@ def test_forward(m, d, k, plan):
     a, gate, up, c, _ = _far(m, d, k)
     ref = gate * torch.sigmoid(gate) * up
     _close(hm.hm_gemm_int8_gated(*a), ref, ref.abs() * (U + c) + TINY, "h")
+
+
+@pytest.mark.parametrize("m,d,k,plan", SIZES)
+def test_largest_values(m, d, k, plan):
+    """Up values, gradients and their products next to fp32's largest number, against gates from -80 on: no
+    intermediate result may pass it."""
+    import quantized_gemm_int4_amd as hm
+    assert plan in hm.hm_gemm_int8_plan(hm.HM_INT8_GATED, m, 2 * d, k)
+    x8, w8 = torch.zeros(m, k, dtype=torch.int8, device="cuda"), torch.zeros(2 * d, k, dtype=torch.int8, device="cuda")
+    x8[:, 0] = 1
+    w8[:d, 0] = -(80 + torch.arange(d, device="cuda") % 48).to(torch.int8)
+    w8[d:, 0] = 127
+    sx = torch.ones(m, device="cuda")
+    gate = w8[:d, 0].to(F)[None].expand(m, d)
+    s, c = torch.sigmoid(gate), (60 + 4 * gate.abs()) * 2 * E
+    for up, grad in ((2.0 ** 120, 1.0), (127.0 ** -1, 2.0 ** 127), (2.0 ** 60, 2.0 ** 60)):  # up values of 127 times that
+        a = (x8, sx, w8, torch.cat([torch.ones(d, device="cuda"), torch.full((d,), up, device="cuda")]))
+        dh = torch.full((m, d), grad, dtype=torch.bfloat16, device="cuda")
+        u = 127.0 * float(torch.tensor(up, dtype=torch.float32))
+        ref = gate * s * u
+        _close(hm.hm_gemm_int8_gated(*a), ref, ref.abs() * (U + c) + TINY, ("h", up))
+        dgu = hm.hm_gemm_int8_gated_grad(dh, *a)
+        du, dg = grad * gate * s, grad * u * s * (1 + gate * torch.sigmoid(-gate))
+        _close(dgu[:, d:], du, du.abs() * (U + c) + TINY, ("du", grad))
+        _close(dgu[:, :d], dg, dg.abs() * U + (grad * u * s * (1 + gate.abs())) * 2 * c + TINY, ("dg", up, grad))
