@@ -239,7 +239,7 @@ template <bool ROWS, int NB = 2> struct Frags {
 // those, turned into bf16(scale * code) on the way to the MFMA.  The scale differs from term to term, so it has to be
 // part of a factor, and a bf16 MFMA takes factors of 8 bits: one of the two is rounded, by half a step (2^-8) at
 // most.  Against fp64 the gradients are then off by 0.0023 in norm, 0.0017 of it the rounding of the results
-// themselves; a second bf16 term that holds what is left would double the MFMAs (of 751 us a call at m = 4096, n = 14336, k = 4096).
+// themselves; a second bf16 term that holds what is left would double the MFMAs (of 763 us a call at m = 4096, n = 14336, k = 4096).
 // Copies (two of codes
 // and one of the step's 64 scales, which every wave has for itself), reads, and the conversion.
 struct Codes {

@@ -1,8 +1,8 @@
 // The products of k_i8_tile.hip on 256 x 256 output tiles, for calls with
 // tiles enough to fill the card: the matrix cores are busy in 61 % of its cycles, and power sets the clock (int8
-// product m = 8192, n = 14336, k = 4096, calls in a row: 400 us with Gaussian codes, 2.4 Pop/s at about 1.9 GHz, 296 with
-// zeros; gated block m = 4096 409, its gradient 451, with an epilogue of four bf16 results a pair; bf16 gradients m = 4096, same n and
-// k, one call at a time: 366 us dx, 396 dw, 1.31 and 1.22 PFLOP/s).
+// product m = 8192, n = 14336, k = 4096, calls in a row, two cards: 399 and 407 us with Gaussian codes, 2.4 Pop/s at about 1.9 GHz, 296 with
+// zeros; gated block m = 4096 409 and 419, its gradient 459, with an epilogue of four bf16 results a pair; bf16 gradients m = 4096, same n and
+// k, one call at a time: 366 and 377 us dx, 396 and 410 dw, 1.27 to 1.31 and 1.17 to 1.22 PFLOP/s).
 //
 // Four waves, one per SIMD, each with 128 x 128 of the tile (256 accumulators a
 // lane): every 16-byte operand read from LDS feeds two (halves: four) MFMAs.  A read of 1 KiB takes
